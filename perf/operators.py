@@ -354,7 +354,10 @@ def work(case):
             # exp, add, compare per expert; a quotient per chosen one
             return {"bytes": T * E * z + T * k * 8 + E * 4 * (1 + bool(case["bias"])),
                     "flops": T * (4 * E + 3 * k)}
-        return {"bytes": 2 * T * E * z + T * k * 8, "flops": T * (6 * E + 6 * k)}
+        if case["score"] == "softmax" and not case["renorm"]:
+            return {"bytes": 2 * T * E * z + T * k * 8, "flops": T * (6 * E + 6 * k)}
+        # the gradient is zero but for the chosen experts, and needs only their logits
+        return {"bytes": T * E * z + T * k * (8 + z), "flops": T * 12 * k}
     B, V, L, z = case["B"], case["V"], case["L"], _SIZE[case["dtype"]]
     # lengths are between half of L and L
     read = B * V * z + B * L * 3 + case["masks"] * ((V + 63) // 64) * 8 + B * case["bias"] * 8
