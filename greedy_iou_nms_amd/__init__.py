@@ -21,6 +21,8 @@ __all__ = [
     "NMSError", "STAGES", "nms", "nms_profiled", "nms_static", "workspace_size", "Workspace",
     "debug_order", "debug_mask", "debug_decide", "debug_plan", "library_path",
     "MATRIX_STAGES", "matrix_nms", "matrix_nms_profiled", "matrix_workspace_size",
+    "route_experts", "route_experts_backward", "LogitRules", "adjust_logits", "pick_tokens",
+    "pick_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -87,6 +89,20 @@ def _load():
     lib.nms_matrix_f32.restype = ctypes.c_int
     lib.nms_matrix_f32_profiled.argtypes = matrix + [ctypes.POINTER(ctypes.c_float)]
     lib.nms_matrix_f32_profiled.restype = ctypes.c_int
+    c_int = ctypes.c_int
+    lib.nms_route_experts.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_vp]
+    lib.nms_route_experts.restype = c_int
+    lib.nms_route_experts_backward.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp,
+                                               c_vp, c_i64, c_vp]
+    lib.nms_route_experts_backward.restype = c_int
+    lib.nms_adjust_logits.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp]
+    lib.nms_adjust_logits.restype = c_int
+    lib.nms_pick_workspace_size.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]
+    lib.nms_pick_workspace_size.restype = c_int
+    lib.nms_pick_tokens.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp,
+                                    c_vp, c_vp, c_int, c_vp, c_vp, c_vp, c_sz, c_vp]
+    lib.nms_pick_tokens.restype = c_int
     return lib
 
 
@@ -464,3 +480,9 @@ def matrix_nms(boxes: torch.Tensor, scores: torch.Tensor, score_threshold: float
 def matrix_nms_profiled(boxes, scores, score_threshold, sigma=0.5, workspace=None, out=None):
     """``matrix_nms`` plus per-stage GPU times in milliseconds."""
     return _run_matrix(boxes, scores, score_threshold, sigma, workspace, out, True)
+
+
+# ---------------------------------------- selection operators of language models
+
+from .selection import (LogitRules, adjust_logits, pick_tokens, pick_workspace_size,  # noqa: E402
+                        route_experts, route_experts_backward)

@@ -1,0 +1,309 @@
+"""Selection operators of language models: routing to experts, rules on
+logits and picking the next token (the ``nms_route_*``, ``nms_adjust_logits``
+and ``nms_pick_tokens`` entry points of ``include/greedy_nms.h``, which states
+what each computes).
+
+Like the rest of the binding: tensor checks, output allocation, pointers and
+the current HIP stream of the tensors' device.  The calls do not wait for the
+GPU and may be captured into a graph (a captured call takes its workspace
+from the graph's own memory).
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import Optional, Tuple
+
+import torch
+
+from . import _check, _lib, _OnDevice, _raw_stream
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # nms_dtype
+_SCORES = {"softmax": 0, "sigmoid": 1}  # NMS_ROUTE_SOFTMAX, NMS_ROUTE_SIGMOID
+
+
+class _RouteOptions(ctypes.Structure):  # nms_route_options
+    _fields_ = [("score", ctypes.c_int), ("top_k", ctypes.c_int), ("renormalise", ctypes.c_int),
+                ("scale", ctypes.c_float), ("groups", ctypes.c_int),
+                ("kept_groups", ctypes.c_int), ("group_top", ctypes.c_int)]
+
+
+class _LogitRules(ctypes.Structure):  # nms_logit_rules
+    _fields_ = [("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64),
+                ("history_capacity", ctypes.c_int64), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_stride", ctypes.c_int64), ("bias_count", ctypes.c_int64),
+                ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64),
+                ("allowed_count", ctypes.c_int64), ("allowed_rows", ctypes.c_void_p)]
+
+
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t, name: str, device=None, shape=None, dtype=None) -> int:
+    """The row stride of a matrix whose rows hold neighbouring elements and
+    do not overlap; other layouts are refused."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix" % name)
+    if dtype is None:
+        if t.dtype not in _DTYPES:
+            raise TypeError("%s must be float32, float16 or bfloat16 (got %s)" % (name, t.dtype))
+    elif t.dtype is not dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if device is None:
+        if not t.is_cuda:
+            raise ValueError("%s must be on a GPU device" % name)
+    elif t.device != device:
+        raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    rows, columns = t.shape
+    if columns > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have neighbouring elements in a row" % name)
+    stride = t.stride(0)
+    if rows > 1 and stride < columns:
+        raise ValueError("the rows of %s overlap" % name)
+    return stride if rows > 1 else columns
+
+
+def _vector(t, name: str, n: int, dtype, device) -> Optional[int]:
+    """The address of a contiguous vector of n elements, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError("%s must have shape (%d,)" % (name, n))
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+# ------------------------------------------------------------------- routing
+
+@functools.lru_cache(maxsize=256)
+def _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top):
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
+    return _RouteOptions(_SCORES[score], int(top_k), int(bool(renormalise)), float(scale),
+                         int(groups), int(groups if kept_groups is None else kept_groups),
+                         int(group_top))
+
+
+def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
+                  bias: Optional[torch.Tensor] = None, groups: int = 1,
+                  kept_groups: Optional[int] = None, group_top: int = 2,
+                  renormalise: bool = True, scale: float = 1.0,
+                  live: Optional[torch.Tensor] = None, counts: bool = False):
+    """The experts of every token and their weights: ``(ids, weights)``, int32
+    and float32 tensors of shape (tokens, top_k); with ``counts=True`` also an
+    int32 tensor of how many tokens chose each expert.
+
+    ``logits`` is a (tokens, experts) tensor; ``bias`` (float32, one per
+    expert) counts for the choice only; of ``groups`` groups of neighbouring
+    experts ``kept_groups`` (default: all) may be chosen from; ``live`` (bool
+    or uint8, one per token) marks padded rows with 0.  A place that no expert
+    is left for holds id -1 and weight 0."""
+    stride = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    device = logits.device
+    options = _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top)
+    b = _vector(bias, "bias", experts, torch.float32, device)
+    alive = _vector(live, "live", tokens, torch.bool if live is not None and
+                    live.dtype is torch.bool else torch.uint8, device)
+    with _OnDevice(device):
+        # a call that will be refused allocates no negative shape
+        shape = (tokens, max(options.top_k, 0))
+        ids = torch.empty(shape, dtype=torch.int32, device=device)
+        weights = torch.empty(shape, dtype=torch.float32, device=device)
+        count = torch.empty(experts, dtype=torch.int32, device=device) if counts else None
+        _check(_lib.nms_route_experts(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts,
+                                      stride, b, alive, ctypes.byref(options), ids.data_ptr(),
+                                      weights.data_ptr(), _address(count), _raw_stream(device)))
+    return (ids, weights, count) if counts else (ids, weights)
+
+
+def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.Tensor,
+                           score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+                           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of ``route_experts``' weights in its logits, from the
+    forward call's ``ids`` and the gradient of its weights; a tensor like
+    ``logits`` (or ``out``).  The choice of the experts, and so the bias, has
+    no gradient."""
+    stride = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    device = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a matrix of shape (tokens, top_k)")
+    shape = torch.Size((tokens, ids.shape[1]))
+    for t, name, dtype in ((ids, "ids", torch.int32), (grad_weights, "grad_weights",
+                                                       torch.float32)):
+        _rows(t, name, device, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    options = _route_options(score, ids.shape[1], renormalise, scale, 1, 1, 1)
+    with _OnDevice(device):
+        if out is None:
+            out = torch.empty((tokens, experts), dtype=logits.dtype, device=device)
+        out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
+        _check(_lib.nms_route_experts_backward(
+            logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, stride, ids.data_ptr(),
+            grad_weights.data_ptr(), ctypes.byref(options), out.data_ptr(), out_stride,
+            _raw_stream(device)))
+    return out
+
+
+# -------------------------------------------------------------------- logits
+
+class LogitRules:
+    """The rules of a batch of rows of logits (``nms_logit_rules``): penalties
+    for tokens of the history, biases and masks of allowed tokens.
+
+    A serving loop makes one and keeps it while the contents of its tensors
+    change from step to step; it holds on to the tensors.  All tensors are on
+    one device, with one row (or entry) per row of logits:
+
+    ``history`` (rows, capacity) int32, the prompt and then what was
+    generated; ``history_len`` and ``prompt_len`` (rows,) int32;
+    ``repetition``, ``presence``, ``frequency`` (rows,) float32; ``bias_ids``
+    int32 and ``bias_values`` float32, (rows, entries), ids outside the
+    vocabulary unused; ``allowed`` (masks, words) int64, bit v mod 64 of word
+    v // 64 for token v; ``allowed_rows`` (rows,) int32, the mask of each row
+    (negative: every token is allowed)."""
+
+    def __init__(self, vocab: int, history=None, history_len=None, prompt_len=None,
+                 repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None,
+                 allowed=None, allowed_rows=None):
+        self.vocab = int(vocab)
+        per_row = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids,
+                   bias_values, allowed_rows)
+        if allowed is not None and allowed_rows is None:
+            per_row += (allowed,)
+        given = [t for t in per_row + (allowed,) if t is not None]
+        if not all(isinstance(t, torch.Tensor) and t.dim() > 0 for t in given):
+            raise TypeError("the rules must be torch tensors with a dimension")
+        self.device = given[0].device if given else None
+        if given and not given[0].is_cuda:
+            raise ValueError("the rules must be on a GPU device")
+        rows = {t.shape[0] for t in per_row if t is not None}
+        if len(rows) > 1:
+            raise ValueError("the rules have different numbers of rows: %s" % sorted(rows))
+        self.rows = rows.pop() if rows else None
+        n, device = self.rows, self.device
+        if (history is None) != (history_len is None):
+            raise ValueError("history and history_len go together")
+        if prompt_len is not None and history is None:
+            raise ValueError("prompt_len goes with a history")
+        if (bias_ids is None) != (bias_values is None):
+            raise ValueError("bias_ids and bias_values go together")
+        if allowed_rows is not None and allowed is None:
+            raise ValueError("allowed_rows goes with masks of allowed tokens")
+        c = _LogitRules()
+        if history is not None:
+            c.history_stride = _rows(history, "history", device, None, torch.int32)
+            c.history, c.history_capacity = history.data_ptr(), history.shape[1]
+            c.history_len = _vector(history_len, "history_len", n, torch.int32, device)
+            c.prompt_len = _vector(prompt_len, "prompt_len", n, torch.int32, device)
+            # an empty history has no address
+            if history.shape[1] == 0:
+                c.history = c.history_len = c.prompt_len = None
+        c.repetition = _vector(repetition, "repetition", n, torch.float32, device)
+        c.presence = _vector(presence, "presence", n, torch.float32, device)
+        c.frequency = _vector(frequency, "frequency", n, torch.float32, device)
+        if bias_ids is not None:
+            c.bias_stride = _rows(bias_ids, "bias_ids", device, None, torch.int32)
+            if _rows(bias_values, "bias_values", device, bias_ids.shape,
+                     torch.float32) != c.bias_stride:
+                raise ValueError("bias_ids and bias_values must have the same strides")
+            c.bias_ids, c.bias_values = bias_ids.data_ptr(), bias_values.data_ptr()
+            c.bias_count = bias_ids.shape[1]
+        if allowed is not None:
+            c.allowed_stride = _rows(allowed, "allowed", device, None, torch.int64)
+            if allowed.shape[1] < (self.vocab + 63) // 64:
+                raise ValueError("allowed must have %d words per mask" % ((self.vocab + 63) // 64))
+            c.allowed, c.allowed_count = allowed.data_ptr(), allowed.shape[0]
+            c.allowed_rows = _vector(allowed_rows, "allowed_rows", n, torch.int32, device)
+        self._tensors = given
+        self._struct = c
+        self._ref = ctypes.byref(c)
+
+    def _for(self, rows: int, vocab: int, device) -> object:
+        """The struct's address, for logits of this shape."""
+        if self.vocab != vocab:
+            raise ValueError("the rules are for %d tokens, the logits have %d" % (self.vocab, vocab))
+        if self.rows is not None and self.rows != rows:
+            raise ValueError("the rules are for %d rows, the logits have %d" % (self.rows, rows))
+        if self.device is not None and self.device != device:
+            raise ValueError("the rules must be on %s (got %s)" % (device, self.device))
+        return self._ref
+
+
+def adjust_logits(logits: torch.Tensor, rules: LogitRules,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The logits under the rules, a tensor like ``logits`` (or ``out``, which
+    may be ``logits`` itself and must not overlap it otherwise)."""
+    stride = _rows(logits, "logits")
+    rows, vocab = logits.shape
+    device = logits.device
+    ref = rules._for(rows, vocab, device)
+    with _OnDevice(device):
+        if out is None:
+            out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
+        _check(_lib.nms_adjust_logits(logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, stride,
+                                      ref, out.data_ptr(), out_stride, _raw_stream(device)))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def pick_workspace_size(rows: int, vocab: int, max_top_k: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.nms_pick_workspace_size(rows, vocab, max_top_k, ctypes.byref(out)))
+    return int(out.value)
+
+
+def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64,
+                temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+                top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+                rules: Optional[LogitRules] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The next token of every row of ``logits`` under the rules: ``(ids,
+    logprobs)``, int32 and float32 tensors of shape (rows,).
+
+    ``uniform`` (rows,) float32 holds one number in [0, 1) per row;
+    ``temperature`` (0: the first token), ``top_p`` and ``min_p`` are float32
+    and ``top_k`` int32, one per row (top_k up to ``max_top_k``, at most
+    1024).  The logprob is that of the token under the softmax over all
+    allowed tokens.  A row without an allowed token gets -1 and -infinity."""
+    stride = _rows(logits, "logits")
+    rows, vocab = logits.shape
+    device = logits.device
+    if uniform is None:
+        raise TypeError("uniform must be a torch tensor")
+    f32 = torch.float32
+    u = _vector(uniform, "uniform", rows, f32, device)
+    t = _vector(temperature, "temperature", rows, f32, device)
+    k = _vector(top_k, "top_k", rows, torch.int32, device)
+    p = _vector(top_p, "top_p", rows, f32, device)
+    m = _vector(min_p, "min_p", rows, f32, device)
+    ref = None if rules is None else rules._for(rows, vocab, device)
+    with _OnDevice(device):
+        nbytes = pick_workspace_size(rows, vocab, max_top_k)
+        # from torch's allocator, not a kept Workspace: calls on other streams
+        # and captured graphs must not share one
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ids = torch.empty(rows, dtype=torch.int32, device=device)
+        logprobs = torch.empty(rows, dtype=f32, device=device)
+        _check(_lib.nms_pick_tokens(logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, stride,
+                                    ref, u, t, k, p, m, max_top_k, ids.data_ptr(),
+                                    logprobs.data_ptr(), buf.data_ptr(), nbytes,
+                                    _raw_stream(device)))
+    return ids, logprobs

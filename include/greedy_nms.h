@@ -44,7 +44,8 @@
  * has a destructor).
  *
  * Streams.  `stream` is a hipStream_t (NULL = the default stream).  All work
- * is enqueued on it.  Each nms_* compute call returns once its result is
+ * is enqueued on it.  The selection operators at the end of this header
+ * return at once; each other nms_* compute call returns once its result is
  * complete: its last kernel posts the result into a pinned buffer of the
  * pool and the host spins on it (for up to 2 ms, then it blocks in
  * hipStreamSynchronize); the profiled variants, nms_f32_static and calls
@@ -412,6 +413,170 @@ nms_status nms_matrix_f32_profiled(const float *boxes, const float *scores, int6
                                    float score_thresh, double sigma, int64_t *keep_out,
                                    int64_t *num_kept, void *workspace, size_t workspace_bytes,
                                    void *stream, float *stage_ms);
+
+/* ------------------------------------------------------------------------
+ * Selection operators of language models: the same step as NMS, a model's
+ * scores in and the selected indices out, by descending score with ties to
+ * the lower index.  Routing of tokens to experts (with its gradient),
+ * penalties, biases and grammar masks on logits, and the next token.
+ *
+ * These calls are asynchronous: they check their arguments, enqueue their
+ * launches on `stream` and return, so they may be captured into a graph.
+ * They allocate nothing, read nothing back and keep nothing; outputs and
+ * workspace must stay as they are until the work on the stream is done.
+ * Two calls that may run at the same time need workspaces of their own.
+ * Device data cannot make them fail: what bad values do is stated below.
+ * ------------------------------------------------------------------------ */
+
+typedef enum nms_dtype { NMS_F32 = 0, NMS_F16 = 1, NMS_BF16 = 2 } nms_dtype;
+
+#define NMS_ROUTE_SOFTMAX 0
+#define NMS_ROUTE_SIGMOID 1
+#define NMS_ROUTE_MAX_EXPERTS 1024
+#define NMS_ROUTE_MAX_TOP_K 64
+#define NMS_ROUTE_MAX_TOKENS (1 << 30)
+
+typedef struct nms_route_options {
+    int score;       /* NMS_ROUTE_SOFTMAX or NMS_ROUTE_SIGMOID */
+    int top_k;       /* experts per token, 1 .. NMS_ROUTE_MAX_TOP_K, and at most
+                        kept_groups * (experts / groups) */
+    int renormalise; /* nonzero: the weights of a token sum to scale */
+    float scale;     /* finite */
+    int groups;      /* groups of neighbouring experts; divides experts; 1: none */
+    int kept_groups; /* groups of a token that may be chosen from, 1 .. groups */
+    int group_top;   /* a group's score: the sum of its best 1 or 2 experts */
+} nms_route_options;
+
+/*
+ * nms_route_experts -- the experts of every token and their weights.
+ *   logits      device, tokens rows of `experts` elements of `dtype`,
+ *               row_stride elements apart.
+ *   bias        device float[experts] or NULL: added to the scores for the
+ *               choice only (balance), not for the weights.
+ *   live        device byte[tokens] or NULL: 0 marks a padded row.
+ *   ids         device int32[tokens * top_k]; weights: float, the same shape.
+ *   counts      device int32[experts] or NULL: receives how many tokens chose
+ *               each expert (written, not added to).
+ * Per token, in binary64 from the logits z:
+ *     s = exp(z - max z) / sum, or 1 / (1 + exp(-z));  c = s + bias.
+ * An expert with z or c NaN or -infinity is never chosen.  With groups > 1
+ * only the kept_groups groups with the largest sums of their best group_top c
+ * stay (a group with fewer takes those it has; with none it never stays).
+ * Then the first top_k experts by descending c (without bias by descending
+ * z), every tie to the lower index.  Their weights are scale * s, divided by
+ * the sum of the chosen s if renormalise is set (for softmax: the softmax of
+ * the chosen logits; all 0 where that sum is 0), rounded once to float32.
+ * Places that no expert is left for, and all places of a padded row, hold id
+ * -1 and weight 0.
+ * Returns NMS_OK, NMS_INVALID_ARG, NMS_TOO_LARGE (experts or tokens above the
+ * limits) or NMS_HIP_ERROR.
+ */
+nms_status nms_route_experts(const void *logits, nms_dtype dtype, int64_t tokens, int64_t experts,
+                             int64_t row_stride, const float *bias, const uint8_t *live,
+                             const nms_route_options *options, int32_t *ids, float *weights,
+                             int32_t *counts, void *stream);
+
+/*
+ * nms_route_experts_backward -- the gradient of nms_route_experts' weights in
+ * its logits (the choice itself has none, and neither has the bias).
+ *   logits, dtype, tokens, experts, row_stride, options  as in the forward
+ *                 call (of the options, the groups are not used).
+ *   ids           device, the forward call's ids (one outside 0..experts-1
+ *                 is an empty place).
+ *   grad_weights  device float[tokens * top_k]: the gradient of the weights.
+ *   grad_logits   device, tokens rows of `experts` elements of dtype,
+ *                 grad_stride elements apart; every element is written
+ *                 (0 in rows without a chosen expert).
+ * Computed in float32, rounded once.  Returns as nms_route_experts.
+ */
+nms_status nms_route_experts_backward(const void *logits, nms_dtype dtype, int64_t tokens,
+                                      int64_t experts, int64_t row_stride, const int32_t *ids,
+                                      const float *grad_weights, const nms_route_options *options,
+                                      void *grad_logits, int64_t grad_stride, void *stream);
+
+#define NMS_MAX_ROWS 65536
+#define NMS_MAX_VOCAB (1 << 22)
+#define NMS_MAX_HISTORY 1048575
+#define NMS_MAX_BIASES 2047
+#define NMS_MAX_TOP_K 1024
+
+/* What applies to a batch of rows of logits.  Every pointer is device memory
+ * or NULL; per-row arrays have one entry per row. */
+typedef struct nms_logit_rules {
+    const int32_t *history;     /* the row's tokens so far: the prompt, then what
+                                   was generated; rows history_stride apart */
+    int64_t history_stride;
+    int64_t history_capacity;   /* entries a row has, at most NMS_MAX_HISTORY */
+    const int32_t *history_len; /* entries in use (clamped into 0..capacity) */
+    const int32_t *prompt_len;  /* of them the prompt; NULL: none */
+    const float *repetition;    /* r > 0; NULL: 1 */
+    const float *presence;      /* NULL: 0 */
+    const float *frequency;     /* NULL: 0 */
+    const int32_t *bias_ids;    /* bias_count entries per row, bias_stride apart; */
+    const float *bias_values;   /* entries outside the vocabulary are unused */
+    int64_t bias_stride;
+    int64_t bias_count;         /* at most NMS_MAX_BIASES */
+    const uint64_t *allowed;    /* allowed_count masks, allowed_stride words apart: */
+    int64_t allowed_stride;     /* bit v mod 64 of word v / 64 set: v is allowed */
+    int64_t allowed_count;
+    const int32_t *allowed_rows; /* the mask of each row: negative: none, every
+                                    token is allowed; allowed_count or above: no
+                                    token is.  NULL: row i has mask i */
+} nms_logit_rules;
+
+/*
+ * nms_adjust_logits -- the rules applied to logits.
+ *   logits, out  device, rows of `vocab` elements of dtype, row_stride and
+ *                out_stride elements apart; out may be logits (with the same
+ *                stride), and must not overlap it otherwise.
+ * For token v of a row, with z its logit in float32, each step rounded to
+ * float32 (no fused multiply-add):
+ *     v is in the history:            z = z > 0 ? z / r : z * r
+ *     v was generated c > 0 times:    z = z - frequency * c;  z = z - presence
+ *     v is in the row's bias list:    z = z + value (of its last entry there)
+ *     v is not allowed:               z = -infinity
+ * and then once to dtype.  History entries outside the vocabulary are skipped.
+ * Returns NMS_OK, NMS_INVALID_ARG, NMS_TOO_LARGE or NMS_HIP_ERROR.
+ */
+nms_status nms_adjust_logits(const void *logits, nms_dtype dtype, int64_t rows, int64_t vocab,
+                             int64_t row_stride, const nms_logit_rules *rules, void *out,
+                             int64_t out_stride, void *stream);
+
+/*
+ * nms_pick_workspace_size -- device workspace needed by nms_pick_tokens.
+ * Returns NMS_OK, NMS_INVALID_ARG or NMS_TOO_LARGE.
+ */
+nms_status nms_pick_workspace_size(int64_t rows, int64_t vocab, int max_top_k, size_t *bytes);
+
+/*
+ * nms_pick_tokens -- the next token of every row, from its logits under the
+ * rules (which are applied on the way: adjusted logits are not written).
+ *   rules        as for nms_adjust_logits, or NULL: none.
+ *   uniform      device float[rows]: one number in [0, 1) per row.
+ *   temperature  device float[rows] or NULL (1): t; 0 takes the first token.
+ *   top_k        device int32[rows] or NULL (max_top_k): clamped into
+ *                1..max_top_k.
+ *   top_p, min_p device float[rows] or NULL (1 and 0).
+ *   max_top_k    1 .. NMS_MAX_TOP_K.
+ *   ids          device int32[rows]; logprobs: device float[rows].
+ *   workspace    device, 256-byte aligned, nms_pick_workspace_size() bytes.
+ * With z the adjusted logits in float32 (not rounded to dtype again), the
+ * candidates of a row are its first top_k tokens by descending z, ties to the
+ * lower token, without those at -infinity or NaN.  In binary64, with z0 the
+ * first one's: w = exp((z - z0) / t).  Of the candidates stay the shortest
+ * prefix whose sum reaches top_p times the sum of all, and of it those with
+ * w >= min_p, at least the first.  The token is the first of them at which
+ * the running sum passes uniform times their sum.  Its logprob is
+ * log(exp(z / t) / sum over all tokens of exp(z / t)), with t = 1 where the
+ * temperature is 0.  A row without candidates gets id -1, logprob -infinity.
+ * Returns NMS_OK, NMS_INVALID_ARG, NMS_WORKSPACE_TOO_SMALL, NMS_TOO_LARGE or
+ * NMS_HIP_ERROR.
+ */
+nms_status nms_pick_tokens(const void *logits, nms_dtype dtype, int64_t rows, int64_t vocab,
+                           int64_t row_stride, const nms_logit_rules *rules, const float *uniform,
+                           const float *temperature, const int32_t *top_k, const float *top_p,
+                           const float *min_p, int max_top_k, int32_t *ids, float *logprobs,
+                           void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
