@@ -1,4 +1,6 @@
-// Penalties for repeated tokens, biases and grammar masks on logits.
+// Penalties for repeated tokens, biases and grammar masks on logits: one
+// workgroup per slice of a row, which adjusts the tokens that the rules touch
+// in LDS and streams the slice once (adjust_core.h).
 #include "adjust_core.h"
 
 #pragma clang fp contract(off)
@@ -6,36 +8,51 @@
 namespace gnms {
 namespace {
 
-constexpr int AT = 1024;       // threads per workgroup
-constexpr int SLICE = 16384;   // tokens per workgroup (64 KiB of LDS words)
-
-template <typename T>
-__global__ __launch_bounds__(AT) void adjust_kernel(AdjustArgs a, int slices) {
-    extern __shared__ uint32_t word[];
+template <typename T, int THREADS, int SLICE>
+__global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a, int slices) {
+    __shared__ uint32_t word[SLICE];
     const int64_t row = blockIdx.x / slices;
     const int lo = (int)(blockIdx.x % slices) * SLICE;
     const int size = min(SLICE, a.vocab - lo);
     const RowRules r = row_rules(a.rules, row);
-    gather_rules(a.rules, r, row, lo, size, word, threadIdx.x, AT);
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + lo;
-    for (int i = threadIdx.x; i < size; i += AT)
-        out[i] = from_f32<T>(adjusted(a.rules, r, row, to_f32(in[i]), r.words ? word[i] : 0u,
-                                      lo + i));
+    if (r.words) slice_rules<T, THREADS, SLICE>(a.rules, r, row, lo, size, in, word);
+    for (int at = 8 * threadIdx.x; at < size; at += 8 * THREADS) {
+        float z[8];
+        adjusted8<T, SLICE>(r, lo, size, at, in, word, z);
+        if (size - at >= 8) {
+            Eight<T> e;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e.v[j] = from_f32<T>(z[j]);
+            __builtin_memcpy(out + at, &e, sizeof(e));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (at + j < size) out[at + j] = from_f32<T>(z[j]);
+        }
+    }
+}
+
+template <typename T, int THREADS, int SLICE>
+void run(const AdjustArgs &a, hipStream_t stream) {
+    const int slices = (a.vocab + SLICE - 1) / SLICE;
+    adjust_kernel<T, THREADS, SLICE><<<(unsigned)(a.rows * slices), THREADS, 0, stream>>>(a,
+                                                                                         slices);
 }
 
 template <typename T>
-void run(const AdjustArgs &a, hipStream_t stream) {
-    const int slices = (a.vocab + SLICE - 1) / SLICE;
-    adjust_kernel<T><<<(unsigned)(a.rows * slices), AT, SLICE * 4, stream>>>(a, slices);
+void choose(const AdjustArgs &a, hipStream_t stream) {
+    if (a.rows * ((a.vocab + 16383) / 16384) >= 256) run<T, 1024, 16384>(a, stream);
+    else run<T, 256, 2048>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_adjust(const AdjustArgs &a, hipStream_t stream) {
-    if (a.dtype == NMS_F32) run<float>(a, stream);
-    else if (a.dtype == NMS_F16) run<half_t>(a, stream);
-    else run<bf16_t>(a, stream);
+    if (a.dtype == NMS_F32) choose<float>(a, stream);
+    else if (a.dtype == NMS_F16) choose<half_t>(a, stream);
+    else choose<bf16_t>(a, stream);
     return hipGetLastError();
 }
 
