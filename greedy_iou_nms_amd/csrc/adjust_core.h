@@ -1,17 +1,15 @@
 // The rules on a slice of a row of logits, shared by nms_adjust_logits and
 // nms_pick_tokens.
 //
-// One word of LDS per token of the slice.  First the words gather what the
-// history and the bias list say: the place of the token's last bias entry
-// (11 bits, stored as 2047 - place so that no entry reads as all ones), a bit
-// for "seen in the prompt" and 20 bits of "how often generated".  Then the
-// touched words are replaced by the token's adjusted value, one thread per
-// touched token, and the slice is streamed once: an untouched word is a NaN
-// that no adjusted value is, so a token costs one compare and one select,
-// however many tokens the history touches.  (Adjusting while streaming costs
-// a division and four more operations for every token of a wave that holds
-// one touched token, and with a history of a few thousand tokens every wave
-// does.)
+// One word of LDS per token of the slice gathers what the history and the
+// bias list say about it: the place of its last bias entry (11 bits, stored
+// as 2047 - place so that no entry reads as all ones), a bit for "seen in the
+// prompt" and 20 bits of "how often generated".  Then every thread looks at
+// the words of its own tokens, eight neighbours at a time, and replaces each
+// touched word by the token's adjusted value: as many rounds as the wave's
+// fullest lane has touched tokens, not eight times the division and the four
+// operations behind it.  An untouched word is a NaN that no adjusted value
+// is, so that a token then costs one compare and one select.
 #pragma once
 
 #include "select_internal.h"
@@ -84,33 +82,26 @@ __device__ __forceinline__ uint32_t replaced(const nms_logit_rules &u, const Row
     return z != z ? 0x7fc00000u : __float_as_uint(z);
 }
 
-// Fills word[0..SLICE) for the tokens lo..lo+size-1 of the row: UNTOUCHED, or
-// the adjusted value's bits.  Every thread of the workgroup calls it, and it
-// ends with a barrier.  in: the slice's logits.
-template <typename T, int THREADS, int SLICE>
+// Gathers the rules of the tokens lo..lo+size-1 of the row in word[0..SLICE).
+// Every thread of the workgroup calls it, and it ends with a barrier.
+template <int THREADS, int SLICE>
 __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowRules &r,
-                                            int64_t row, int lo, int size, const T *in,
-                                            uint32_t *word) {
+                                            int64_t row, int lo, int size, uint32_t *word) {
     const int tid = threadIdx.x;
     const uint4 none = make_uint4(UNTOUCHED, UNTOUCHED, UNTOUCHED, UNTOUCHED);
     for (int i = tid; i < SLICE / 4; i += THREADS) reinterpret_cast<uint4 *>(word)[i] = none;
     __syncthreads();
-    const int32_t *bias_ids = u.bias_ids + row * u.bias_stride;
     if (u.bias_count > 0) {
+        const int32_t *ids = u.bias_ids + row * u.bias_stride;
         for (int i = tid; i < (int)u.bias_count; i += THREADS) {
-            const unsigned at = (unsigned)bias_ids[i] - (unsigned)lo;
+            const unsigned at = (unsigned)ids[i] - (unsigned)lo;
             if (at < (unsigned)size)
                 atomicMin(&word[slot<SLICE>(at)], (RULE_NO_BIAS - (uint32_t)(i + 1))
                                                       << RULE_BIAS_SHIFT);
         }
         __syncthreads();
     }
-    // The thread whose access is the first to a token adjusts it; which
-    // thread that is makes no difference to the value.  Up to 64 entries per
-    // thread are remembered in a bit each.
     const int32_t *history = u.history + row * u.history_stride;
-    const bool remember = r.length <= 64 * THREADS;
-    uint64_t owned = 0;
     for (int i0 = 0; i0 < r.length; i0 += 4 * THREADS) {
         int v[4];
 #pragma unroll
@@ -123,53 +114,9 @@ __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowR
             const unsigned at = (unsigned)v[q] - (unsigned)lo;
             if (at < (unsigned)size) {
                 uint32_t *w = &word[slot<SLICE>(at)];
-                const uint32_t old = i0 + q * THREADS + tid < r.prompt ? atomicOr(w, RULE_SEEN)
-                                                                       : atomicAdd(w, 1u);
-                if ((old & RULE_TOUCHED) == 0u && remember)
-                    owned |= 1ull << (i0 / THREADS + q);
+                if (i0 + q * THREADS + tid < r.prompt) atomicOr(w, RULE_SEEN);
+                else atomicAdd(w, 1u);
             }
-        }
-    }
-    __syncthreads();
-    if (remember) {
-        // tokens that only the bias list touches: decided for every entry
-        // before any word is replaced
-        constexpr int MOST = (NMS_MAX_BIASES + THREADS - 1) / THREADS;
-        uint32_t biased[MOST];
-#pragma unroll
-        for (int q = 0; q < MOST; ++q) {
-            const int i = q * THREADS + tid;
-            biased[q] = UNTOUCHED;
-            if (i < (int)u.bias_count) {
-                const unsigned at = (unsigned)bias_ids[i] - (unsigned)lo;
-                if (at < (unsigned)size) {
-                    const uint32_t w = word[slot<SLICE>(at)];
-                    if ((w & RULE_TOUCHED) == 0u &&
-                        w >> RULE_BIAS_SHIFT == RULE_NO_BIAS - (uint32_t)(i + 1))
-                        biased[q] = w;
-                }
-            }
-        }
-        if (u.bias_count > 0) __syncthreads();
-#pragma unroll
-        for (int q = 0; q < MOST; ++q)
-            if (biased[q] != UNTOUCHED) {
-                const unsigned at = (unsigned)bias_ids[q * THREADS + tid] - (unsigned)lo;
-                word[slot<SLICE>(at)] = replaced(u, r, row, to_f32(in[at]), biased[q]);
-            }
-        while (owned != 0ull) {
-            const int q = __builtin_ctzll(owned);
-            owned &= owned - 1ull;
-            const unsigned at = (unsigned)history[q * THREADS + tid] - (unsigned)lo;
-            uint32_t *w = &word[slot<SLICE>(at)];
-            *w = replaced(u, r, row, to_f32(in[at]), *w);
-        }
-    } else {
-        // a history this long touches a good part of the slice: every thread
-        // looks through tokens of its own
-        for (int i = tid; i < size; i += THREADS) {
-            uint32_t *w = &word[slot<SLICE>(i)];
-            if (*w != UNTOUCHED) *w = replaced(u, r, row, to_f32(in[i]), *w);
         }
     }
     __syncthreads();
@@ -182,35 +129,55 @@ struct Eight {
 };
 
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int left, float *z) {
+__device__ __forceinline__ Eight<T> load8(const T *p, int left) {
+    Eight<T> e;
     if (left >= 8) {
-        Eight<T> e;
         __builtin_memcpy(&e, p, sizeof(e));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = to_f32(e.v[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = j < left ? to_f32(p[j]) : NEG_INF;
+        for (int j = 0; j < 8; ++j) e.v[j] = j < left ? p[j] : from_f32<T>(NEG_INF);
     }
+    return e;
 }
 
 // The adjusted values of the eight tokens at..at+7 of the slice (at a
-// multiple of 8); those past the slice are -infinity.
+// multiple of 8) from their logits, which start at in; those past the slice
+// are -infinity.
 template <typename T, int SLICE>
-__device__ __forceinline__ void adjusted8(const RowRules &r, int lo, int size, int at, const T *in,
-                                          const uint32_t *word, float *z) {
-    load8(in + at, size - at, z);
+__device__ __forceinline__ void adjusted8(const nms_logit_rules &u, const RowRules &r, int64_t row,
+                                          int lo, int size, int at, const T *in,
+                                          const Eight<T> &logits, uint32_t *word, float *z) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] = to_f32(logits.v[j]);
     if (r.words) {
         uint32_t w[8];
-        __builtin_memcpy(w, word + at / 2, 16);
-        __builtin_memcpy(w + 4, word + SLICE / 2 + at / 2, 16);
+        uint4 *w0 = reinterpret_cast<uint4 *>(word + at / 2);
+        uint4 *w1 = reinterpret_cast<uint4 *>(word + SLICE / 2 + at / 2);
+        __builtin_memcpy(w, w0, 16);
+        __builtin_memcpy(w + 4, w1, 16);
+        uint32_t touched = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) touched |= w[j] == UNTOUCHED ? 0u : 1u << j;
+        if (touched != 0u) {
+            do {
+                const int j = __builtin_ctz(touched);
+                touched &= touched - 1u;
+                uint32_t *x = word + (j >> 2) * (SLICE / 2) + at / 2 + (j & 3);
+                *x = replaced(u, r, row, to_f32(in[at + j]), *x);
+            } while (touched != 0u);
+            __builtin_memcpy(w, w0, 16);
+            __builtin_memcpy(w + 4, w1, 16);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] = w[j] == UNTOUCHED ? z[j] : __uint_as_float(w[j]);
     }
     if (r.allowed) {
-        const uint32_t bits = at < size ? r.allowed[(lo + at) >> 3] : 0u;
+        const int bits = at < size ? r.allowed[(lo + at) >> 3] : 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = (bits >> j) & 1u ? z[j] : NEG_INF;
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t keep = (uint32_t)((int)((uint32_t)bits << (31 - j)) >> 31);
+            z[j] = __uint_as_float((__float_as_uint(z[j]) & keep) | (0xff800000u & ~keep));
+        }
     } else if (r.none_allowed) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] = NEG_INF;

@@ -9,18 +9,18 @@ namespace gnms {
 namespace {
 
 template <typename T, int THREADS, int SLICE>
-__global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a, int slices) {
+__global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
     __shared__ uint32_t word[SLICE];
-    const int64_t row = blockIdx.x / slices;
-    const int lo = (int)(blockIdx.x % slices) * SLICE;
+    const int64_t row = blockIdx.x;
+    const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
     const RowRules r = row_rules(a.rules, row);
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + lo;
-    if (r.words) slice_rules<T, THREADS, SLICE>(a.rules, r, row, lo, size, in, word);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, word);
     for (int at = 8 * threadIdx.x; at < size; at += 8 * THREADS) {
         float z[8];
-        adjusted8<T, SLICE>(r, lo, size, at, in, word, z);
+        adjusted8<T, SLICE>(a.rules, r, row, lo, size, at, in, load8(in + at, size - at), word, z);
         if (size - at >= 8) {
             Eight<T> e;
 #pragma unroll
@@ -36,9 +36,8 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a, int slice
 
 template <typename T, int THREADS, int SLICE>
 void run(const AdjustArgs &a, hipStream_t stream) {
-    const int slices = (a.vocab + SLICE - 1) / SLICE;
-    adjust_kernel<T, THREADS, SLICE><<<(unsigned)(a.rows * slices), THREADS, 0, stream>>>(a,
-                                                                                         slices);
+    const dim3 grid((unsigned)a.rows, (unsigned)((a.vocab + SLICE - 1) / SLICE));
+    adjust_kernel<T, THREADS, SLICE><<<grid, THREADS, 0, stream>>>(a);
 }
 
 template <typename T>

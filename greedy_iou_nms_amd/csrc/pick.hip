@@ -18,10 +18,10 @@
 namespace gnms {
 namespace {
 
-constexpr int JT = 1024;     // threads of the join
-constexpr int JCAP = 2 * JT; // candidates that the join sorts
-constexpr int BINS = 512;    // of the histograms that bound the k-th value
-static_assert(NMS_MAX_TOP_K <= JT, "a candidate per thread once they are sorted");
+constexpr int BINS = 512;         // of a slice's histogram
+constexpr int JOIN_BINS = 1024;   // of the join's
+constexpr int JOIN_HELD = 12;     // pieces of 64 candidates that a wave of it holds
+constexpr int CROWDED = 64;       // most candidates of a bin that it ranks one by one
 
 struct Part {
     float top;       // the slice's largest value
@@ -64,6 +64,15 @@ struct Bins {
         // v = lo gives 0 whatever the scale; an overflow ends in the last bin
         return (int)fminf((v - lo) * scale, (float)(bins - 1));
     }
+    // Not above any value of bin b or higher, and not far below (-1: below
+    // every value).  v in such a bin has (v - lo) * scale >= b after two
+    // roundings, of 2^-24 each; the subtracted parts cover these and the
+    // roundings here.
+    __device__ __forceinline__ float edge(int b) const {
+        if (b <= 0 || !(scale > 0.0f)) return b < 0 || !(lo > -3.4e38f) ? -3.402823466e38f : lo;
+        const float up = (float)b / scale;
+        return fmaxf(lo, (lo + up) - (fabsf(lo) + up) * 0x1p-20f);
+    }
 };
 
 // The highest bin at or above which there are at least `need` entries, and
@@ -97,43 +106,67 @@ __device__ __forceinline__ int bin_of_rank(const uint32_t *hist, uint32_t need) 
     return __shfl(bin, at);
 }
 
+// One digit of a k-th largest word: chosen[0] is the digit of the word that
+// is `left`-th largest among those counted in hist[0..256), chosen[1] its rank
+// among those with this digit.  One wave.
+__device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t left,
+                                              uint32_t *chosen) {
+    const int lane = threadIdx.x & 63;
+    const int d = bin_of_rank<4>(hist, left);
+    uint32_t over = 0;
+    for (int i = d + 1 + lane; i < 256; i += 64) over += hist[i];
+    over = wave_sum(over);
+    if (lane == 0) {
+        chosen[0] = (uint32_t)d;
+        chosen[1] = left - over;
+    }
+}
+
 // ------------------------------------------------------------------- slices
 
 // VALUES per thread in groups of eight neighbouring tokens; GROUP of them
 // share an entry in the histogram (their largest).
 template <typename T, int THREADS, int VALUES, int GROUP>
-__global__ __launch_bounds__(THREADS) void slice_kernel(PickArgs a, int slices, Part *parts,
-                                                        uint64_t *found) {
+__global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *parts,
+                                                           uint64_t *found) {
     constexpr int SLICE = THREADS * VALUES;
     constexpr int WAVES = THREADS / 64;
-    __shared__ uint32_t word[SLICE];
-    __shared__ uint32_t hist[BINS], low[BINS];
-    __shared__ float wave_top[WAVES], wave_low[WAVES];
-    __shared__ float wave_sums[WAVES];
-    __shared__ uint32_t bound_key, taken, chosen[2];
+    __shared__ uint32_t word[SLICE];  // the rules, then the values
+    __shared__ uint32_t hist[BINS];
+    __shared__ float wave_top[WAVES], wave_low[WAVES], wave_sums[WAVES];
+    __shared__ uint32_t taken, chosen[2];
+    __shared__ float bound;
     const int tid = threadIdx.x, wave = tid >> 6;
-    const int64_t row = blockIdx.x / slices;
-    const int lo = (int)(blockIdx.x % slices) * SLICE;
+    const int64_t row = blockIdx.x;
+    const int64_t part = row * gridDim.y + blockIdx.y;
+    const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
     const RowRules r = row_rules(a.rules, row);
     const float c = fminf(1.4426950408889634f / warmth(a.temperature, row), 3.0e38f);
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
-    for (int i = tid; i < BINS; i += THREADS) {
-        hist[i] = 0;
-        low[i] = 0xffffffffu;
+    Eight<T> logits[VALUES / 8];  // in flight while the rules are gathered
+#pragma unroll
+    for (int g = 0; g < VALUES / 8; ++g) {
+        const int at = 8 * (g * THREADS + tid);
+        logits[g] = load8(in + at, size - at);
     }
+    for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) taken = 0;
-    if (r.words) slice_rules<T, THREADS, SLICE>(a.rules, r, row, lo, size, in, word);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, word);
     float z[VALUES];
 #pragma unroll
-    for (int g = 0; g < VALUES / 8; ++g)
-        adjusted8<T, SLICE>(r, lo, size, 8 * (g * THREADS + tid), in, word, z + 8 * g);
+    for (int g = 0; g < VALUES / 8; ++g) {
+        const int at = 8 * (g * THREADS + tid);
+        adjusted8<T, SLICE>(a.rules, r, row, lo, size, at, in, logits[g], word, z + 8 * g);
+        // a copy that can be read by a number of its place
+        __builtin_memcpy(word + at / 2, z + 8 * g, 16);
+        __builtin_memcpy(word + SLICE / 2 + at / 2, z + 8 * g + 4, 16);
+    }
     // v_max drops a NaN
     float m[VALUES / GROUP], top = NEG_INF, least = __builtin_inff();
 #pragma unroll
     for (int g = 0; g < VALUES / GROUP; ++g) {
-        m[g] = z[g * GROUP];
-        if (!(m[g] > NEG_INF)) m[g] = NEG_INF;
+        m[g] = fmaxf(NEG_INF, z[g * GROUP]);
 #pragma unroll
         for (int j = 1; j < GROUP; ++j) m[g] = fmaxf(m[g], z[g * GROUP + j]);
         top = fmaxf(top, m[g]);
@@ -160,38 +193,41 @@ __global__ __launch_bounds__(THREADS) void slice_kernel(PickArgs a, int slices, 
         wave_sums[wave] = sum;
     }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        top = fmaxf(top, wave_top[w]);
-        least = fminf(least, wave_low[w]);
-    }
+    top = wave_max((tid & 63) < WAVES ? wave_top[tid & (WAVES - 1)] : NEG_INF);
+    least = -wave_max((tid & 63) < WAVES ? -wave_low[tid & (WAVES - 1)] : NEG_INF);
     const int k = a.max_top_k, cap = slice_cap(k);
     const Bins bins(least, top, BINS);
 #pragma unroll
     for (int g = 0; g < VALUES / GROUP; ++g)
-        if (m[g] > NEG_INF) {
-            const int b = bins.of(m[g], BINS);
-            atomicAdd(&hist[b], 1u);
-            atomicMin(&low[b], order_key(m[g]));
-        }
+        if (m[g] > NEG_INF) atomicAdd(&hist[bins.of(m[g], BINS)], 1u);
     __syncthreads();
     if (wave == 0) {
         const int b = bin_of_rank<BINS / 64>(hist, (uint32_t)k);
-        // fewer groups than k: every value is a candidate
-        if (tid == 0) bound_key = b < 0 ? 1u : low[b];
+        if (tid == 0) bound = bins.edge(b);
     }
     __syncthreads();
     // at least k values (or all there are) lie at the bound or above
-    const uint32_t bound = bound_key;
-    float edge = bound <= 1u ? -3.402823466e38f : key_value(bound);
-    uint64_t *to = found + (int64_t)blockIdx.x * cap;
+    float edge = bound;
+    uint32_t hits = 0;
 #pragma unroll
-    for (int j = 0; j < VALUES; ++j)
-        if (z[j] >= edge) {
-            const uint32_t at = atomicAdd(&taken, 1u);
-            if (at < (uint32_t)cap)
-                to[at] = candidate(z[j], lo + 8 * ((j / 8) * THREADS + tid) + j % 8);
-        }
+    for (int j = 0; j < VALUES; ++j) hits |= z[j] >= edge ? 1u << j : 0u;
+    const uint32_t mine = (uint32_t)__popc(hits);
+    const uint32_t through = wave_scan(mine);
+    uint32_t to = 0;
+    if ((tid & 63) == 63) to = atomicAdd(&taken, through);
+    to = last_lane(to) + through - mine;
+    // the candidate of the thread's j-th token
+    auto own = [&](int j) -> uint64_t {
+        const int at = 8 * ((j >> 3) * THREADS + tid) + (j & 7);
+        return candidate(__uint_as_float(word[slot<SLICE>((unsigned)at)]), lo + at);
+    };
+    found += part * cap;
+    while (hits != 0u) {
+        const int j = __builtin_ctz(hits);
+        hits &= hits - 1u;
+        if (to < (uint32_t)cap) found[to] = own(j);
+        ++to;
+    }
     __syncthreads();
     if (taken > (uint32_t)cap) {
         // Equal values, or a spread that the bins do not resolve: the k-th
@@ -201,96 +237,78 @@ __global__ __launch_bounds__(THREADS) void slice_kernel(PickArgs a, int slices, 
         for (int shift = 56; shift >= 0; shift -= 8) {
             for (int i = tid; i < 256; i += THREADS) hist[i] = 0;
             __syncthreads();
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < VALUES; ++j) {
-                const uint64_t w = candidate(z[j], lo + 8 * ((j / 8) * THREADS + tid) + j % 8);
+                const uint64_t w = own(j);
                 if (w != 0 && (w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
             }
             __syncthreads();
-            if (wave == 0) {
-                const int d = bin_of_rank<4>(hist, left);
-                uint32_t over = 0;
-                for (int i = d + 1 + (tid & 63); i < 256; i += 64) over += hist[i];
-                over = wave_sum(over);
-                if (tid == 0) {
-                    chosen[0] = (uint32_t)d;
-                    chosen[1] = left - over;
-                }
-            }
+            if (wave == 0) digit_of_rank(hist, left, chosen);
             if (tid == 0) taken = 0;
             __syncthreads();
             prefix |= (uint64_t)chosen[0] << shift;
             mask |= 255ull << shift;
             left = chosen[1];
         }
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < VALUES; ++j) {
-            const uint64_t w = candidate(z[j], lo + 8 * ((j / 8) * THREADS + tid) + j % 8);
-            if (w >= prefix) to[atomicAdd(&taken, 1u)] = w;
+            const uint64_t w = own(j);
+            if (w >= prefix) found[atomicAdd(&taken, 1u)] = w;
         }
         edge = key_value((uint32_t)(prefix >> 32));
         __syncthreads();
     }
-    if (tid == 0) {
+    if (wave == 0) {
+        const float wt = tid < WAVES ? wave_top[tid & (WAVES - 1)] : NEG_INF;
         double all = 0.0;
-        for (int w = 0; w < WAVES; ++w)
-            if (wave_top[w] > NEG_INF)
-                all += (double)wave_sums[w] *
-                       (wave_top[w] == top ? 1.0
-                                           : (double)__builtin_amdgcn_exp2f((wave_top[w] - top) * c));
-        parts[blockIdx.x] = Part{top, edge, taken, all};
+        if (wt > NEG_INF)
+            all = (double)wave_sums[tid & (WAVES - 1)] *
+                  (wt == top ? 1.0 : (double)__builtin_amdgcn_exp2f((wt - top) * c));
+        all = wave_sum(all);
+        if (tid == 0) parts[part] = Part{top, edge, taken, all};
     }
 }
 
 // --------------------------------------------------------------------- join
 
-// Descending sort of E * JT words over the workgroup, word t + JT * e in
-// thread t; only the first `n` (a power of two, 64 at least) take part.  Steps
-// within a wave are shuffles, between waves they go through LDS.
-template <int E>
-__device__ __forceinline__ void sort_words(uint64_t *v, int n, uint64_t *lds) {
+// Descending sort of one word per thread over the first n threads (n a power
+// of two, 64 at least; the others' words must be 0).  Steps within a wave are
+// shuffles, between waves they go through LDS.
+__device__ __forceinline__ uint64_t sort_words(uint64_t v, int n, uint64_t *lds) {
     const int tid = threadIdx.x;
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step > 0; step >>= 1) {
-            if (E == 2 && step == JT) {
-                const uint64_t x = v[0], y = v[E - 1];
-                v[0] = x > y ? x : y;
-                v[E - 1] = x > y ? y : x;
-                continue;
-            }
-            uint64_t other[E];
+            uint64_t other;
             if (step >= 64) {
                 __syncthreads();
-#pragma unroll
-                for (int e = 0; e < E; ++e) lds[tid + JT * e] = v[e];
+                lds[tid] = v;
                 __syncthreads();
-#pragma unroll
-                for (int e = 0; e < E; ++e) other[e] = lds[(tid ^ step) + JT * e];
+                other = lds[tid ^ step];
             } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) other[e] = __shfl_xor((unsigned long long)v[e], step);
+                other = __shfl_xor((unsigned long long)v, step);
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = tid + JT * e;
-                // the larger word goes to the lower place in a descending run
-                const bool larger = ((i & size) == 0) == ((i & step) == 0);
-                if ((other[e] > v[e]) == larger) v[e] = other[e];
-            }
+            // the larger word goes to the lower place in a descending run
+            const bool larger = ((tid & size) == 0) == ((tid & step) == 0);
+            if ((other > v) == larger) v = other;
         }
+    return v;
 }
 
-__global__ __launch_bounds__(JT) void join_kernel(PickArgs a, int slices, const Part *parts,
-                                                  const uint64_t *found) {
-    constexpr int WAVES = JT / 64;
-    constexpr int HELD = 12;  // pieces of 64 candidates that a wave keeps in registers
-    __shared__ uint64_t list[JCAP];
-    __shared__ double scan[JT];
-    __shared__ uint32_t hist[JT];
-    __shared__ double wave_d[WAVES];
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, const Part *parts,
+                                                       const uint64_t *found) {
+    constexpr int WAVES = THREADS / 64;
+    constexpr int HELD = JOIN_HELD;
+    constexpr int PER = JOIN_BINS / THREADS;  // bins per thread
+    constexpr int LIST = THREADS + CROWDED;
+    __shared__ uint64_t list[LIST], sorted[THREADS];
+    __shared__ uint32_t hist[JOIN_BINS], fill[JOIN_BINS];
+    __shared__ double wave_d[2][WAVES];
     __shared__ float wave_f[3][WAVES];
-    __shared__ int wave_i[4][WAVES];
-    __shared__ uint32_t taken, chosen[2];
+    __shared__ uint32_t wave_u[WAVES];
+    __shared__ int wave_i[3][WAVES];
+    __shared__ uint32_t taken, crowded, inside, chosen[2];
+    __shared__ double kept;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int kmax = a.max_top_k, cap = slice_cap(kmax);
@@ -311,21 +329,24 @@ __global__ __launch_bounds__(JT) void join_kernel(PickArgs a, int slices, const 
     uint64_t held[HELD];
 #pragma unroll
     for (int q = 0; q < HELD; ++q) held[q] = load(q * WAVES + wave);
+    // f is called with every candidate, and with 0 in their places' rest
     auto each = [&](auto f) {
 #pragma unroll
         for (int q = 0; q < HELD; ++q)
-            if (held[q] != 0) f(held[q]);
-        for (int p = HELD * WAVES + wave; p < total; p += WAVES) {
-            const uint64_t w = load(p);
-            if (w != 0) f(w);
-        }
+            if (q * WAVES < total) f(held[q]);
+        for (int p = HELD * WAVES + wave; p < total; p += WAVES) f(load(p));
     };
+    // the row's parameters, in flight with the candidates
     const float t = a.temperature ? a.temperature[row] : 1.0f;
-    const float warm = warmth(a.temperature, row);
+    const float warm = t > 0.0f ? t : 1.0f;
+    const double top_p = a.top_p ? (double)a.top_p[row] : 1.0;
+    const double min_p = a.min_p ? (double)a.min_p[row] : 0.0;
+    const double uniform = (double)a.uniform[row];
+    const int k = min(max(a.top_k ? a.top_k[row] : kmax, 1), kmax);
     // The row's largest value; a bound that its max_top_k-th value is not
     // below (any slice's with so many candidates), or one below them all.
     float top = NEG_INF, edge = NEG_INF, least = __builtin_inff();
-    for (int s = tid; s < slices; s += JT) {
+    for (int s = tid; s < slices; s += THREADS) {
         const Part x = parts[s];
         top = fmaxf(top, x.top);
         if (x.count >= (uint32_t)kmax) edge = fmaxf(edge, x.edge);
@@ -339,15 +360,21 @@ __global__ __launch_bounds__(JT) void join_kernel(PickArgs a, int slices, const 
         wave_f[1][wave] = edge;
         wave_f[2][wave] = least;
     }
-    hist[tid] = 0;
-    if (tid == 0) taken = 0;
-    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        top = fmaxf(top, wave_f[0][w]);
-        edge = fmaxf(edge, wave_f[1][w]);
-        least = fminf(least, wave_f[2][w]);
+    for (int i = 0; i < PER; ++i) {
+        hist[i * THREADS + tid] = 0;
+        fill[i * THREADS + tid] = 0;
     }
+    if (tid == 0) {
+        taken = 0;
+        crowded = 0;
+    }
+    sorted[tid] = 0;
+    for (int i = tid; i < LIST; i += THREADS) list[i] = 0;
+    __syncthreads();
+    top = wave_max(lane < WAVES ? wave_f[0][lane & (WAVES - 1)] : NEG_INF);
+    edge = wave_max(lane < WAVES ? wave_f[1][lane & (WAVES - 1)] : NEG_INF);
+    least = -wave_max(lane < WAVES ? -wave_f[2][lane & (WAVES - 1)] : NEG_INF);
     if (!(top > NEG_INF)) {
         if (tid == 0) {
             a.ids[row] = -1;
@@ -356,145 +383,133 @@ __global__ __launch_bounds__(JT) void join_kernel(PickArgs a, int slices, const 
         return;
     }
     if (!(edge > NEG_INF)) edge = least;
-    // the candidates at the bound or above, as far as the list holds them
+    // Counting sort by bins between the bound and the top, then by rank
+    // within a bin; bins that start at rank max_top_k or later are left out.
+    const Bins bins(edge, top, JOIN_BINS);
     each([&](uint64_t w) {
-        if (key_value((uint32_t)(w >> 32)) >= edge) {
-            const uint32_t at = atomicAdd(&taken, 1u);
-            if (at < (uint32_t)JCAP) list[at] = w;
-        }
+        const float v = key_value((uint32_t)(w >> 32));
+        if (w != 0 && v >= edge) atomicAdd(&hist[bins.of(v, JOIN_BINS)], 1u);
     });
     __syncthreads();
-    if (taken > (uint32_t)JCAP) {
-        // too many: a closer bound, from a histogram between it and the top
-        const Bins bins(edge, top, JT);
+    // bins in descending order: thread i has those from JOIN_BINS - 1 - i * PER
+    uint32_t counts[PER], bin_sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        counts[i] = hist[JOIN_BINS - 1 - tid * PER - i];
+        bin_sum += counts[i];
+    }
+    uint32_t start = wave_scan(bin_sum);
+    if (lane == 63) wave_u[wave] = start;
+    __syncthreads();
+    uint32_t earlier = lane < wave ? wave_u[lane & (WAVES - 1)] : 0u;
+    start += wave_sum(earlier) - bin_sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        hist[JOIN_BINS - 1 - tid * PER - i] = start;
+        if (start < (uint32_t)kmax && counts[i] > (uint32_t)CROWDED) crowded = 1;
+        start += counts[i];
+    }
+    if (tid == THREADS - 1) inside = start;
+    __syncthreads();
+    uint64_t mine;
+    if (crowded == 0) {
         each([&](uint64_t w) {
             const float v = key_value((uint32_t)(w >> 32));
-            if (v >= edge) atomicAdd(&hist[bins.of(v, JT)], 1u);
+            if (w != 0 && v >= edge) {
+                const int b = bins.of(v, JOIN_BINS);
+                const uint32_t first = hist[b];
+                // a bin that starts before kmax ends before LIST
+                if (first < (uint32_t)kmax) list[first + atomicAdd(&fill[b], 1u)] = w;
+            }
         });
         __syncthreads();
-        if (wave == 0) {
-            const int b = bin_of_rank<JT / 64>(hist, (uint32_t)kmax);
-            uint32_t inside = 0;
-            for (int i = b + lane; i < JT; i += 64) inside += hist[i];
-            inside = wave_sum(inside);
-            if (lane == 0) {
-                chosen[0] = (uint32_t)b;
-                chosen[1] = inside;
-                taken = 0;
-            }
+        for (int i = tid; i < LIST; i += THREADS) {
+            const uint64_t w = list[i];
+            if (w == 0) break;
+            const int b = bins.of(key_value((uint32_t)(w >> 32)), JOIN_BINS);
+            const uint32_t first = hist[b], last = first + fill[b];
+            uint32_t rank = first;
+            for (uint32_t x = first; x < last; ++x) rank += list[x] > w ? 1u : 0u;
+            if (rank < (uint32_t)THREADS) sorted[rank] = w;
         }
         __syncthreads();
-        const int b = (int)chosen[0];
-        if (chosen[1] <= (uint32_t)JCAP) {
-            each([&](uint64_t w) {
-                const float v = key_value((uint32_t)(w >> 32));
-                if (v >= edge && bins.of(v, JT) >= b) list[atomicAdd(&taken, 1u)] = w;
-            });
+        mine = sorted[tid];
+    } else {
+        // Many values that are equal or nearly so: the kmax-th largest word,
+        // digit by digit, and a sort of those from there up.
+        uint64_t prefix = 0, mask = 0;
+        uint32_t left = (uint32_t)kmax;
+        if (inside <= (uint32_t)kmax) {
+            prefix = 1;
         } else {
-            // as in the slices: the k-th largest word, digit by digit
-            uint64_t prefix = 0, mask = 0;
-            uint32_t left = (uint32_t)kmax;
             for (int shift = 56; shift >= 0; shift -= 8) {
                 __syncthreads();
-                if (tid < 256) hist[tid] = 0;
+                if (tid < 256) fill[tid] = 0;
                 __syncthreads();
                 each([&](uint64_t w) {
-                    if ((w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
+                    if (w != 0 && (w & mask) == prefix) atomicAdd(&fill[(w >> shift) & 255], 1u);
                 });
                 __syncthreads();
-                if (wave == 0) {
-                    const int d = bin_of_rank<4>(hist, left);
-                    uint32_t over = 0;
-                    for (int i = d + 1 + lane; i < 256; i += 64) over += hist[i];
-                    over = wave_sum(over);
-                    if (lane == 0) {
-                        chosen[0] = (uint32_t)d;
-                        chosen[1] = left - over;
-                    }
-                }
+                if (wave == 0) digit_of_rank(fill, left, chosen);
                 __syncthreads();
                 prefix |= (uint64_t)chosen[0] << shift;
                 mask |= 255ull << shift;
                 left = chosen[1];
             }
-            each([&](uint64_t w) {
-                if (w >= prefix) list[atomicAdd(&taken, 1u)] = w;
-            });
         }
+        each([&](uint64_t w) {
+            if (w >= prefix && key_value((uint32_t)(w >> 32)) >= edge)
+                list[atomicAdd(&taken, 1u)] = w;
+        });
         __syncthreads();
-    }
-    const int listed = (int)taken;
-    uint64_t v[2];
-    v[0] = tid < listed ? list[tid] : 0ull;
-    v[1] = JT + tid < listed ? list[JT + tid] : 0ull;
-    if (listed > JT) {
-        sort_words<2>(v, JCAP, list);
-    } else {
+        mine = list[tid];
         int p = 64;
-        while (p < listed) p <<= 1;
-        sort_words<1>(v, p, list);
+        while (p < (int)taken) p <<= 1;
+        mine = sort_words(mine, p, list);
     }
-    const uint64_t mine = v[0];
 
-    int k = a.top_k ? a.top_k[row] : kmax;
-    k = min(max(k, 1), kmax);
     const bool there = tid < k && mine != 0;
     const float z = key_value((uint32_t)(mine >> 32));
     const double w = there ? exp(below_top(z, top) / (double)warm) : 0.0;
     // running sums of the candidates' weights
-    double cum = w;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double up = __shfl_up(cum, d);
-        if (lane >= d) cum += up;
-    }
+    double cum = wave_scan(w);
     // the softmax sum over the whole vocabulary, relative to the top
     double sum = 0.0;
-    for (int s = tid; s < slices; s += JT)
+    for (int s = tid; s < slices; s += THREADS)
         if (parts[s].top > NEG_INF)
             sum += parts[s].sum * exp(below_top(parts[s].top, top) / (double)warm);
     sum = wave_sum(sum);
-    __syncthreads();
-    if (lane == 63) wave_d[wave] = cum;
-    if (lane == 0) scan[wave] = sum;
-    __syncthreads();
-    double all = 0.0, before = 0.0;
-    sum = 0.0;
-#pragma unroll
-    for (int x = 0; x < WAVES; ++x) {
-        if (x == wave) before = all;
-        all += wave_d[x];
-        sum += scan[x];
+    if (lane == 63) {
+        wave_d[0][wave] = cum;
+        wave_d[1][wave] = sum;
     }
-    cum += before;
-    const double top_p = a.top_p ? (double)a.top_p[row] : 1.0;
-    const double min_p = a.min_p ? (double)a.min_p[row] : 0.0;
+    __syncthreads();
+    const int other = lane & (WAVES - 1);
+    const double there_sum = lane < WAVES ? wave_d[0][other] : 0.0;
+    const double all = wave_sum(there_sum);
+    cum += wave_sum(lane < wave ? there_sum : 0.0);
+    sum = wave_sum(lane < WAVES ? wave_d[1][other] : 0.0);
+    // how many candidates there are, how many come before the sum reaches
+    // top_p of all, and how many have enough weight
     const int in_k = __popcll(__ballot(there));
     const int in_p = __popcll(__ballot(there && cum < top_p * all));
     const int in_m = __popcll(__ballot(there && w >= min_p));
-    __syncthreads();
-    scan[tid] = cum;
     if (lane == 0) {
         wave_i[0][wave] = in_k;
         wave_i[1][wave] = in_p;
         wave_i[2][wave] = in_m;
     }
     __syncthreads();
-    int count = 0, short_n = 1, large_n = 0;
-#pragma unroll
-    for (int x = 0; x < WAVES; ++x) {
-        count += wave_i[0][x];
-        short_n += wave_i[1][x];
-        large_n += wave_i[2][x];
-    }
+    const int count = wave_sum(lane < WAVES ? wave_i[0][other] : 0);
+    const int short_n = wave_sum(lane < WAVES ? wave_i[1][other] : 0) + 1;
+    const int large_n = wave_sum(lane < WAVES ? wave_i[2][other] : 0);
     const int keep = max(1, min(min(short_n, large_n), count));
-    const double bound = (double)a.uniform[row] * scan[keep - 1];
-    const int passed = __popcll(__ballot(tid < keep && cum <= bound));
-    if (lane == 0) wave_i[3][wave] = passed;
+    if (tid == keep - 1) kept = cum;
     __syncthreads();
-    int j = 0;
-#pragma unroll
-    for (int x = 0; x < WAVES; ++x) j += wave_i[3][x];
+    const int passed = __popcll(__ballot(tid < keep && cum <= uniform * kept));
+    if (lane == 0) wave_i[0][wave] = passed;
+    __syncthreads();
+    int j = wave_sum(lane < WAVES ? wave_i[0][other] : 0);
     j = t > 0.0f ? min(j, keep - 1) : 0;
     if (tid == j) {
         a.ids[row] = (int32_t)~(uint32_t)mine;
@@ -517,8 +532,8 @@ size_t parts_bytes(int64_t rows, int slices) {
 
 template <typename T, int THREADS, int VALUES, int GROUP>
 void run_slices(const PickArgs &a, int slices, Part *parts, uint64_t *found, hipStream_t stream) {
-    slice_kernel<T, THREADS, VALUES, GROUP>
-        <<<(unsigned)(a.rows * slices), THREADS, 0, stream>>>(a, slices, parts, found);
+    const dim3 grid((unsigned)a.rows, (unsigned)slices);
+    slice_kernel<T, THREADS, VALUES, GROUP><<<grid, THREADS, 0, stream>>>(a, parts, found);
 }
 
 template <typename T>
@@ -537,7 +552,11 @@ void run(const PickArgs &a, hipStream_t stream) {
         if (a.max_top_k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 1>(a, slices, parts, found, stream);
     }
-    join_kernel<<<(unsigned)a.rows, JT, 0, stream>>>(a, slices, parts, found);
+    // A join of four waves where they hold all candidates.
+    if (a.max_top_k <= 256 && slices * ((slice_cap(a.max_top_k) + 63) / 64) <= 4 * JOIN_HELD)
+        join_kernel<256><<<(unsigned)a.rows, 256, 0, stream>>>(a, slices, parts, found);
+    else
+        join_kernel<1024><<<(unsigned)a.rows, 1024, 0, stream>>>(a, slices, parts, found);
 }
 
 }  // namespace

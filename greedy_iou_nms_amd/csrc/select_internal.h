@@ -48,17 +48,66 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+// One step of a reduction over the wave in DPP moves: every lane combines
+// with a lane before it, in six steps lane 63 has combined with all.  `none`
+// is the value that changes nothing.
+#define GNMS_DPP_STEPS(STEP) STEP(0x111, 0xf) STEP(0x112, 0xf) STEP(0x114, 0xf) \
+    STEP(0x118, 0xf) STEP(0x142, 0xa) STEP(0x143, 0xc)
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int none, int v) {
+    return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xf, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float none, float v) {
+    return __uint_as_float(dpp<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double none, double v) {
+    const uint64_t n = (uint64_t)__double_as_longlong(none), x = (uint64_t)__double_as_longlong(v);
+    const uint64_t lo = dpp<CTRL, ROWS>((uint32_t)n, (uint32_t)x);
+    const uint64_t hi = dpp<CTRL, ROWS>((uint32_t)(n >> 32), (uint32_t)(x >> 32));
+    return __longlong_as_double((long long)(hi << 32 | lo));
+}
+
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+__device__ __forceinline__ float last_lane(float v) {
+    return __uint_as_float(last_lane(__float_as_uint(v)));
+}
+__device__ __forceinline__ double last_lane(double v) {
+    const uint64_t x = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)last_lane((uint32_t)(x >> 32)) << 32 |
+                                            last_lane((uint32_t)x)));
+}
+
+// Inclusive sums over the lanes.
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v) {
+#define GNMS_STEP(CTRL, ROWS) v += dpp<CTRL, ROWS>((V)0, v);
+    GNMS_DPP_STEPS(GNMS_STEP)
+#undef GNMS_STEP
     return v;
 }
 
+// The reductions' results are the same in every lane.
+template <typename V>
+__device__ __forceinline__ V wave_sum(V v) { return last_lane(wave_scan(v)); }
+
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+#define GNMS_STEP(CTRL, ROWS) v = fmaxf(v, dpp<CTRL, ROWS>(NEG_INF, v));
+    GNMS_DPP_STEPS(GNMS_STEP)
+#undef GNMS_STEP
+    return last_lane(v);
 }
 
 // ----------------------------------------------------------------- launches
