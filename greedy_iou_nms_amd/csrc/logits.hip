@@ -14,10 +14,11 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
     const int64_t row = blockIdx.x;
     const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
-    const RowRules r = row_rules(a.rules, row);
+    const EarlyHistory early = early_history<THREADS>(a.rules, row);
+    const RowRules r = row_rules(a.rules, row, readable(a.logits));
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + lo;
-    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, word);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word);
     for (int at = 8 * threadIdx.x; at < size; at += 8 * THREADS) {
         float z[8];
         adjusted8<T, SLICE>(a.rules, r, row, lo, size, at, in, load8(in + at, size - at), word, z);

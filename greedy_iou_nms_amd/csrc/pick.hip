@@ -23,11 +23,16 @@ constexpr int JOIN_BINS = 1024;   // of the join's
 constexpr int JOIN_HELD = 12;     // pieces of 64 candidates that a wave of it holds
 constexpr int CROWDED = 64;       // most candidates of a bin that it ranks one by one
 
+// What a slice says about itself.  edge[i]: at least max_top_k / 2^i (rounded
+// up) of its values are not below; -infinity if it has fewer.
+constexpr int EDGES = 4;
 struct Part {
     float top;       // the slice's largest value
-    float edge;      // no candidate of the slice is below
     uint32_t count;  // candidates written
     double sum;      // of exp((value - top) / temperature)
+    float edge[EDGES];
+    float least;     // no candidate is below
+    float pad;
 };
 
 // Candidates a slice may write: more than max_top_k, because the bound that
@@ -41,10 +46,7 @@ __device__ __forceinline__ uint64_t candidate(float z, int token) {
 
 // The temperature of the softmax: greedy rows (0, or anything not above it)
 // use 1.
-__device__ __forceinline__ float warmth(const float *temperature, int64_t row) {
-    const float t = temperature ? temperature[row] : 1.0f;
-    return t > 0.0f ? t : 1.0f;
-}
+__device__ __forceinline__ float warmth(float t) { return t > 0.0f ? t : 1.0f; }
 
 // z - top, with the limit 0 at z = top = +infinity.
 __device__ __forceinline__ double below_top(float z, float top) {
@@ -75,36 +77,36 @@ struct Bins {
     }
 };
 
-// The highest bin at or above which there are at least `need` entries, and
-// -1 if there are fewer in all.  One wave; hist has 64 * PER bins.
+// A wave's view of a histogram of 64 * PER bins from the top.
 template <int PER>
-__device__ __forceinline__ int bin_of_rank(const uint32_t *hist, uint32_t need) {
-    const int lane = threadIdx.x & 63;
-    uint32_t c[PER], s = 0;
+struct Ranks {
+    uint32_t c[PER], s, above;
+    __device__ __forceinline__ explicit Ranks(const uint32_t *hist) : s(0) {
+        const int lane = threadIdx.x & 63;
+        // lane 0 has the highest bins
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        c[i] = hist[lane * PER + i];
-        s += c[i];
+        for (int i = 0; i < PER; ++i) {
+            c[i] = hist[64 * PER - 1 - lane * PER - i];
+            s += c[i];
+        }
+        above = wave_scan(s);
     }
-    // entries in this lane's bins and above: an inclusive sum from the top
-    uint32_t above = s;
+    // The highest bin at or above which there are at least `need` entries,
+    // and -1 if there are fewer in all.
+    __device__ __forceinline__ int bin(uint32_t need) const {
+        const int lane = threadIdx.x & 63;
+        const uint64_t enough = __ballot(above >= need);
+        if (enough == 0ull) return -1;
+        int at = -1;
+        uint32_t sum = above - s;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t v = __shfl_down(above, d);
-        if (lane + d < 64) above += v;
+        for (int i = 0; i < PER; ++i) {
+            sum += c[i];
+            if (at < 0 && sum >= need) at = 64 * PER - 1 - lane * PER - i;
+        }
+        return __builtin_amdgcn_readlane(at, __builtin_ctzll(enough));
     }
-    const uint64_t enough = __ballot(above >= need);
-    if (enough == 0ull) return -1;
-    const int at = 63 - __builtin_clzll(enough);
-    int bin = -1;
-    uint32_t sum = above - s;
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i) {
-        sum += c[i];
-        if (bin < 0 && sum >= need) bin = lane * PER + i;
-    }
-    return __shfl(bin, at);
-}
+};
 
 // One digit of a k-th largest word: chosen[0] is the digit of the word that
 // is `left`-th largest among those counted in hist[0..256), chosen[1] its rank
@@ -112,7 +114,7 @@ __device__ __forceinline__ int bin_of_rank(const uint32_t *hist, uint32_t need) 
 __device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t left,
                                               uint32_t *chosen) {
     const int lane = threadIdx.x & 63;
-    const int d = bin_of_rank<4>(hist, left);
+    const int d = Ranks<4>(hist).bin(left);
     uint32_t over = 0;
     for (int i = d + 1 + lane; i < 256; i += 64) over += hist[i];
     over = wave_sum(over);
@@ -135,14 +137,16 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
     __shared__ uint32_t hist[BINS];
     __shared__ float wave_top[WAVES], wave_low[WAVES], wave_sums[WAVES];
     __shared__ uint32_t taken, chosen[2];
-    __shared__ float bound;
+    __shared__ float bound[EDGES];
     const int tid = threadIdx.x, wave = tid >> 6;
     const int64_t row = blockIdx.x;
     const int64_t part = row * gridDim.y + blockIdx.y;
     const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
-    const RowRules r = row_rules(a.rules, row);
-    const float c = fminf(1.4426950408889634f / warmth(a.temperature, row), 3.0e38f);
+    const EarlyHistory early = early_history<THREADS>(a.rules, row);
+    const RowRules r = row_rules(a.rules, row, a.uniform);
+    const float warm = warmth(parameter(a.temperature, row, 1.0f, a.uniform));
+    const float c = fminf(1.4426950408889634f / warm, 3.0e38f);
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     Eight<T> logits[VALUES / 8];  // in flight while the rules are gathered
 #pragma unroll
@@ -152,7 +156,7 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
     }
     for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) taken = 0;
-    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, word);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word);
     float z[VALUES];
 #pragma unroll
     for (int g = 0; g < VALUES / 8; ++g) {
@@ -202,12 +206,18 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
         if (m[g] > NEG_INF) atomicAdd(&hist[bins.of(m[g], BINS)], 1u);
     __syncthreads();
     if (wave == 0) {
-        const int b = bin_of_rank<BINS / 64>(hist, (uint32_t)k);
-        if (tid == 0) bound = bins.edge(b);
+        const Ranks<BINS / 64> ranks(hist);
+#pragma unroll
+        for (int i = 0; i < EDGES; ++i) {
+            const int b = ranks.bin((uint32_t)(k + (1 << i) - 1) >> i);
+            if (tid == 0) bound[i] = b < 0 ? NEG_INF : bins.edge(b);
+        }
     }
     __syncthreads();
-    // at least k values (or all there are) lie at the bound or above
-    float edge = bound;
+    // at least k values lie at the bound or above; without one, all values
+    // are candidates
+    const float first = bound[0];
+    float edge = fmaxf(first, -3.402823466e38f);
     uint32_t hits = 0;
 #pragma unroll
     for (int j = 0; j < VALUES; ++j) hits |= z[j] >= edge ? 1u << j : 0u;
@@ -228,7 +238,18 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
         if (to < (uint32_t)cap) found[to] = own(j);
         ++to;
     }
+    if (first == NEG_INF) {
+        // the smallest of them, which the join's bins begin at
+        float low = __builtin_inff();
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j)
+            if (z[j] > NEG_INF) low = fminf(low, z[j]);
+        low = -wave_max(-low);
+        if ((tid & 63) == 0) wave_low[wave] = low;
+    }
     __syncthreads();
+    if (first == NEG_INF)
+        edge = -wave_max((tid & 63) < WAVES ? -wave_low[tid & (WAVES - 1)] : NEG_INF);
     if (taken > (uint32_t)cap) {
         // Equal values, or a spread that the bins do not resolve: the k-th
         // largest word, digit by digit from the top, and exactly k of them.
@@ -265,7 +286,8 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
             all = (double)wave_sums[tid & (WAVES - 1)] *
                   (wt == top ? 1.0 : (double)__builtin_amdgcn_exp2f((wt - top) * c));
         all = wave_sum(all);
-        if (tid == 0) parts[part] = Part{top, edge, taken, all};
+        if (tid == 0)
+            parts[part] = Part{top, taken, all, {first, bound[1], bound[2], bound[3]}, edge, 0.0f};
     }
 }
 
@@ -295,22 +317,22 @@ __device__ __forceinline__ uint64_t sort_words(uint64_t v, int n, uint64_t *lds)
 }
 
 template <int THREADS>
-__global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, const Part *parts,
-                                                       const uint64_t *found) {
+__global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, uint32_t inverse,
+                                                       const Part *parts, const uint64_t *found) {
     constexpr int WAVES = THREADS / 64;
     constexpr int HELD = JOIN_HELD;
     constexpr int PER = JOIN_BINS / THREADS;  // bins per thread
     constexpr int LIST = THREADS + CROWDED;
     __shared__ uint64_t list[LIST], sorted[THREADS];
     __shared__ uint32_t hist[JOIN_BINS], fill[JOIN_BINS];
-    __shared__ double wave_d[2][WAVES];
-    __shared__ float wave_f[3][WAVES];
+    __shared__ double wave_d[WAVES];
     __shared__ uint32_t wave_u[WAVES];
     __shared__ int wave_i[3][WAVES];
     __shared__ uint32_t taken, crowded, inside, chosen[2];
     __shared__ double kept;
     const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kmax = a.max_top_k, cap = slice_cap(kmax);
     parts += row * slices;
     found += row * slices * cap;
@@ -321,7 +343,8 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, c
     const int pieces = (cap + 63) / 64, total = slices * pieces;
     auto load = [&](int p) -> uint64_t {
         if (p >= total) return 0;
-        const int s = p / pieces, i = (p - s * pieces) * 64 + lane;
+        // p / pieces: exact for p < 2^21 and pieces < 2^6
+        const int s = inverse == 0u ? p : (int)__umulhi((uint32_t)p, inverse), i = (p - s * pieces) * 64 + lane;
         const uint32_t count = parts[s].count;
         const uint64_t w = i < cap ? found[(int64_t)s * cap + i] : 0ull;
         return (uint32_t)i < count ? w : 0ull;
@@ -337,28 +360,40 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, c
         for (int p = HELD * WAVES + wave; p < total; p += WAVES) f(load(p));
     };
     // the row's parameters, in flight with the candidates
-    const float t = a.temperature ? a.temperature[row] : 1.0f;
-    const float warm = t > 0.0f ? t : 1.0f;
-    const double top_p = a.top_p ? (double)a.top_p[row] : 1.0;
-    const double min_p = a.min_p ? (double)a.min_p[row] : 0.0;
+    const float t = parameter(a.temperature, row, 1.0f, a.uniform);
+    const float warm = warmth(t);
+    const double top_p = (double)parameter(a.top_p, row, 1.0f, a.uniform);
+    const double min_p = (double)parameter(a.min_p, row, 0.0f, a.uniform);
     const double uniform = (double)a.uniform[row];
-    const int k = min(max(a.top_k ? a.top_k[row] : kmax, 1), kmax);
-    // The row's largest value; a bound that its max_top_k-th value is not
-    // below (any slice's with so many candidates), or one below them all.
-    float top = NEG_INF, edge = NEG_INF, least = __builtin_inff();
-    for (int s = tid; s < slices; s += THREADS) {
-        const Part x = parts[s];
-        top = fmaxf(top, x.top);
-        if (x.count >= (uint32_t)kmax) edge = fmaxf(edge, x.edge);
-        if (x.count > 0) least = fminf(least, x.edge);
+    const int k = min(max(parameter(a.top_k, row, kmax, a.uniform), 1), kmax);
+    // Every wave reads all slices' parts: the row's largest value and its
+    // softmax sum, and a bound that its kmax-th value is not below, or failing
+    // that one that no candidate is below.  2^i slices with kmax / 2^i values
+    // each at a bound or above make a bound, so it is the 2^i-th largest of the
+    // slices' edge[i]: with eight slices of like values their eighth lets
+    // about kmax candidates through where one slice's own kmax-th would let
+    // eight times as many.
+    const bool have = lane < slices;
+    Part x = have ? parts[lane] : Part{NEG_INF, 0, 0.0, {NEG_INF, NEG_INF, NEG_INF, NEG_INF},
+                                       __builtin_inff(), 0.0f};
+    float top = x.top, least = x.count > 0 ? x.least : __builtin_inff(), best = x.edge[0];
+    for (int s = 64 + lane; s < slices; s += 64) {
+        top = fmaxf(top, parts[s].top);
+        if (parts[s].count > 0) least = fminf(least, parts[s].least);
+        best = fmaxf(best, parts[s].edge[0]);
     }
     top = wave_max(top);
-    edge = wave_max(edge);
     least = -wave_max(-least);
-    if (lane == 0) {
-        wave_f[0][wave] = top;
-        wave_f[1][wave] = edge;
-        wave_f[2][wave] = least;
+    float edge = wave_max(best);
+    if (slices > 1) {
+        const int level = slices >= 8 ? 3 : slices >= 4 ? 2 : 1;
+        float e = level == 3 ? x.edge[3] : level == 2 ? x.edge[2] : x.edge[1];
+        float m = NEG_INF;
+        for (int i = 0; i < 1 << level; ++i) {
+            m = wave_max(e);
+            if (lane == __builtin_ctzll(__ballot(e == m))) e = NEG_INF;
+        }
+        edge = fmaxf(edge, m);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -372,9 +407,6 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, c
     sorted[tid] = 0;
     for (int i = tid; i < LIST; i += THREADS) list[i] = 0;
     __syncthreads();
-    top = wave_max(lane < WAVES ? wave_f[0][lane & (WAVES - 1)] : NEG_INF);
-    edge = wave_max(lane < WAVES ? wave_f[1][lane & (WAVES - 1)] : NEG_INF);
-    least = -wave_max(lane < WAVES ? -wave_f[2][lane & (WAVES - 1)] : NEG_INF);
     if (!(top > NEG_INF)) {
         if (tid == 0) {
             a.ids[row] = -1;
@@ -468,49 +500,55 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, c
         mine = sort_words(mine, p, list);
     }
 
-    const bool there = tid < k && mine != 0;
-    const float z = key_value((uint32_t)(mine >> 32));
-    const double w = there ? exp(below_top(z, top) / (double)warm) : 0.0;
-    // running sums of the candidates' weights
-    double cum = wave_scan(w);
     // the softmax sum over the whole vocabulary, relative to the top
-    double sum = 0.0;
-    for (int s = tid; s < slices; s += THREADS)
+    double sum = x.top > NEG_INF ? x.sum * exp(below_top(x.top, top) / (double)warm) : 0.0;
+    for (int s = 64 + lane; s < slices; s += 64)
         if (parts[s].top > NEG_INF)
             sum += parts[s].sum * exp(below_top(parts[s].top, top) / (double)warm);
     sum = wave_sum(sum);
-    if (lane == 63) {
-        wave_d[0][wave] = cum;
-        wave_d[1][wave] = sum;
-    }
-    __syncthreads();
-    const int other = lane & (WAVES - 1);
-    const double there_sum = lane < WAVES ? wave_d[0][other] : 0.0;
-    const double all = wave_sum(there_sum);
-    cum += wave_sum(lane < wave ? there_sum : 0.0);
-    sum = wave_sum(lane < WAVES ? wave_d[1][other] : 0.0);
-    // how many candidates there are, how many come before the sum reaches
-    // top_p of all, and how many have enough weight
+    const bool there = tid < k && mine != 0;
+    const float z = key_value((uint32_t)(mine >> 32));
+    const double w = there ? exp(below_top(z, top) / (double)warm) : 0.0;
+    // Running sums of the candidates' weights; how many candidates there are,
+    // how many come before the sum reaches top_p of all, and how many have
+    // enough weight.
+    double cum = wave_scan(w), all = last_lane(cum);
     const int in_k = __popcll(__ballot(there));
-    const int in_p = __popcll(__ballot(there && cum < top_p * all));
     const int in_m = __popcll(__ballot(there && w >= min_p));
-    if (lane == 0) {
-        wave_i[0][wave] = in_k;
-        wave_i[1][wave] = in_p;
-        wave_i[2][wave] = in_m;
+    int j;
+    if (kmax <= 64) {
+        // they are all in the first wave
+        if (wave != 0) return;
+        const int in_p = __popcll(__ballot(there && cum < top_p * all));
+        const int keep = max(1, min(min(in_p + 1, in_m), in_k));
+        const double bound = uniform * __shfl(cum, keep - 1);
+        j = min(__popcll(__ballot(lane < keep && cum <= bound)), keep - 1);
+    } else {
+        const int other = lane & (WAVES - 1);
+        if (lane == 0) {
+            wave_d[wave] = all;
+            wave_i[0][wave] = in_k;
+            wave_i[1][wave] = in_m;
+        }
+        __syncthreads();
+        const double part = lane < WAVES ? wave_d[other] : 0.0;
+        all = wave_sum(part);
+        cum += wave_sum(lane < wave ? part : 0.0);
+        const int in_p = __popcll(__ballot(there && cum < top_p * all));
+        if (lane == 0) wave_i[2][wave] = in_p;
+        __syncthreads();
+        const int count = wave_sum(lane < WAVES ? wave_i[0][other] : 0);
+        const int large_n = wave_sum(lane < WAVES ? wave_i[1][other] : 0);
+        const int short_n = wave_sum(lane < WAVES ? wave_i[2][other] : 0) + 1;
+        const int keep = max(1, min(min(short_n, large_n), count));
+        if (tid == keep - 1) kept = cum;
+        __syncthreads();
+        const int passed = __popcll(__ballot(tid < keep && cum <= uniform * kept));
+        if (lane == 0) wave_i[0][wave] = passed;
+        __syncthreads();
+        j = min(wave_sum(lane < WAVES ? wave_i[0][other] : 0), keep - 1);
     }
-    __syncthreads();
-    const int count = wave_sum(lane < WAVES ? wave_i[0][other] : 0);
-    const int short_n = wave_sum(lane < WAVES ? wave_i[1][other] : 0) + 1;
-    const int large_n = wave_sum(lane < WAVES ? wave_i[2][other] : 0);
-    const int keep = max(1, min(min(short_n, large_n), count));
-    if (tid == keep - 1) kept = cum;
-    __syncthreads();
-    const int passed = __popcll(__ballot(tid < keep && cum <= uniform * kept));
-    if (lane == 0) wave_i[0][wave] = passed;
-    __syncthreads();
-    int j = wave_sum(lane < WAVES ? wave_i[0][other] : 0);
-    j = t > 0.0f ? min(j, keep - 1) : 0;
+    if (!(t > 0.0f)) j = 0;
     if (tid == j) {
         a.ids[row] = (int32_t)~(uint32_t)mine;
         a.logprobs[row] = (float)(below_top(z, top) / (double)warm - log(sum));
@@ -552,11 +590,13 @@ void run(const PickArgs &a, hipStream_t stream) {
         if (a.max_top_k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 1>(a, slices, parts, found, stream);
     }
-    // A join of four waves where they hold all candidates.
-    if (a.max_top_k <= 256 && slices * ((slice_cap(a.max_top_k) + 63) / 64) <= 4 * JOIN_HELD)
-        join_kernel<256><<<(unsigned)a.rows, 256, 0, stream>>>(a, slices, parts, found);
+    const int pieces = (slice_cap(a.max_top_k) + 63) / 64;
+    const uint32_t inverse = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
+    // a join of four waves where they hold all candidates
+    if (a.max_top_k <= 256 && slices * pieces <= 4 * JOIN_HELD)
+        join_kernel<256><<<(unsigned)a.rows, 256, 0, stream>>>(a, slices, inverse, parts, found);
     else
-        join_kernel<1024><<<(unsigned)a.rows, 1024, 0, stream>>>(a, slices, parts, found);
+        join_kernel<1024><<<(unsigned)a.rows, 1024, 0, stream>>>(a, slices, inverse, parts, found);
 }
 
 }  // namespace
