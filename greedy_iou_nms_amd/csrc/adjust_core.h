@@ -2,35 +2,33 @@
 // nms_pick_tokens.
 //
 // One word of LDS per token of the slice gathers what the history and the
-// bias list say about it: the place of its last bias entry (11 bits, stored
-// as 2047 - place so that no entry reads as all ones), a bit for "seen in the
-// prompt" and 20 bits of "how often generated".  Then every thread looks at
-// the words of its own tokens, eight neighbours at a time, and replaces each
-// touched word by the token's adjusted value: as many rounds as the wave's
-// fullest lane has touched tokens, not eight times the division and the four
-// operations behind it.  An untouched word is a NaN that no adjusted value
-// is, so that a token then costs one compare and one select.
+// bias list say about it: how often it was generated (20 bits), whether it was
+// seen in the prompt, and the place of its last bias entry plus one (11 bits);
+// one bit per token says whether there is anything.  Then every thread looks
+// through the bits of its own tokens, replaces the words of those touched by
+// their adjusted values, and selects between these and the logits.  That is
+// as many rounds as the wave's fullest lane has touched tokens, where
+// adjusting in line costs every token of a wave with one touched token the
+// division and the four operations behind it.
 #pragma once
 
 #include "select_internal.h"
 
 namespace gnms {
 
-constexpr int RULE_BIAS_SHIFT = 21;
+constexpr uint32_t RULE_COUNT = (1u << 20) - 1u;
 constexpr uint32_t RULE_SEEN = 1u << 20;
-constexpr uint32_t RULE_COUNT = RULE_SEEN - 1u;
 constexpr uint32_t RULE_TOUCHED = RULE_SEEN | RULE_COUNT;  // by the history
-constexpr uint32_t RULE_NO_BIAS = 2047u;
-constexpr uint32_t UNTOUCHED = RULE_NO_BIAS << RULE_BIAS_SHIFT;  // a NaN
+constexpr int RULE_BIAS_SHIFT = 21;
 static_assert(NMS_MAX_HISTORY == RULE_COUNT, "a count fits its field");
-static_assert(NMS_MAX_BIASES <= (int)RULE_NO_BIAS, "a place fits its field");
+static_assert(NMS_MAX_BIASES < (1 << (32 - RULE_BIAS_SHIFT)), "a place fits its field");
 
 // What one row's rules are, read once per workgroup.
 struct RowRules {
     float repetition, presence, frequency;
     int length, prompt;        // of the history, both within its capacity
-    const uint8_t *allowed;    // the row's mask, a byte per 8 tokens; null: none
-    bool none_allowed;         // the row names a mask that does not exist
+    bool masked;               // the row has a mask,
+    const uint8_t *allowed;    // a byte per 8 tokens; null: no token is allowed
     bool words;                // the history or the bias list has entries
 };
 
@@ -61,8 +59,8 @@ __device__ __forceinline__ RowRules row_rules(const nms_logit_rules &u, int64_t 
     const int64_t at = parameter(u.allowed_rows, row, (int)row, any);
     r.length = min(max(length, 0), (int)u.history_capacity);
     r.prompt = min(max(prompt, 0), r.length);
-    r.none_allowed = u.allowed && at >= u.allowed_count;
-    r.allowed = u.allowed && at >= 0 && !r.none_allowed
+    r.masked = u.allowed && at >= 0;
+    r.allowed = r.masked && at < u.allowed_count
                     ? reinterpret_cast<const uint8_t *>(u.allowed + at * u.allowed_stride)
                     : nullptr;
     r.words = r.length > 0 || u.bias_count > 0;
@@ -99,37 +97,42 @@ __device__ __forceinline__ unsigned slot(unsigned at) {
 
 // The adjusted value of a touched token, but for its mask.  Every operation
 // is one binary32 operation (compiled without contraction).
-__device__ __forceinline__ uint32_t replaced(const nms_logit_rules &u, const RowRules &r,
-                                             int64_t row, float z, uint32_t word) {
+__device__ __forceinline__ float replaced(const nms_logit_rules &u, const RowRules &r, int64_t row,
+                                          float z, uint32_t word) {
     if (word & RULE_TOUCHED) z = z > 0.0f ? z / r.repetition : z * r.repetition;
     const uint32_t count = word & RULE_COUNT;
     if (count > 0u) {
         z = z - r.frequency * (float)count;
         z = z - r.presence;
     }
-    const uint32_t place = RULE_NO_BIAS - (word >> RULE_BIAS_SHIFT);
+    const uint32_t place = word >> RULE_BIAS_SHIFT;
     if (place > 0u) z = z + u.bias_values[row * u.bias_stride + place - 1];
-    // one NaN for all, which is not UNTOUCHED
-    return z != z ? 0x7fc00000u : __float_as_uint(z);
+    return z;
 }
 
-// Gathers the rules of the tokens lo..lo+size-1 of the row in word[0..SLICE).
-// Every thread of the workgroup calls it, and it ends with a barrier.
+// Gathers the rules of the tokens lo..lo+size-1 of the row in word[0..SLICE)
+// and bit[0..SLICE / 32).  Every thread of the workgroup calls it, and it ends
+// with a barrier.
 template <int THREADS, int SLICE>
 __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowRules &r,
                                             int64_t row, int lo, int size,
-                                            const EarlyHistory &early, uint32_t *word) {
+                                            const EarlyHistory &early, uint32_t *word,
+                                            uint32_t *bit) {
     const int tid = threadIdx.x;
-    const uint4 none = make_uint4(UNTOUCHED, UNTOUCHED, UNTOUCHED, UNTOUCHED);
-    for (int i = tid; i < SLICE / 4; i += THREADS) reinterpret_cast<uint4 *>(word)[i] = none;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < SLICE / 4 / THREADS; ++i)
+        reinterpret_cast<uint4 *>(word)[i * THREADS + tid] = none;
+    if (tid < SLICE / 32) bit[tid] = 0;
     __syncthreads();
     if (u.bias_count > 0) {
         const int32_t *ids = u.bias_ids + row * u.bias_stride;
         for (int i = tid; i < (int)u.bias_count; i += THREADS) {
             const unsigned at = (unsigned)ids[i] - (unsigned)lo;
-            if (at < (unsigned)size)
-                atomicMin(&word[slot<SLICE>(at)], (RULE_NO_BIAS - (uint32_t)(i + 1))
-                                                      << RULE_BIAS_SHIFT);
+            if (at < (unsigned)size) {
+                atomicMax(&word[slot<SLICE>(at)], (uint32_t)(i + 1) << RULE_BIAS_SHIFT);
+                atomicOr(&bit[at >> 5], 1u << (at & 31u));
+            }
         }
         __syncthreads();
     }
@@ -139,6 +142,7 @@ __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowR
             uint32_t *w = &word[slot<SLICE>(at)];
             if (i < r.prompt) atomicOr(w, RULE_SEEN);
             else atomicAdd(w, 1u);
+            atomicOr(&bit[at >> 5], 1u << (at & 31u));
         }
     };
 #pragma unroll
@@ -175,47 +179,72 @@ __device__ __forceinline__ Eight<T> load8(const T *p, int left) {
     return e;
 }
 
-// The adjusted values of the eight tokens at..at+7 of the slice (at a
-// multiple of 8) from their logits, which start at in; those past the slice
-// are -infinity.
-template <typename T, int SLICE>
-__device__ __forceinline__ void adjusted8(const nms_logit_rules &u, const RowRules &r, int64_t row,
-                                          int lo, int size, int at, const T *in,
-                                          const Eight<T> &logits, uint32_t *word, float *z) {
+// A thread's VALUES tokens of the slice, in groups of eight neighbours: value
+// j is the slice's token at(j).
+template <int THREADS>
+__device__ __forceinline__ int token_at(int j) {
+    return 8 * ((j >> 3) * THREADS + (int)threadIdx.x) + (j & 7);
+}
+
+// What a thread reads of its tokens, in flight while the rules are gathered.
+template <typename T, int THREADS, int VALUES>
+struct Raw {
+    Eight<T> logits[VALUES / 8];
+    uint32_t allowed[VALUES / 8];
+    __device__ __forceinline__ Raw(const RowRules &r, int lo, int size, const T *in) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = to_f32(logits.v[j]);
+        for (int g = 0; g < VALUES / 8; ++g) {
+            const int at = token_at<THREADS>(8 * g);
+            logits[g] = load8(in + at, size - at);
+            allowed[g] = r.allowed && at < size ? r.allowed[(lo + at) >> 3] : 0u;
+        }
+    }
+};
+
+// The adjusted values of the thread's tokens, whose logits start at in; those
+// past the slice are -infinity.
+template <typename T, int THREADS, int VALUES>
+__device__ __forceinline__ void adjusted(const nms_logit_rules &u, const RowRules &r, int64_t row,
+                                         const T *in, const Raw<T, THREADS, VALUES> &raw,
+                                         uint32_t *word, const uint32_t *bit, float *z) {
+    constexpr int SLICE = THREADS * VALUES;
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw.logits[j / 8].v[j % 8]);
+    // m is -1 or 0: a or b
+    auto select = [](int m, float a, float b) {
+        return __uint_as_float((__float_as_uint(a) & (uint32_t)m) |
+                               (__float_as_uint(b) & ~(uint32_t)m));
+    };
+    auto bit_of = [](uint32_t bits, int j) { return (int)(bits << (31 - j)) >> 31; };
     if (r.words) {
-        uint32_t w[8];
-        uint4 *w0 = reinterpret_cast<uint4 *>(word + at / 2);
-        uint4 *w1 = reinterpret_cast<uint4 *>(word + SLICE / 2 + at / 2);
-        __builtin_memcpy(w, w0, 16);
-        __builtin_memcpy(w + 4, w1, 16);
         uint32_t touched = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) touched |= w[j] == UNTOUCHED ? 0u : 1u << j;
+        for (int g = 0; g < VALUES / 8; ++g)
+            touched |= (uint32_t)reinterpret_cast<const uint8_t *>(bit)[g * THREADS + tid]
+                       << (8 * g);
         if (touched != 0u) {
+            uint32_t left = touched;
             do {
-                const int j = __builtin_ctz(touched);
-                touched &= touched - 1u;
-                uint32_t *x = word + (j >> 2) * (SLICE / 2) + at / 2 + (j & 3);
-                *x = replaced(u, r, row, to_f32(in[at + j]), *x);
-            } while (touched != 0u);
-            __builtin_memcpy(w, w0, 16);
-            __builtin_memcpy(w + 4, w1, 16);
-        }
+                const int j = __builtin_ctz(left), at = token_at<THREADS>(j);
+                left &= left - 1u;
+                uint32_t *x = word + slot<SLICE>((unsigned)at);
+                *x = __float_as_uint(replaced(u, r, row, to_f32(in[at]), *x));
+            } while (left != 0u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = w[j] == UNTOUCHED ? z[j] : __uint_as_float(w[j]);
+            for (int q = 0; q < VALUES / 4; ++q) {
+                float w[4];
+                __builtin_memcpy(w, word + slot<SLICE>((unsigned)token_at<THREADS>(4 * q)), 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    z[4 * q + j] = select(bit_of(touched, 4 * q + j), w[j], z[4 * q + j]);
+            }
+        }
     }
-    if (r.allowed) {
-        const int bits = at < size ? r.allowed[(lo + at) >> 3] : 0;
+    if (r.masked) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t keep = (uint32_t)((int)((uint32_t)bits << (31 - j)) >> 31);
-            z[j] = __uint_as_float((__float_as_uint(z[j]) & keep) | (0xff800000u & ~keep));
-        }
-    } else if (r.none_allowed) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = NEG_INF;
+        for (int j = 0; j < VALUES; ++j)
+            z[j] = select(bit_of(raw.allowed[j / 8], j % 8), z[j], NEG_INF);
     }
 }
 

@@ -8,9 +8,10 @@
 namespace gnms {
 namespace {
 
-template <typename T, int THREADS, int SLICE>
-__global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
-    __shared__ uint32_t word[SLICE];
+template <typename T, int THREADS, int VALUES>
+__global__ __launch_bounds__(THREADS, 8) void adjust_kernel(AdjustArgs a) {
+    constexpr int SLICE = THREADS * VALUES;
+    __shared__ uint32_t word[SLICE], bit[SLICE / 32];
     const int64_t row = blockIdx.x;
     const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
@@ -18,33 +19,37 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
     const RowRules r = row_rules(a.rules, row, readable(a.logits));
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + lo;
-    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word);
-    for (int at = 8 * threadIdx.x; at < size; at += 8 * THREADS) {
-        float z[8];
-        adjusted8<T, SLICE>(a.rules, r, row, lo, size, at, in, load8(in + at, size - at), word, z);
+    const Raw<T, THREADS, VALUES> raw(r, lo, size, in);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word, bit);
+    float z[VALUES];
+    adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, word, bit, z);
+#pragma unroll
+    for (int g = 0; g < VALUES / 8; ++g) {
+        const int at = token_at<THREADS>(8 * g);
         if (size - at >= 8) {
             Eight<T> e;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) e.v[j] = from_f32<T>(z[j]);
+            for (int j = 0; j < 8; ++j) e.v[j] = from_f32<T>(z[8 * g + j]);
             __builtin_memcpy(out + at, &e, sizeof(e));
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (at + j < size) out[at + j] = from_f32<T>(z[j]);
+                if (at + j < size) out[at + j] = from_f32<T>(z[8 * g + j]);
         }
     }
 }
 
-template <typename T, int THREADS, int SLICE>
+template <typename T, int THREADS, int VALUES>
 void run(const AdjustArgs &a, hipStream_t stream) {
+    constexpr int SLICE = THREADS * VALUES;
     const dim3 grid((unsigned)a.rows, (unsigned)((a.vocab + SLICE - 1) / SLICE));
-    adjust_kernel<T, THREADS, SLICE><<<grid, THREADS, 0, stream>>>(a);
+    adjust_kernel<T, THREADS, VALUES><<<grid, THREADS, 0, stream>>>(a);
 }
 
 template <typename T>
 void choose(const AdjustArgs &a, hipStream_t stream) {
-    if (a.rows * ((a.vocab + 16383) / 16384) >= 256) run<T, 1024, 16384>(a, stream);
-    else run<T, 256, 2048>(a, stream);
+    if (a.rows * ((a.vocab + 16383) / 16384) >= 256) run<T, 1024, 16>(a, stream);
+    else run<T, 256, 8>(a, stream);
 }
 
 }  // namespace

@@ -59,7 +59,7 @@ struct Bins {
     float lo, scale;
     __device__ __forceinline__ Bins(float lo_, float hi, int bins) : lo(lo_) {
         const float width = hi - lo_;
-        scale = width > 0.0f ? (float)bins / width : 0.0f;
+        scale = width > 0.0f ? (float)bins * __builtin_amdgcn_rcpf(width) : 0.0f;
         if (!(scale < 3.0e38f)) scale = 3.0e38f;
     }
     __device__ __forceinline__ int of(float v, int bins) const {
@@ -134,8 +134,10 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
     constexpr int SLICE = THREADS * VALUES;
     constexpr int WAVES = THREADS / 64;
     __shared__ uint32_t word[SLICE];  // the rules, then the values
+    __shared__ uint32_t bit[SLICE / 32];
     __shared__ uint32_t hist[BINS];
-    __shared__ float wave_top[WAVES], wave_low[WAVES], wave_sums[WAVES];
+    __shared__ float wave_top[WAVES], wave_sums[WAVES];
+    __shared__ int highest, lowest;  // as ordered()
     __shared__ uint32_t taken, chosen[2];
     __shared__ float bound[EDGES];
     const int tid = threadIdx.x, wave = tid >> 6;
@@ -148,59 +150,74 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
     const float warm = warmth(parameter(a.temperature, row, 1.0f, a.uniform));
     const float c = fminf(1.4426950408889634f / warm, 3.0e38f);
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
-    Eight<T> logits[VALUES / 8];  // in flight while the rules are gathered
-#pragma unroll
-    for (int g = 0; g < VALUES / 8; ++g) {
-        const int at = 8 * (g * THREADS + tid);
-        logits[g] = load8(in + at, size - at);
-    }
+    const Raw<T, THREADS, VALUES> raw(r, lo, size, in);
     for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
-    if (tid == 0) taken = 0;
-    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word);
+    if (tid == 0) {
+        taken = 0;
+        highest = ordered(NEG_INF);
+        lowest = ordered(__builtin_inff());
+    }
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word, bit);
+    else __syncthreads();
     float z[VALUES];
+    adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, word, bit, z);
+    // The groups' largest values and the wave's, and the softmax sum relative
+    // to that: exp2(z c - top c), one multiply-add and one exponential a value,
+    // where the rounding of top c is a factor of all terms and is taken out of
+    // the sum.  A NaN, an infinite top, a c of 0 or a product of 2^24 and more
+    // show in the sum or in what is taken out; then the values are gone over
+    // again, with a NaN made -infinity and each difference taken by itself.
+    float m[VALUES / GROUP], top, sum;
+    for (bool again = false;; again = true) {
+        if (again) {
 #pragma unroll
-    for (int g = 0; g < VALUES / 8; ++g) {
-        const int at = 8 * (g * THREADS + tid);
-        adjusted8<T, SLICE>(a.rules, r, row, lo, size, at, in, logits[g], word, z + 8 * g);
-        // a copy that can be read by a number of its place
-        __builtin_memcpy(word + at / 2, z + 8 * g, 16);
-        __builtin_memcpy(word + SLICE / 2 + at / 2, z + 8 * g + 4, 16);
-    }
-    // v_max drops a NaN
-    float m[VALUES / GROUP], top = NEG_INF, least = __builtin_inff();
+            for (int j = 0; j < VALUES; ++j) z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
+        }
+        top = NEG_INF;
 #pragma unroll
-    for (int g = 0; g < VALUES / GROUP; ++g) {
-        m[g] = fmaxf(NEG_INF, z[g * GROUP]);
+        for (int g = 0; g < VALUES / GROUP; ++g) {
+            m[g] = z[g * GROUP];
 #pragma unroll
-        for (int j = 1; j < GROUP; ++j) m[g] = fmaxf(m[g], z[g * GROUP + j]);
-        top = fmaxf(top, m[g]);
-        if (m[g] > NEG_INF) least = fminf(least, m[g]);
-    }
-    top = wave_max(top);
-    least = -wave_max(-least);
-    // the softmax sum, relative to the wave's largest value
-    float sum = 0.0f;
-    if (top == __builtin_inff()) {
+            for (int j = 1; j < GROUP; ++j) m[g] = fmaxf(m[g], z[g * GROUP + j]);
+            top = fmaxf(top, m[g]);
+        }
+        top = wave_max(top);
+        sum = 0.0f;
+        if (!again) {
+            const float hi = top * c, rest = __builtin_fmaf(top, c, -hi);
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) sum += z[j] == top ? 1.0f : 0.0f;
-    } else if (top > NEG_INF) {
+            for (int j = 0; j < VALUES; ++j)
+                sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[j], c, -hi));
+            sum = wave_sum(sum) * __builtin_amdgcn_exp2f(-rest);
+            if (__builtin_amdgcn_readfirstlane(sum < 3.0e38f && fabsf(rest) <= 1.0f)) break;
+        } else {
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) {
-            const float e = __builtin_amdgcn_exp2f((z[j] - top) * c);
-            sum += z[j] > NEG_INF ? e : 0.0f;
+            for (int j = 0; j < VALUES; ++j)
+                if (z[j] > NEG_INF)
+                    sum += z[j] == top ? 1.0f : __builtin_amdgcn_exp2f((z[j] - top) * c);
+            sum = wave_sum(sum);
+            break;
         }
     }
-    sum = wave_sum(sum);
+#pragma unroll
+    for (int q = 0; q < VALUES / 4; ++q)
+        // a copy that can be read by a number of its place
+        __builtin_memcpy(word + slot<SLICE>((unsigned)token_at<THREADS>(4 * q)), z + 4 * q, 16);
+    int least = ordered(__builtin_inff());
+#pragma unroll
+    for (int g = 0; g < VALUES / GROUP; ++g)
+        if (m[g] > NEG_INF) least = min(least, ordered(m[g]));
+    least = wave_min(least);
     if ((tid & 63) == 0) {
         wave_top[wave] = top;
-        wave_low[wave] = least;
         wave_sums[wave] = sum;
+        atomicMax(&highest, ordered(top));
+        atomicMin(&lowest, least);
     }
     __syncthreads();
-    top = wave_max((tid & 63) < WAVES ? wave_top[tid & (WAVES - 1)] : NEG_INF);
-    least = -wave_max((tid & 63) < WAVES ? -wave_low[tid & (WAVES - 1)] : NEG_INF);
+    top = unordered(highest);
     const int k = a.max_top_k, cap = slice_cap(k);
-    const Bins bins(least, top, BINS);
+    const Bins bins(unordered(lowest), top, BINS);
 #pragma unroll
     for (int g = 0; g < VALUES / GROUP; ++g)
         if (m[g] > NEG_INF) atomicAdd(&hist[bins.of(m[g], BINS)], 1u);
@@ -212,15 +229,20 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
             const int b = ranks.bin((uint32_t)(k + (1 << i) - 1) >> i);
             if (tid == 0) bound[i] = b < 0 ? NEG_INF : bins.edge(b);
         }
+        if (tid == 0) lowest = ordered(__builtin_inff());
     }
     __syncthreads();
     // at least k values lie at the bound or above; without one, all values
     // are candidates
     const float first = bound[0];
-    float edge = fmaxf(first, -3.402823466e38f);
+    float edge = fminf(fmaxf(first, -3.402823466e38f), 3.402823466e38f);
+    if (edge == 0.0f) edge = -1.0e-38f;  // so that -0 is not below it
+    // bit j: z[j] >= edge, the sign of a difference that is no NaN
     uint32_t hits = 0;
 #pragma unroll
-    for (int j = 0; j < VALUES; ++j) hits |= z[j] >= edge ? 1u << j : 0u;
+    for (int j = VALUES - 1; j >= 0; --j)
+        hits = __builtin_amdgcn_alignbit(hits, __float_as_uint(z[j] - edge), 31);
+    hits = ~hits & (uint32_t)((1ull << VALUES) - 1);
     const uint32_t mine = (uint32_t)__popc(hits);
     const uint32_t through = wave_scan(mine);
     uint32_t to = 0;
@@ -228,7 +250,7 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
     to = last_lane(to) + through - mine;
     // the candidate of the thread's j-th token
     auto own = [&](int j) -> uint64_t {
-        const int at = 8 * ((j >> 3) * THREADS + tid) + (j & 7);
+        const int at = token_at<THREADS>(j);
         return candidate(__uint_as_float(word[slot<SLICE>((unsigned)at)]), lo + at);
     };
     found += part * cap;
@@ -244,12 +266,11 @@ __global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *par
 #pragma unroll
         for (int j = 0; j < VALUES; ++j)
             if (z[j] > NEG_INF) low = fminf(low, z[j]);
-        low = -wave_max(-low);
-        if ((tid & 63) == 0) wave_low[wave] = low;
+        low = wave_min(low);
+        if ((tid & 63) == 0) atomicMin(&lowest, ordered(low));
     }
     __syncthreads();
-    if (first == NEG_INF)
-        edge = -wave_max((tid & 63) < WAVES ? -wave_low[tid & (WAVES - 1)] : NEG_INF);
+    if (first == NEG_INF) edge = unordered(lowest);
     if (taken > (uint32_t)cap) {
         // Equal values, or a spread that the bins do not resolve: the k-th
         // largest word, digit by digit from the top, and exactly k of them.
@@ -383,7 +404,7 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         best = fmaxf(best, parts[s].edge[0]);
     }
     top = wave_max(top);
-    least = -wave_max(-least);
+    least = wave_min(least);
     float edge = wave_max(best);
     if (slices > 1) {
         const int level = slices >= 8 ? 3 : slices >= 4 ? 2 : 1;

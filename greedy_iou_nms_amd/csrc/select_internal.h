@@ -103,12 +103,31 @@ __device__ __forceinline__ V wave_scan(V v) {
 template <typename V>
 __device__ __forceinline__ V wave_sum(V v) { return last_lane(wave_scan(v)); }
 
-__device__ __forceinline__ float wave_max(float v) {
-#define GNMS_STEP(CTRL, ROWS) v = fmaxf(v, dpp<CTRL, ROWS>(NEG_INF, v));
+// The order of floats as that of signed integers (and back): integer steps
+// are one instruction each, where every float maximum costs two more that
+// quieten its inputs.  No NaN.
+__device__ __forceinline__ int ordered(float v) {
+    const int i = __float_as_int(v);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) {
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+__device__ __forceinline__ int wave_max(int v) {
+#define GNMS_STEP(CTRL, ROWS) v = max(v, dpp<CTRL, ROWS>((int)0x80000000, v));
     GNMS_DPP_STEPS(GNMS_STEP)
 #undef GNMS_STEP
     return last_lane(v);
 }
+__device__ __forceinline__ int wave_min(int v) {
+#define GNMS_STEP(CTRL, ROWS) v = min(v, dpp<CTRL, ROWS>(0x7fffffff, v));
+    GNMS_DPP_STEPS(GNMS_STEP)
+#undef GNMS_STEP
+    return last_lane(v);
+}
+__device__ __forceinline__ float wave_max(float v) { return unordered(wave_max(ordered(v))); }
+__device__ __forceinline__ float wave_min(float v) { return unordered(wave_min(ordered(v))); }
 
 // ----------------------------------------------------------------- launches
 
