@@ -129,7 +129,7 @@ __device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t lef
 // VALUES per thread in groups of eight neighbouring tokens; GROUP of them
 // share an entry in the histogram (their largest).
 template <typename T, int THREADS, int VALUES, int GROUP>
-__global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *parts,
+__global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(PickArgs a, Part *parts,
                                                            uint64_t *found) {
     constexpr int SLICE = THREADS * VALUES;
     constexpr int WAVES = THREADS / 64;
@@ -605,8 +605,8 @@ void run(const PickArgs &a, hipStream_t stream) {
     // the k-th largest group bounds the k-th value closely (of values without
     // order about 1.15 k lie above it).
     if (wide_slices(a.rows, a.vocab)) {
-        if (a.max_top_k <= 256) run_slices<T, 1024, 16, 16>(a, slices, parts, found, stream);
-        else run_slices<T, 1024, 16, 4>(a, slices, parts, found, stream);
+        if (a.max_top_k <= 256) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
+        else run_slices<T, 512, 32, 4>(a, slices, parts, found, stream);
     } else {
         if (a.max_top_k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 1>(a, slices, parts, found, stream);

@@ -1,187 +1,530 @@
 // Routing of tokens to experts, and its gradient.
 //
-// Forward.  s = softmax(z) or sigmoid(z) in binary64, c = s + bias; an expert
-// whose logit or c is NaN or -infinity cannot be chosen.  With groups, the
-// kept groups are those with the largest sums of their best one or two c.
-// The chosen experts come in descending c (in descending logit when there is
-// no bias, which is the same order before rounding), ties to the lower index.
-// Binary64 because the choice is a comparison: a float32 sigmoid is off by a
-// few 2^-24, and of 16384 tokens with 256 experts about one has two
-// candidates closer than that.
+// Forward.  s = softmax(z) or sigmoid(z), c = s + bias; an expert whose logit
+// or c is NaN or -infinity cannot be chosen.  With groups, the kept groups are
+// those with the largest sums of their best one or two c.  The chosen experts
+// come in descending c (in descending z where there is no bias), ties to the
+// lower index.  The choice is a comparison of real numbers, made as in
+// binary64: of 16384 tokens with 256 experts about one has two candidates
+// closer than a float32 sigmoid's error.
+//
+// Two forms.  quick_kernel makes the choice on 32-bit keys, 22 bits of the
+// value's distance from the token's largest and 10 bits of the index, so that
+// a comparison, a sort step and a maximum over lanes are one or two
+// instructions each.  It knows how far a key may be off; a token with two
+// candidates that its keys cannot order, and that are not equal, is chosen by
+// exact_token, in binary64 (about one in 500 where scores have no ties).
+// exact_kernel is exact_token for every token, for shapes that the first form
+// does not hold.
 #include "select_internal.h"
 
 namespace gnms {
 namespace {
 
-constexpr int RT = 256;  // threads per workgroup, one wave per token
+constexpr int RT = 256;  // threads per workgroup
 constexpr int RWAVES = RT / 64;
-constexpr int MAX_VALUES = NMS_ROUTE_MAX_EXPERTS / 64;  // experts per lane
-
 constexpr double LOWEST = -__builtin_inf();
 
-template <typename T>
-__global__ __launch_bounds__(RT) void route_kernel(RouteArgs a) {
-    __shared__ double group_c[RWAVES][NMS_ROUTE_MAX_EXPERTS];
-    __shared__ uint8_t group_kept[RWAVES][NMS_ROUTE_MAX_EXPERTS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * RWAVES + wave;
-    // every wave of the workgroup reaches its end by itself (no barrier)
-    if (t >= a.tokens) return;
-    const int E = a.experts, k = a.opt.top_k;
-    int32_t *ids = a.ids + t * k;
-    float *weights = a.weights + t * k;
-    if (a.live != nullptr && a.live[t] == 0) {
-        if (lane < k) {
-            ids[lane] = -1;
-            weights[lane] = 0.0f;
+// ---------------------------------------- reductions over 4 .. 64 lanes
+
+// Combines with every lane of the aligned N lanes; the result is in all of
+// them.  Mirrors serve as butterfly steps once the halves agree.
+template <int N, typename V, typename F>
+__device__ __forceinline__ V all_lanes(V v, F f) {
+    if (N >= 2) v = f(v, dpp<0xB1, 0xf>(v, v));    // lane ^ 1
+    if (N >= 4) v = f(v, dpp<0x4E, 0xf>(v, v));    // lane ^ 2
+    if (N >= 8) v = f(v, dpp<0x141, 0xf>(v, v));   // mirrored in 8
+    if (N >= 16) v = f(v, dpp<0x140, 0xf>(v, v));  // mirrored in 16
+    if (N >= 32) v = f(v, __shfl_xor(v, 16));
+    if (N >= 64) v = f(v, __shfl_xor(v, 32));
+    return v;
+}
+template <int N, typename V>
+__device__ __forceinline__ V all_max(V v) {
+    return all_lanes<N>(v, [](V a, V b) { return a > b ? a : b; });
+}
+template <int N, typename V>
+__device__ __forceinline__ V all_min(V v) {
+    return all_lanes<N>(v, [](V a, V b) { return a < b ? a : b; });
+}
+template <int N, typename V>
+__device__ __forceinline__ V all_sum(V v) {
+    return all_lanes<N>(v, [](V a, V b) { return a + b; });
+}
+
+// ------------------------------------------------------------ exact scores
+
+// exp(x) to 2^-40 of its value: 2^n from the exponent, a Taylor polynomial of
+// degree 11 on [-ln 2 / 2, ln 2 / 2] (its remainder is below
+// 0.3466^12 / 12! = 6e-15).  The library's exp takes four times as many
+// instructions for the last 12 bits, which no float32 weight shows.
+__device__ __forceinline__ double exp_of(double x) {
+    x = fmin(fmax(x, -800.0), 800.0);
+    const double n = rint(x * 1.4426950408889634);
+    double f = __builtin_fma(n, -0.6931471805599453, x);
+    f = __builtin_fma(n, -2.3190468138462996e-17, f);
+    double p = 1.0 / 39916800;
+    p = __builtin_fma(p, f, 1.0 / 3628800);
+    p = __builtin_fma(p, f, 1.0 / 362880);
+    p = __builtin_fma(p, f, 1.0 / 40320);
+    p = __builtin_fma(p, f, 1.0 / 5040);
+    p = __builtin_fma(p, f, 1.0 / 720);
+    p = __builtin_fma(p, f, 1.0 / 120);
+    p = __builtin_fma(p, f, 1.0 / 24);
+    p = __builtin_fma(p, f, 1.0 / 6);
+    p = __builtin_fma(p, f, 0.5);
+    p = __builtin_fma(p, f, 1.0);
+    p = __builtin_fma(p, f, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+}
+
+// exp(z - top), 1 at z = top (infinite ones too), 0 at -infinity.
+template <typename EXP>
+__device__ __forceinline__ double exp_below(float z, float top, EXP e) {
+    return z == top ? 1.0 : z == NEG_INF ? 0.0 : e((double)z - (double)top);
+}
+
+// ------------------------------------------------- one token, in binary64
+
+// What a wave needs of LDS for rows of up to N experts.
+template <int N>
+struct ExactSpace {
+    double c[N];
+    uint8_t kept[N];
+};
+
+// The largest value above -infinity that the lanes know, and the lowest place
+// that has it; place -1 if there is none.
+__device__ __forceinline__ void wave_best(double &v, int &at) {
+#pragma unroll 1
+    for (int d = 32; d > 0; d >>= 1) {
+        const double v2 = __shfl_xor(v, d);
+        const int at2 = __shfl_xor(at, d);
+        if (at2 >= 0 && (at < 0 || v2 > v || (v2 == v && at2 < at))) {
+            v = v2;
+            at = at2;
         }
-        return;
-    }
-    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
-    float z[MAX_VALUES];
-    float m = NEG_INF;
-#pragma unroll
-    for (int j = 0; j < MAX_VALUES; ++j) {
-        const int e = 64 * j + lane;
-        float v = e < E ? to_f32(row[e]) : NEG_INF;
-        if (!(v > NEG_INF)) v = NEG_INF;
-        z[j] = v;
-        m = fmaxf(m, v);
-    }
-    double s[MAX_VALUES], c[MAX_VALUES], r[MAX_VALUES];
-    double total = 0.0;
-    const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX;
-    if (softmax) {
-        m = wave_max(m);
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j) {
-            s[j] = z[j] == NEG_INF ? 0.0 : z[j] == m ? 1.0 : exp((double)z[j] - (double)m);
-            total += s[j];
-        }
-        total = wave_sum(total);
-    }
-#pragma unroll
-    for (int j = 0; j < MAX_VALUES; ++j) {
-        const int e = 64 * j + lane;
-        s[j] = z[j] == NEG_INF ? 0.0 : softmax ? s[j] / total : 1.0 / (1.0 + exp(-(double)z[j]));
-        c[j] = z[j] == NEG_INF ? LOWEST : s[j] + (a.bias ? (double)a.bias[e] : 0.0);
-        if (!(c[j] > LOWEST)) c[j] = LOWEST;
-        r[j] = a.bias == nullptr && c[j] > LOWEST ? (double)z[j] : c[j];
-    }
-    if (a.opt.groups > 1) {
-        const int G = a.opt.groups, size = E / G;
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j)
-            if (64 * j + lane < E) group_c[wave][64 * j + lane] = c[j];
-        wave_fence();
-        double best[MAX_VALUES];
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j) {
-            const int g = 64 * j + lane;
-            double b0 = LOWEST, b1 = LOWEST;
-            if (g < G)
-                for (int i = 0; i < size; ++i) {
-                    const double v = group_c[wave][g * size + i];
-                    b1 = v > b0 ? b0 : v > b1 ? v : b1;
-                    b0 = v > b0 ? v : b0;
-                }
-            best[j] = a.opt.group_top == 2 && b1 > LOWEST ? b0 + b1 : b0;
-        }
-        for (int g = lane; g < G; g += 64) group_kept[wave][g] = 0;
-        wave_fence();
-        for (int i = 0; i < a.opt.kept_groups; ++i) {
-            double v = LOWEST;
-            int at = -1;
-#pragma unroll
-            for (int j = 0; j < MAX_VALUES; ++j)
-                if (best[j] > v) {
-                    v = best[j];
-                    at = 64 * j + lane;
-                }
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) {
-                const double v2 = __shfl_xor(v, d);
-                const int at2 = __shfl_xor(at, d);
-                if (v2 > v || (v2 == v && at2 >= 0 && at2 < at)) {
-                    v = v2;
-                    at = at2;
-                }
-            }
-            if (at < 0) break;
-#pragma unroll
-            for (int j = 0; j < MAX_VALUES; ++j)
-                if (at == 64 * j + lane) {
-                    best[j] = LOWEST;
-                    group_kept[wave][at] = 1;
-                }
-        }
-        wave_fence();
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j) {
-            const int e = 64 * j + lane;
-            if (e < E && group_kept[wave][e / size] == 0) r[j] = LOWEST;
-        }
-    }
-    int my_id = -1;
-    float my_z = NEG_INF;
-    double my_s = 0.0;
-    for (int i = 0; i < k; ++i) {
-        double v = LOWEST;
-        int at = -1;
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j)
-            if (r[j] > v) {
-                v = r[j];
-                at = 64 * j + lane;
-            }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) {
-            const double v2 = __shfl_xor(v, d);
-            const int at2 = __shfl_xor(at, d);
-            if (v2 > v || (v2 == v && at2 >= 0 && (at < 0 || at2 < at))) {
-                v = v2;
-                at = at2;
-            }
-        }
-        if (at < 0) break;
-        double sv = 0.0;
-        float zv = 0.0f;
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j)
-            if (at == 64 * j + lane) {
-                r[j] = LOWEST;
-                sv = s[j];
-                zv = z[j];
-            }
-        sv = __shfl(sv, at & 63);
-        zv = __shfl(zv, at & 63);
-        if (lane == i) {
-            my_id = at;
-            my_s = sv;
-            my_z = zv;
-        }
-    }
-    if (a.opt.renormalise) {
-        if (softmax) {
-            // the softmax over the chosen logits: the same quotient, and it
-            // holds where every chosen probability is below binary64's range
-            const float zm = wave_max(my_z);
-            my_s = my_id < 0 ? 0.0 : my_z == zm ? 1.0 : exp((double)my_z - (double)zm);
-        }
-        const double sum = wave_sum(my_s);
-        my_s = sum > 0.0 ? my_s / sum : 0.0;
-    }
-    if (lane < k) {
-        ids[lane] = my_id;
-        weights[lane] = (float)(my_s * (double)a.opt.scale);
-        if (a.counts != nullptr && my_id >= 0) atomicAdd(a.counts + my_id, 1);
     }
 }
 
-__global__ void zero_counts_kernel(int32_t *counts, int n) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n) counts[i] = 0;
+// Chooses the experts of token t: lane i gets the i-th one's index, or -1.
+// Every loop is over LDS and rolled, so that it takes few registers.
+template <typename T, int N>
+__device__ __forceinline__ int exact_token(const RouteArgs &a, int64_t t, ExactSpace<N> &x) {
+    const int lane = threadIdx.x & 63;
+    const int E = a.experts, G = a.opt.groups, size = E / G;
+    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
+    const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX;
+    float top = NEG_INF;
+    double sum = 0.0;
+    wave_fence();
+    if (softmax) {
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64) top = fmaxf(top, to_f32(row[e]));
+        top = wave_max(top > NEG_INF ? top : NEG_INF);
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64) {
+            const float z = to_f32(row[e]);
+            if (z > NEG_INF) sum += exp_below(z, top, [](double v) { return exp(v); });
+        }
+        sum = wave_sum(sum);
+    }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+        const float z = to_f32(row[e]);
+        double c = LOWEST;
+        if (z > NEG_INF) {
+            c = softmax ? exp_below(z, top, [](double v) { return exp(v); }) / sum
+                        : 1.0 / (1.0 + exp(-(double)z));
+            if (a.bias != nullptr) c += (double)a.bias[e];
+            if (!(c > LOWEST)) c = LOWEST;
+        }
+        x.c[e] = c;
+    }
+    if (G > 1) {
+#pragma unroll 1
+        for (int g = lane; g < G; g += 64) x.kept[g] = 0;
+        wave_fence();
+#pragma unroll 1
+        for (int i = 0; i < a.opt.kept_groups; ++i) {
+            // the groups' scores anew each time: nothing is kept of them
+            double v = LOWEST;
+            int at = -1;
+#pragma unroll 1
+            for (int g = lane; g < G; g += 64) {
+                double b0 = LOWEST, b1 = LOWEST;
+#pragma unroll 1
+                for (int j = 0; j < size; ++j) {
+                    const double w = x.c[g * size + j];
+                    b1 = w > b0 ? b0 : w > b1 ? w : b1;
+                    b0 = w > b0 ? w : b0;
+                }
+                if (a.opt.group_top == 2 && b1 > LOWEST) b0 += b1;
+                if (x.kept[g] == 0 && b0 > v) {
+                    v = b0;
+                    at = g;
+                }
+            }
+            wave_best(v, at);
+            if (at < 0) break;
+            if (lane == 0) x.kept[at] = 1;
+            wave_fence();
+        }
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            if (x.kept[e / size] == 0) x.c[e] = LOWEST;
+    }
+    // without a bias the order is the logits'
+    if (a.bias == nullptr) {
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            if (x.c[e] > LOWEST) x.c[e] = (double)to_f32(row[e]);
+    }
+    int mine = -1;
+#pragma unroll 1
+    for (int i = 0; i < a.opt.top_k; ++i) {
+        double v = LOWEST;
+        int at = -1;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            if (x.c[e] > v) {
+                v = x.c[e];
+                at = e;
+            }
+        wave_best(v, at);
+        if (at < 0) break;
+        if (lane == (at & 63)) x.c[at] = LOWEST;
+        if (lane == i) mine = at;
+    }
+    wave_fence();
+    return mine;
 }
+
+// The weights of a token's chosen experts and what is written of them.  The
+// token's LANES lanes call it together; lane i has the i-th expert (or -1).
+// sum: of exp(z - top) over the whole row where the softmax needs it.
+template <typename T, int LANES>
+__device__ __forceinline__ void write_token(const RouteArgs &a, int64_t t, bool write, int place,
+                                            int id, float top, double sum) {
+    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
+    const float z = id >= 0 ? to_f32(row[id]) : NEG_INF;
+    const auto e = [](double v) { return exp_of(v); };
+    double w = 0.0;
+    if (a.opt.score == NMS_ROUTE_SOFTMAX) {
+        // renormalised: the softmax over the chosen logits, the same quotient,
+        // which holds where every chosen probability is below binary64's range
+        if (a.opt.renormalise) top = unordered(all_max<LANES>(ordered(z)));
+        w = id >= 0 ? exp_below(z, top, e) : 0.0;
+        if (a.opt.renormalise) sum = all_sum<LANES>(w);
+    } else {
+        w = id >= 0 ? 1.0 / (1.0 + e(-(double)z)) : 0.0;
+        sum = a.opt.renormalise ? all_sum<LANES>(w) : 1.0;
+    }
+    w = sum > 0.0 ? w / sum : 0.0;
+    if (write && place < a.opt.top_k) {
+        a.ids[t * a.opt.top_k + place] = id;
+        a.weights[t * a.opt.top_k + place] = (float)(w * (double)a.opt.scale);
+    }
+}
+
+// The softmax sum of a row by the whole wave.
+template <typename T>
+__device__ __forceinline__ void row_sum(const RouteArgs &a, int64_t t, float &top, double &sum) {
+    const int lane = threadIdx.x & 63;
+    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
+    top = NEG_INF;
+    sum = 0.0;
+    for (int e = lane; e < a.experts; e += 64) top = fmaxf(top, to_f32(row[e]));
+    top = wave_max(top > NEG_INF ? top : NEG_INF);
+    for (int e = lane; e < a.experts; e += 64) {
+        const float z = to_f32(row[e]);
+        if (z > NEG_INF) sum += exp_below(z, top, [](double v) { return exp_of(v); });
+    }
+    sum = wave_sum(sum);
+}
+
+// The first workgroup clears the counts, which count_kernel adds to.
+__device__ __forceinline__ void clear_counts(const RouteArgs &a) {
+    if (a.counts != nullptr && blockIdx.x == 0)
+        for (int e = threadIdx.x; e < a.experts; e += RT) a.counts[e] = 0;
+}
+
+template <typename T>
+__global__ __launch_bounds__(RT) void exact_kernel(RouteArgs a) {
+    __shared__ ExactSpace<NMS_ROUTE_MAX_EXPERTS> space[RWAVES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * RWAVES + wave;
+    clear_counts(a);
+    if (t >= a.tokens) return;  // no barrier follows
+    const bool live = a.live == nullptr || a.live[t] != 0;
+    const int id = live ? exact_token<T>(a, t, space[wave]) : -1;
+    float top = 0.0f;
+    double sum = 1.0;
+    if (a.opt.score == NMS_ROUTE_SOFTMAX && !a.opt.renormalise) row_sum<T>(a, t, top, sum);
+    write_token<T, 64>(a, t, true, lane, id, top, sum);
+}
+
+// -------------------------------------------------------------- quick form
+
+// Batcher's merge exchange, descending.
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t *key) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t x = key[i + j], y = key[i + j + k];
+                        key[i + j] = max(x, y);
+                        key[i + j + k] = min(x, y);
+                    }
+}
+
+constexpr uint32_t INDEX_BITS = 10, INDEX_MASK = (1u << INDEX_BITS) - 1u;
+constexpr uint32_t Q_TOP = (1u << 22) - 1u;
+static_assert(NMS_ROUTE_MAX_EXPERTS <= (int)INDEX_MASK + 1, "an index fits its field");
+
+__device__ __forceinline__ uint32_t with_index(uint32_t q, int e) {
+    return q << INDEX_BITS | (INDEX_MASK - (uint32_t)e);
+}
+
+// The 16-bit types' order in 16 bits (-0 folded onto +0), 0 for -infinity and
+// NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t short_key(T v) {
+    uint16_t u;
+    __builtin_memcpy(&u, &v, 2);
+    if (u == 0x8000u) u = 0;
+    const uint32_t k = (u & 0x8000u) ? (uint16_t)~u : (uint32_t)(u | 0x8000u);
+    return to_f32(v) > NEG_INF ? k : 0u;
+}
+
+// LANES lanes share a token, VALUES experts each: lane l has the experts
+// VALUES * l and on.  top_k is at most LANES.
+template <typename T, int LANES, int VALUES>
+__global__ __launch_bounds__(RT) void quick_kernel(RouteArgs a, int group_lanes) {
+    constexpr int TOKENS = 64 / LANES;  // per wave
+    __shared__ ExactSpace<LANES * VALUES> space[RWAVES];
+    const int lane = threadIdx.x & 63, sub = lane % LANES;
+    const int64_t t = ((int64_t)blockIdx.x * RWAVES + (threadIdx.x >> 6)) * TOKENS + lane / LANES;
+    const bool inside = t < a.tokens;
+    const int64_t tok = inside ? t : a.tokens - 1;
+    const bool live = inside && (a.live == nullptr || a.live[tok] != 0);
+    const int E = a.experts, k = a.opt.top_k, e0 = sub * VALUES;
+    const T *row = static_cast<const T *>(a.logits) + tok * a.row_stride;
+    clear_counts(a);
+
+    // the lane's logits, past the row -infinity
+    T raw[VALUES];
+    if (e0 + VALUES <= E) {
+        __builtin_memcpy(raw, row + e0, sizeof(raw));
+    } else {
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) raw[j] = e0 + j < E ? row[e0 + j] : from_f32<T>(NEG_INF);
+    }
+    float z[VALUES], top = NEG_INF;
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j) {
+        const float v = to_f32(raw[j]);
+        z[j] = v > NEG_INF ? v : NEG_INF;
+        top = fmaxf(top, z[j]);
+    }
+    const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX;
+    const bool grouped = a.opt.groups > 1, scored = a.bias != nullptr || grouped;
+    const bool whole = softmax && (scored || !a.opt.renormalise);
+    top = unordered(all_max<LANES>(ordered(top)));
+
+    // the softmax sum, which the weights need to 2^-24 and better
+    double sum = 1.0;
+    if (whole) {
+        sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j)
+            sum += exp_below(z[j], top, [](double v) { return exp_of(v); });
+        sum = all_sum<LANES>(sum);
+    }
+
+    // Keys.  margin: two candidates whose q differ by no more may be in either
+    // order, unless they are equal; negative: the keys are exact.
+    uint32_t key[VALUES];
+    int margin = 0;
+    bool bad = false;  // the token needs exact_token
+    if (scored) {
+        // c in float32: a sigmoid or a softmax share is off by less than
+        // 3 * 2^-23, and its sum with a bias by |c| 2^-24 more; the scale is
+        // 2^22, and q is rounded twice
+        float c[VALUES], c_top = NEG_INF;
+        const float share = (float)(1.0 / sum);
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            const float s = softmax ? __builtin_amdgcn_exp2f((z[j] - top) * 1.44269504f) * share
+                                    : __builtin_amdgcn_rcpf(
+                                          1.0f + __builtin_amdgcn_exp2f(z[j] * -1.44269504f));
+            c[j] = s + (a.bias != nullptr && e0 + j < E ? a.bias[e0 + j] : 0.0f);
+            if (!(z[j] > NEG_INF && c[j] > NEG_INF)) c[j] = NEG_INF;
+            c_top = fmaxf(c_top, c[j]);
+        }
+        c_top = unordered(all_max<LANES>(ordered(c_top)));
+        bad = !(fabsf(c_top) < 64.0f) || !(fabsf(top) < 3.0e38f);
+        margin = 8 + (int)fabsf(bad ? 0.0f : c_top);
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            const float q = fmaxf((c[j] - c_top) * 4194304.0f + (float)Q_TOP, 1.0f);
+            key[j] = c[j] > NEG_INF ? with_index((uint32_t)q, e0 + j) : 0u;
+        }
+    } else if (sizeof(T) == 2) {
+        margin = -1;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            const uint32_t q = short_key(raw[j]);
+            key[j] = q != 0u ? with_index(q, e0 + j) : 0u;
+        }
+    } else {
+        // z down to 64 below the top, monotone: only equal q are open
+        bad = !(fabsf(top) < 3.0e38f);
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            const float q = fmaxf((z[j] - top) * 65536.0f + (float)Q_TOP, 1.0f);
+            key[j] = z[j] > NEG_INF ? with_index((uint32_t)q, e0 + j) : 0u;
+        }
+    }
+    // a row without eligible experts has nothing to choose from
+    if (top == NEG_INF) bad = false;
+    sort_keys<VALUES>(key);
+
+    if (grouped) {
+        // The best two of each group, over its lanes; then how many groups
+        // have a larger sum, equal ones ordered by their number.
+        uint32_t b0 = key[0], b1 = VALUES > 1 ? key[VALUES > 1 ? 1 : 0] : 0u;
+        auto merge = [&](uint32_t o0, uint32_t o1) {
+            b1 = max(min(b0, o0), max(b1, o1));
+            b0 = max(b0, o0);
+        };
+        if (group_lanes >= 2) merge(dpp<0xB1, 0xf>(b0, b0), dpp<0xB1, 0xf>(b1, b1));
+        if (group_lanes >= 4) merge(dpp<0x4E, 0xf>(b0, b0), dpp<0x4E, 0xf>(b1, b1));
+        if (group_lanes >= 8) merge(dpp<0x141, 0xf>(b0, b0), dpp<0x141, 0xf>(b1, b1));
+        if (group_lanes >= 16) merge(dpp<0x140, 0xf>(b0, b0), dpp<0x140, 0xf>(b1, b1));
+        if (group_lanes >= 32) merge(__shfl_xor(b0, 16), __shfl_xor(b1, 16));
+        const int g = sub / group_lanes;
+        const bool group = g < a.opt.groups;
+        const bool two = a.opt.group_top == 2;
+        const uint32_t q0 = b0 >> INDEX_BITS, q1 = b1 >> INDEX_BITS;
+        // a group with one expert where others sum two, or one that reaches
+        // the keys' end
+        if (group && q0 != 0u && (q0 <= 1u || (two && q1 <= 1u))) bad = true;
+        const uint32_t score = group ? q0 + (two ? q1 : 0u) : 0u;
+        const uint32_t ranked = score << 6 | (uint32_t)(63 - g);
+        int larger = 0;
+        if (LANES == 16) {
+#define GNMS_ROTATE(N) \
+    if (((N) & (group_lanes - 1)) == 0) larger += dpp<0x120 + N, 0xf>(ranked, ranked) > ranked ? 1 : 0;
+            GNMS_ROTATE(1) GNMS_ROTATE(2) GNMS_ROTATE(3) GNMS_ROTATE(4) GNMS_ROTATE(5)
+            GNMS_ROTATE(6) GNMS_ROTATE(7) GNMS_ROTATE(8) GNMS_ROTATE(9) GNMS_ROTATE(10)
+            GNMS_ROTATE(11) GNMS_ROTATE(12) GNMS_ROTATE(13) GNMS_ROTATE(14) GNMS_ROTATE(15)
+#undef GNMS_ROTATE
+        } else {
+            for (int o = group_lanes; o < LANES; o += group_lanes)
+                larger += __shfl(ranked, (lane + o) & 63) > ranked ? 1 : 0;
+        }
+        const bool kept = score > 0u && larger < a.opt.kept_groups;
+        // how close the choice of the groups was
+        const uint32_t least = all_min<LANES>(kept ? score : 0xffffffffu);
+        const uint32_t most = all_max<LANES>(kept ? 0u : score);
+        if (most != 0u && least - most <= (uint32_t)(2 * margin)) bad = true;
+        if (!kept) {
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) key[j] = 0u;
+        }
+    }
+
+    // The largest key of all lanes, top_k times; the lane that has it moves
+    // its next one up.
+    uint32_t mine = 0u, last = 0u;
+    bool close = false;
+    auto next = [&]() -> uint32_t {
+        const uint32_t m = all_max<LANES>(key[0]);
+        if (key[0] == m) {
+#pragma unroll
+            for (int j = 0; j + 1 < VALUES; ++j) key[j] = key[j + 1];
+            key[VALUES - 1] = 0u;
+        }
+        return m;
+    };
+    for (int i = 0; i < k; ++i) {
+        const uint32_t m = next();
+        // an end of the keys that a candidate lies at, or two that are close
+        close |= m != 0u && ((int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin && i > 0);
+        if (margin >= 0 && m != 0u && (m >> INDEX_BITS) <= 1u) bad = true;
+        if (sub == i) mine = m;
+        last = m;
+    }
+    int id = mine != 0u ? (int)(INDEX_MASK - (mine & INDEX_MASK)) : -1;
+    // Candidates that are close must be equal, in their logits and biases; the
+    // one after the last, too, and those that are equal to it.
+    auto equal = [&](int x, int y) {
+        return to_f32(row[x]) == to_f32(row[y]) &&
+               (a.bias == nullptr || a.bias[x] == a.bias[y]);
+    };
+    if (margin >= 0) {
+        bool open = last != 0u && !bad;
+        while (__ballot(open) != 0ull) {
+            const uint32_t m = next();
+            open = open && m != 0u &&
+                   (int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin;
+            if (open && !equal((int)(INDEX_MASK - (last & INDEX_MASK)),
+                               (int)(INDEX_MASK - (m & INDEX_MASK)))) {
+                bad = true;
+                open = false;
+            }
+        }
+        if (__ballot(close) != 0ull) {
+            const uint32_t after = __shfl_down(mine, 1);
+            if (sub + 1 < k && after != 0u &&
+                (int)((mine >> INDEX_BITS) - (after >> INDEX_BITS)) <= margin &&
+                !equal(id, (int)(INDEX_MASK - (after & INDEX_MASK))))
+                bad = true;
+        }
+        // any lane of the token
+        bad = all_max<LANES>((int)(live && bad)) != 0;
+    } else {
+        bad = false;
+    }
+    if (!live) id = -1;
+    write_token<T, LANES>(a, tok, inside && !bad, sub, id, top, sum);
+    for (uint64_t left = __ballot(bad && sub == 0); left != 0ull; left &= left - 1ull) {
+        const int first = __builtin_ctzll(left);
+        const int64_t one = __shfl((long long)tok, first);
+        id = exact_token<T>(a, one, space[threadIdx.x >> 6]);
+        write_token<T, 64>(a, one, true, lane, id, __shfl(top, first), __shfl(sum, first));
+    }
+}
+
+// Adds the experts of ids[0..n) to the counts; a single workgroup writes them.
+constexpr int CT = 1024, COUNTED = 4096;  // threads; ids per workgroup
+__global__ __launch_bounds__(CT) void count_kernel(const int32_t *ids, int64_t n, int experts,
+                                                   int32_t *counts) {
+    __shared__ int32_t hist[NMS_ROUTE_MAX_EXPERTS];
+    hist[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t step = (int64_t)gridDim.x * CT;
+    for (int64_t i = (int64_t)blockIdx.x * CT + threadIdx.x; i < n; i += step) {
+        const int id = ids[i];
+        if (id >= 0) atomicAdd(&hist[id], 1);
+    }
+    __syncthreads();
+    const int e = threadIdx.x, c = hist[e];
+    if (e < experts) {
+        if (gridDim.x == 1) counts[e] = c;
+        else if (c != 0) atomicAdd(&counts[e], c);
+    }
+}
+static_assert(CT == NMS_ROUTE_MAX_EXPERTS, "a thread per expert");
+
+// ---------------------------------------------------------------- gradient
 
 // Gradient of the weights in the logits, given the chosen experts.
 //   softmax, not renormalised  w_i = scale p_i:
@@ -190,106 +533,212 @@ __global__ void zero_counts_kernel(int32_t *counts, int n) {
 //       dz_j = q_j scale (g_j - sum_i g_i q_i), 0 for the others
 //   sigmoid                    w_i = scale s_i / D, D = 1 or sum of chosen s:
 //       dz_j = scale (g_j - [renormalised] sum_i g_i s_i / D) / D s_j (1 - s_j)
-template <typename T>
-__global__ __launch_bounds__(RT) void route_back_kernel(RouteBackArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * RWAVES + (threadIdx.x >> 6);
-    if (t >= a.tokens) return;
-    const int E = a.experts, k = a.opt.top_k;
-    const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
-    T *out = static_cast<T *>(a.grad_logits) + t * a.grad_stride;
-    int id = -1;
-    float g = 0.0f, zc = NEG_INF;
-    if (lane < k) {
-        id = a.ids[t * k + lane];
-        if ((unsigned)id >= (unsigned)E) id = -1;
-        if (id >= 0) {
-            g = a.grad_weights[t * k + lane] * a.opt.scale;
-            zc = to_f32(row[id]);
-        }
-    }
+// Only the first needs the whole row.  LANES lanes share a token, VALUES
+// experts each; the chosen experts' terms go to their places through LDS, one
+// after another, so that an index that comes twice adds up in a fixed order.
+template <typename T, int LANES, int VALUES>
+__global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
+    constexpr int TOKENS = 64 / LANES;            // per wave
+    constexpr int CHOSEN = NMS_ROUTE_MAX_TOP_K / LANES;  // per lane, at most
+    __shared__ float place[RWAVES * TOKENS][LANES * VALUES];
+    const int lane = threadIdx.x & 63, sub = lane % LANES;
+    const int mine = (threadIdx.x >> 6) * TOKENS + lane / LANES;
+    const int64_t t = (int64_t)blockIdx.x * (RWAVES * TOKENS) + mine;
+    const bool inside = t < a.tokens;
+    const int64_t tok = inside ? t : a.tokens - 1;
+    const int E = a.experts, k = a.opt.top_k, e0 = sub * VALUES;
+    const T *row = static_cast<const T *>(a.logits) + tok * a.row_stride;
     const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX;
-    float z[MAX_VALUES], p[MAX_VALUES];
-    float inner = 0.0f, d = 0.0f;
-    bool whole = softmax && !a.opt.renormalise;
+    const bool whole = softmax && !a.opt.renormalise;
+
+    float z[VALUES];
     if (whole) {
-        float m = NEG_INF, total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j) {
-            const int e = 64 * j + lane;
-            float v = e < E ? to_f32(row[e]) : NEG_INF;
-            if (!(v > NEG_INF)) v = NEG_INF;
-            z[j] = v;
-            m = fmaxf(m, v);
-        }
-        m = wave_max(m);
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j) {
-            p[j] = z[j] == NEG_INF ? 0.0f : z[j] == m ? 1.0f : expf(z[j] - m);
-            total += p[j];
-        }
-        total = wave_sum(total);
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-#pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j) p[j] *= inv;
-        const float pc = !(zc > NEG_INF) ? 0.0f : (zc == m ? 1.0f : expf(zc - m)) * inv;
-        inner = wave_sum(g * pc);
-        d = g;
-    } else if (softmax) {
-        if (!(zc > NEG_INF)) zc = NEG_INF;
-        const float m = wave_max(zc);
-        float q = zc == NEG_INF ? 0.0f : zc == m ? 1.0f : expf(zc - m);
-        const float total = wave_sum(q);
-        q = total > 0.0f ? q / total : 0.0f;
-        d = q * (g - wave_sum(g * q));
-    } else {
-        // a NaN or -infinity logit is never chosen by the forward pass
-        const float s = !(zc > NEG_INF) ? 0.0f : 1.0f / (1.0f + expf(-zc));
-        const float slope = !(zc > NEG_INF) ? 0.0f : s / (1.0f + expf(zc));
-        if (a.opt.renormalise) {
-            const float total = wave_sum(s);
-            const float mean = total > 0.0f ? wave_sum(g * s) / total : 0.0f;
-            d = total > 0.0f ? (g - mean) / total * slope : 0.0f;
+        T raw[VALUES];
+        if (e0 + VALUES <= E) {
+            __builtin_memcpy(raw, row + e0, sizeof(raw));
         } else {
-            d = g * slope;
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j)
+                raw[j] = e0 + j < E ? row[e0 + j] : from_f32<T>(NEG_INF);
+        }
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw[j]);
+    }
+    int id[CHOSEN];
+    float g[CHOSEN], zc[CHOSEN];
+#pragma unroll
+    for (int q = 0; q < CHOSEN; ++q) {
+        const int i = q * LANES + sub;
+        id[q] = -1;
+        g[q] = 0.0f;
+        zc[q] = NEG_INF;
+        if (i < k) {
+            const int e = a.ids[tok * k + i];
+            if ((unsigned)e < (unsigned)E) {
+                id[q] = e;
+                g[q] = a.grad_weights[tok * k + i] * a.opt.scale;
+                const float v = to_f32(row[e]);
+                zc[q] = v > NEG_INF ? v : NEG_INF;
+            }
         }
     }
-    float ds[MAX_VALUES];
+    // LDS executes a wave's accesses in order
 #pragma unroll
-    for (int j = 0; j < MAX_VALUES; ++j) ds[j] = 0.0f;
-    for (int i = 0; i < k; ++i) {
-        const int at = __shfl(id, i);
-        const float v = __shfl(d, i);
+    for (int j = 0; j < VALUES; ++j) place[mine][e0 + j] = 0.0f;
+
+    const auto share = [](float v, float top) {
+        return v == top ? 1.0f : v == NEG_INF ? 0.0f : expf(v - top);
+    };
+    float top = NEG_INF, total = 0.0f, inner = 0.0f, s[CHOSEN], d[CHOSEN];
+    if (softmax) {
+        if (whole) {
 #pragma unroll
-        for (int j = 0; j < MAX_VALUES; ++j)
-            if (at == 64 * j + lane) ds[j] += v;
+            for (int j = 0; j < VALUES; ++j) {
+                z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
+                top = fmaxf(top, z[j]);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < CHOSEN; ++q) top = fmaxf(top, zc[q]);
+        }
+        top = unordered(all_max<LANES>(ordered(top)));
+#pragma unroll
+        for (int q = 0; q < CHOSEN; ++q) s[q] = zc[q] == NEG_INF ? 0.0f : share(zc[q], top);
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) {
+                z[j] = z[j] == NEG_INF ? 0.0f : share(z[j], top);
+                total += z[j];
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < CHOSEN; ++q) total += s[q];
+        }
+        total = all_sum<LANES>(total);
+        const float inverse = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+        for (int q = 0; q < CHOSEN; ++q) {
+            s[q] *= inverse;
+            inner += g[q] * s[q];
+        }
+        inner = all_sum<LANES>(inner);
+#pragma unroll
+        for (int q = 0; q < CHOSEN; ++q) d[q] = whole ? g[q] : s[q] * (g[q] - inner);
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) z[j] *= inverse;
+        }
+    } else {
+        float weighted = 0.0f;
+#pragma unroll
+        for (int q = 0; q < CHOSEN; ++q) {
+            s[q] = zc[q] == NEG_INF ? 0.0f : 1.0f / (1.0f + expf(-zc[q]));
+            total += s[q];
+            weighted += g[q] * s[q];
+        }
+        if (a.opt.renormalise) {
+            total = all_sum<LANES>(total);
+            weighted = all_sum<LANES>(weighted);
+            inner = total > 0.0f ? weighted / total : 0.0f;
+        } else {
+            total = 1.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < CHOSEN; ++q) {
+            // s (1 - s)
+            const float slope = s[q] == 0.0f ? 0.0f : s[q] / (1.0f + expf(zc[q]));
+            d[q] = total > 0.0f ? (g[q] - inner) / total * slope : 0.0f;
+        }
     }
 #pragma unroll
-    for (int j = 0; j < MAX_VALUES; ++j) {
-        const int e = 64 * j + lane;
-        if (e < E) out[e] = from_f32<T>(whole ? p[j] * (ds[j] - inner) : ds[j]);
+    for (int q = 0; q < CHOSEN; ++q)
+        for (int l = 0; l < LANES && q * LANES + l < k; ++l) {
+            wave_fence();
+            if (sub == l && id[q] >= 0) place[mine][id[q]] += d[q];
+        }
+    wave_fence();
+    if (!inside) return;
+    T out[VALUES];
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j) {
+        const float ds = place[mine][e0 + j];
+        out[j] = from_f32<T>(whole ? z[j] * (ds - inner) : ds);
     }
+    T *to = static_cast<T *>(a.grad_logits) + t * a.grad_stride + e0;
+    if (e0 + VALUES <= E) {
+        __builtin_memcpy(to, out, sizeof(out));
+    } else {
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j)
+            if (e0 + j < E) to[j] = out[j];
+    }
+}
+
+// ----------------------------------------------------------------- launches
+
+template <typename T, int LANES, int VALUES>
+void run_quick(const RouteArgs &a, int group_lanes, hipStream_t stream) {
+    constexpr int per = RWAVES * (64 / LANES);
+    quick_kernel<T, LANES, VALUES>
+        <<<(unsigned)((a.tokens + per - 1) / per), RT, 0, stream>>>(a, group_lanes);
+}
+
+// Whether quick_kernel<., lanes, values> holds the shape, and over how many
+// lanes a group lies.
+bool holds(const RouteArgs &a, int lanes, int values, int *group_lanes) {
+    if (a.experts > lanes * values || a.opt.top_k > lanes) return false;
+    *group_lanes = 1;
+    if (a.opt.groups == 1) return true;
+    const int size = a.experts / a.opt.groups, n = size / values;
+    *group_lanes = n;
+    return size % values == 0 && n >= 1 && (n & (n - 1)) == 0 && a.opt.groups * n <= lanes;
+}
+
+template <typename T>
+void run_route(const RouteArgs &a, hipStream_t stream) {
+    int g = 1;
+    if (holds(a, 16, 4, &g)) run_quick<T, 16, 4>(a, g, stream);
+    else if (holds(a, 16, 8, &g)) run_quick<T, 16, 8>(a, g, stream);
+    else if (holds(a, 16, 16, &g)) run_quick<T, 16, 16>(a, g, stream);
+    else if (holds(a, 64, 4, &g)) run_quick<T, 64, 4>(a, g, stream);
+    else if (holds(a, 64, 16, &g)) run_quick<T, 64, 16>(a, g, stream);
+    else exact_kernel<T><<<(unsigned)((a.tokens + RWAVES - 1) / RWAVES), RT, 0, stream>>>(a);
+}
+
+template <typename T, int LANES, int VALUES>
+void run_back(const RouteBackArgs &a, hipStream_t stream) {
+    constexpr int per = RWAVES * (64 / LANES);
+    back_kernel<T, LANES, VALUES><<<(unsigned)((a.tokens + per - 1) / per), RT, 0, stream>>>(a);
+}
+
+template <typename T>
+void run_back(const RouteBackArgs &a, hipStream_t stream) {
+    if (a.experts <= 64) run_back<T, 16, 4>(a, stream);
+    else if (a.experts <= 128) run_back<T, 16, 8>(a, stream);
+    else if (a.experts <= 256) run_back<T, 16, 16>(a, stream);
+    else run_back<T, 64, 16>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-    if (a.counts != nullptr)
-        zero_counts_kernel<<<(a.experts + 255) / 256, 256, 0, stream>>>(a.counts, a.experts);
     if (a.tokens > 0) {
-        const unsigned grid = (unsigned)((a.tokens + RWAVES - 1) / RWAVES);
-        if (a.dtype == NMS_F32) route_kernel<float><<<grid, RT, 0, stream>>>(a);
-        else if (a.dtype == NMS_F16) route_kernel<half_t><<<grid, RT, 0, stream>>>(a);
-        else route_kernel<bf16_t><<<grid, RT, 0, stream>>>(a);
+        if (a.dtype == NMS_F32) run_route<float>(a, stream);
+        else if (a.dtype == NMS_F16) run_route<half_t>(a, stream);
+        else run_route<bf16_t>(a, stream);
+    }
+    if (a.counts != nullptr) {
+        const int64_t n = a.tokens * a.opt.top_k, groups = (n + COUNTED - 1) / COUNTED;
+        count_kernel<<<(unsigned)(groups < 1 ? 1 : groups > 256 ? 256 : groups), CT, 0, stream>>>(
+            a.ids, n, a.experts, a.counts);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream) {
-    const unsigned grid = (unsigned)((a.tokens + RWAVES - 1) / RWAVES);
-    if (a.dtype == NMS_F32) route_back_kernel<float><<<grid, RT, 0, stream>>>(a);
-    else if (a.dtype == NMS_F16) route_back_kernel<half_t><<<grid, RT, 0, stream>>>(a);
-    else route_back_kernel<bf16_t><<<grid, RT, 0, stream>>>(a);
+    if (a.dtype == NMS_F32) run_back<float>(a, stream);
+    else if (a.dtype == NMS_F16) run_back<half_t>(a, stream);
+    else run_back<bf16_t>(a, stream);
     return hipGetLastError();
 }
 
