@@ -127,8 +127,10 @@ __device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t lef
 // ------------------------------------------------------------------- slices
 
 // VALUES per thread in groups of eight neighbouring tokens; GROUP of them
-// share an entry in the histogram (their largest).
-template <typename T, int THREADS, int VALUES, int GROUP>
+// share an entry in the histogram (their largest).  FIRST is for max_top_k = 1:
+// the slice's first largest token, without a histogram (1.1 us of a slice's
+// 4.8 where little else runs).
+template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
 __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(PickArgs a, Part *parts,
                                                            uint64_t *found) {
     constexpr int SLICE = THREADS * VALUES;
@@ -139,6 +141,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
     __shared__ float wave_top[WAVES], wave_sums[WAVES];
     __shared__ int highest, lowest;  // as ordered()
     __shared__ uint32_t taken, chosen[2];
+    __shared__ unsigned long long greatest;
     __shared__ float bound[EDGES];
     const int tid = threadIdx.x, wave = tid >> 6;
     const int64_t row = blockIdx.x;
@@ -154,6 +157,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
     for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) {
         taken = 0;
+        greatest = 0;
         highest = ordered(NEG_INF);
         lowest = ordered(__builtin_inff());
     }
@@ -199,10 +203,13 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
             break;
         }
     }
+    if (!FIRST) {
 #pragma unroll
-    for (int q = 0; q < VALUES / 4; ++q)
-        // a copy that can be read by a number of its place
-        __builtin_memcpy(word + slot<SLICE>((unsigned)token_at<THREADS>(4 * q)), z + 4 * q, 16);
+        for (int q = 0; q < VALUES / 4; ++q)
+            // a copy that can be read by a number of its place
+            __builtin_memcpy(word + slot<SLICE>((unsigned)token_at<THREADS>(4 * q)),
+                             z + 4 * q, 16);
+    }
     int least = ordered(__builtin_inff());
 #pragma unroll
     for (int g = 0; g < VALUES / GROUP; ++g)
@@ -217,6 +224,30 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
     __syncthreads();
     top = unordered(highest);
     const int k = a.max_top_k, cap = slice_cap(k);
+    found += part * cap;
+    // the slice's softmax sum from its waves', and what else it says; wave 0
+    auto finish = [&](uint32_t count, float e0, float e1, float e2, float e3, float least_found) {
+        const float wt = tid < WAVES ? wave_top[tid & (WAVES - 1)] : NEG_INF;
+        double all = 0.0;
+        if (wt > NEG_INF)
+            all = (double)wave_sums[tid & (WAVES - 1)] *
+                  (wt == top ? 1.0 : (double)__builtin_amdgcn_exp2f((wt - top) * c));
+        all = wave_sum(all);
+        if (tid == 0) parts[part] = Part{top, count, all, {e0, e1, e2, e3}, least_found, 0.0f};
+    };
+    if (FIRST) {
+        uint64_t best = 0;
+        if (top > NEG_INF) {
+#pragma unroll
+            for (int j = VALUES - 1; j >= 0; --j)
+                if (z[j] == top) best = candidate(z[j], lo + token_at<THREADS>(j));
+        }
+        if (best != 0) atomicMax(&greatest, (unsigned long long)best);
+        __syncthreads();
+        if (tid == 0) found[0] = greatest;
+        if (wave == 0) finish(top > NEG_INF ? 1u : 0u, top, top, top, top, top);
+        return;
+    }
     const Bins bins(unordered(lowest), top, BINS);
 #pragma unroll
     for (int g = 0; g < VALUES / GROUP; ++g)
@@ -253,7 +284,6 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
         const int at = token_at<THREADS>(j);
         return candidate(__uint_as_float(word[slot<SLICE>((unsigned)at)]), lo + at);
     };
-    found += part * cap;
     while (hits != 0u) {
         const int j = __builtin_ctz(hits);
         hits &= hits - 1u;
@@ -300,16 +330,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
         edge = key_value((uint32_t)(prefix >> 32));
         __syncthreads();
     }
-    if (wave == 0) {
-        const float wt = tid < WAVES ? wave_top[tid & (WAVES - 1)] : NEG_INF;
-        double all = 0.0;
-        if (wt > NEG_INF)
-            all = (double)wave_sums[tid & (WAVES - 1)] *
-                  (wt == top ? 1.0 : (double)__builtin_amdgcn_exp2f((wt - top) * c));
-        all = wave_sum(all);
-        if (tid == 0)
-            parts[part] = Part{top, taken, all, {first, bound[1], bound[2], bound[3]}, edge, 0.0f};
-    }
+    if (wave == 0) finish(taken, first, bound[1], bound[2], bound[3], edge);
 }
 
 // --------------------------------------------------------------------- join
@@ -337,18 +358,80 @@ __device__ __forceinline__ uint64_t sort_words(uint64_t v, int n, uint64_t *lds)
     return v;
 }
 
+// The row's largest value, its softmax sum relative to that, and a bound that
+// its kmax-th value is not below, or failing that one that no candidate is
+// below.  2^i slices with kmax / 2^i values each at a bound or above make a
+// bound, so it is the 2^i-th largest of the slices' edge[i]: with eight slices
+// of like values their eighth lets about kmax candidates through where one
+// slice's own kmax-th would let eight times as many.  One wave; a lane has the
+// part of slice `lane` already.
+struct RowParts {
+    float top, edge;
+    double sum;
+};
+
+__device__ __forceinline__ RowParts join_parts(const Part *parts, int slices, const Part &first,
+                                               float warm) {
+    const int lane = threadIdx.x & 63;
+    RowParts r;
+    r.top = first.top;
+    float least = first.count > 0 ? first.least : __builtin_inff(), best = first.edge[0];
+    for (int s = 64 + lane; s < slices; s += 64) {
+        r.top = fmaxf(r.top, parts[s].top);
+        if (parts[s].count > 0) least = fminf(least, parts[s].least);
+        best = fmaxf(best, parts[s].edge[0]);
+    }
+    r.top = wave_max(r.top);
+    r.sum = first.top > NEG_INF ? first.sum * exp(below_top(first.top, r.top) / (double)warm) : 0.0;
+    for (int s = 64 + lane; s < slices; s += 64)
+        if (parts[s].top > NEG_INF)
+            r.sum += parts[s].sum * exp(below_top(parts[s].top, r.top) / (double)warm);
+    r.sum = wave_sum(r.sum);
+    r.edge = wave_max(best);
+    if (slices > 1) {
+        const int level = slices >= 8 ? 3 : slices >= 4 ? 2 : 1;
+        const float e1 = first.edge[1], e2 = first.edge[2], e3 = first.edge[3];
+        float e = level == 3 ? e3 : level == 2 ? e2 : e1;
+        float m = NEG_INF;
+        for (int i = 0; i < 1 << level; ++i) {
+            m = wave_max(e);
+            if (lane == __builtin_ctzll(__ballot(e == m))) e = NEG_INF;
+        }
+        r.edge = fmaxf(r.edge, m);
+    }
+    if (!(r.edge > NEG_INF)) r.edge = wave_min(least);
+    return r;
+}
+
+// The part of slice `lane`, or an empty one.
+__device__ __forceinline__ Part lane_part(const Part *parts, int slices) {
+    const int lane = threadIdx.x & 63;
+    Part p = parts[min(lane, slices - 1)];
+    if (lane >= slices) {
+        p.top = NEG_INF;
+        p.count = 0;
+#pragma unroll
+        for (int i = 0; i < EDGES; ++i) p.edge[i] = NEG_INF;
+    }
+    return p;
+}
+
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, uint32_t inverse,
                                                        const Part *parts, const uint64_t *found) {
     constexpr int WAVES = THREADS / 64;
     constexpr int HELD = JOIN_HELD;
     constexpr int PER = JOIN_BINS / THREADS;  // bins per thread
+    constexpr int DRAW = THREADS / 256;       // candidates per thread that draws
     constexpr int LIST = THREADS + CROWDED;
     __shared__ uint64_t list[LIST], sorted[THREADS];
-    __shared__ uint32_t hist[JOIN_BINS], fill[JOIN_BINS];
-    __shared__ double wave_d[WAVES];
+    // per bin: its count of held candidates, then its first place; its count
+    // of the rest, then the next place of the rest; and its end
+    __shared__ uint32_t hist[JOIN_BINS], rest[JOIN_BINS], ends[JOIN_BINS];
+    __shared__ RowParts whole;
     __shared__ uint32_t wave_u[WAVES];
-    __shared__ int wave_i[3][WAVES];
+    __shared__ double wave_d[4];
+    __shared__ int wave_i[3][4];
     __shared__ uint32_t taken, crowded, inside, chosen[2];
     __shared__ double kept;
     const int64_t row = blockIdx.x;
@@ -357,28 +440,33 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
     const int kmax = a.max_top_k, cap = slice_cap(kmax);
     parts += row * slices;
     found += row * slices * cap;
+    const Part first = lane_part(parts, slices);
     // The slices' candidates in pieces of 64, one piece per wave at a time: a
     // wave's first pieces are loaded once, further ones (many slices of many
-    // candidates) again for every pass over them.  A place past a slice's
-    // count is read but not used.
+    // candidates) again for every pass over them.  Loads are made without a
+    // branch, from a place that exists, so that all are in flight together;
+    // what lies past a slice's count is read but not used.
     const int pieces = (cap + 63) / 64, total = slices * pieces;
     auto load = [&](int p) -> uint64_t {
-        if (p >= total) return 0;
-        // p / pieces: exact for p < 2^21 and pieces < 2^6
-        const int s = inverse == 0u ? p : (int)__umulhi((uint32_t)p, inverse), i = (p - s * pieces) * 64 + lane;
-        const uint32_t count = parts[s].count;
-        const uint64_t w = i < cap ? found[(int64_t)s * cap + i] : 0ull;
-        return (uint32_t)i < count ? w : 0ull;
+        const int q = min(p, total - 1);
+        // q / pieces: exact for q < 2^21 and pieces < 2^6
+        const int s = inverse == 0u ? q : (int)__umulhi((uint32_t)q, inverse);
+        const int i = (q - s * pieces) * 64 + lane;
+        const uint64_t w = found[(int64_t)s * cap + min(i, cap - 1)];
+        return p < total && (uint32_t)i < parts[s].count ? w : 0ull;
     };
     uint64_t held[HELD];
 #pragma unroll
     for (int q = 0; q < HELD; ++q) held[q] = load(q * WAVES + wave);
     // f is called with every candidate, and with 0 in their places' rest
+    auto each_rest = [&](auto f) {
+        for (int p = HELD * WAVES + wave; p < total; p += WAVES) f(load(p));
+    };
     auto each = [&](auto f) {
 #pragma unroll
         for (int q = 0; q < HELD; ++q)
             if (q * WAVES < total) f(held[q]);
-        for (int p = HELD * WAVES + wave; p < total; p += WAVES) f(load(p));
+        each_rest(f);
     };
     // the row's parameters, in flight with the candidates
     const float t = parameter(a.temperature, row, 1.0f, a.uniform);
@@ -387,39 +475,10 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
     const double min_p = (double)parameter(a.min_p, row, 0.0f, a.uniform);
     const double uniform = (double)a.uniform[row];
     const int k = min(max(parameter(a.top_k, row, kmax, a.uniform), 1), kmax);
-    // Every wave reads all slices' parts: the row's largest value and its
-    // softmax sum, and a bound that its kmax-th value is not below, or failing
-    // that one that no candidate is below.  2^i slices with kmax / 2^i values
-    // each at a bound or above make a bound, so it is the 2^i-th largest of the
-    // slices' edge[i]: with eight slices of like values their eighth lets
-    // about kmax candidates through where one slice's own kmax-th would let
-    // eight times as many.
-    const bool have = lane < slices;
-    Part x = have ? parts[lane] : Part{NEG_INF, 0, 0.0, {NEG_INF, NEG_INF, NEG_INF, NEG_INF},
-                                       __builtin_inff(), 0.0f};
-    float top = x.top, least = x.count > 0 ? x.least : __builtin_inff(), best = x.edge[0];
-    for (int s = 64 + lane; s < slices; s += 64) {
-        top = fmaxf(top, parts[s].top);
-        if (parts[s].count > 0) least = fminf(least, parts[s].least);
-        best = fmaxf(best, parts[s].edge[0]);
-    }
-    top = wave_max(top);
-    least = wave_min(least);
-    float edge = wave_max(best);
-    if (slices > 1) {
-        const int level = slices >= 8 ? 3 : slices >= 4 ? 2 : 1;
-        float e = level == 3 ? x.edge[3] : level == 2 ? x.edge[2] : x.edge[1];
-        float m = NEG_INF;
-        for (int i = 0; i < 1 << level; ++i) {
-            m = wave_max(e);
-            if (lane == __builtin_ctzll(__ballot(e == m))) e = NEG_INF;
-        }
-        edge = fmaxf(edge, m);
-    }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         hist[i * THREADS + tid] = 0;
-        fill[i * THREADS + tid] = 0;
+        rest[i * THREADS + tid] = 0;
     }
     if (tid == 0) {
         taken = 0;
@@ -427,7 +486,12 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
     }
     sorted[tid] = 0;
     for (int i = tid; i < LIST; i += THREADS) list[i] = 0;
+    if (wave == 0) {
+        const RowParts r = join_parts(parts, slices, first, warm);
+        if (lane == 0) whole = r;
+    }
     __syncthreads();
+    const float top = whole.top, edge = whole.edge;
     if (!(top > NEG_INF)) {
         if (tid == 0) {
             a.ids[row] = -1;
@@ -435,58 +499,72 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         }
         return;
     }
-    if (!(edge > NEG_INF)) edge = least;
     // Counting sort by bins between the bound and the top, then by rank
-    // within a bin; bins that start at rank max_top_k or later are left out.
+    // within a bin; bins that start at rank kmax or later are left out.  A held
+    // candidate keeps the number it arrived with.
     const Bins bins(edge, top, JOIN_BINS);
-    each([&](uint64_t w) {
-        const float v = key_value((uint32_t)(w >> 32));
-        if (w != 0 && v >= edge) atomicAdd(&hist[bins.of(v, JOIN_BINS)], 1u);
+    auto value = [](uint64_t w) { return key_value((uint32_t)(w >> 32)); };
+    uint32_t arrival[HELD];
+#pragma unroll
+    for (int q = 0; q < HELD; ++q) {
+        uint32_t n = 0;
+        if (held[q] != 0 && value(held[q]) >= edge)
+            n = atomicAdd(&hist[bins.of(value(held[q]), JOIN_BINS)], 1u);
+        arrival[q] = n;
+    }
+    each_rest([&](uint64_t w) {
+        if (w != 0 && value(w) >= edge) atomicAdd(&rest[bins.of(value(w), JOIN_BINS)], 1u);
     });
     __syncthreads();
     // bins in descending order: thread i has those from JOIN_BINS - 1 - i * PER
-    uint32_t counts[PER], bin_sum = 0;
+    uint32_t held_count[PER], all_count[PER], bin_sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        counts[i] = hist[JOIN_BINS - 1 - tid * PER - i];
-        bin_sum += counts[i];
+        const int b = JOIN_BINS - 1 - tid * PER - i;
+        held_count[i] = hist[b];
+        all_count[i] = held_count[i] + rest[b];
+        bin_sum += all_count[i];
     }
     uint32_t start = wave_scan(bin_sum);
     if (lane == 63) wave_u[wave] = start;
     __syncthreads();
-    uint32_t earlier = lane < wave ? wave_u[lane & (WAVES - 1)] : 0u;
-    start += wave_sum(earlier) - bin_sum;
+    start -= bin_sum;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) start += w < wave ? wave_u[w] : 0u;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        hist[JOIN_BINS - 1 - tid * PER - i] = start;
-        if (start < (uint32_t)kmax && counts[i] > (uint32_t)CROWDED) crowded = 1;
-        start += counts[i];
+        const int b = JOIN_BINS - 1 - tid * PER - i;
+        hist[b] = start;
+        rest[b] = start + held_count[i];
+        if (start < (uint32_t)kmax && all_count[i] > (uint32_t)CROWDED) crowded = 1;
+        start += all_count[i];
+        ends[b] = start;
     }
     if (tid == THREADS - 1) inside = start;
     __syncthreads();
-    uint64_t mine;
     if (crowded == 0) {
-        each([&](uint64_t w) {
-            const float v = key_value((uint32_t)(w >> 32));
-            if (w != 0 && v >= edge) {
-                const int b = bins.of(v, JOIN_BINS);
-                const uint32_t first = hist[b];
-                // a bin that starts before kmax ends before LIST
-                if (first < (uint32_t)kmax) list[first + atomicAdd(&fill[b], 1u)] = w;
+        // a bin that starts before kmax ends before LIST
+#pragma unroll
+        for (int q = 0; q < HELD; ++q)
+            if (held[q] != 0 && value(held[q]) >= edge) {
+                const uint32_t at = hist[bins.of(value(held[q]), JOIN_BINS)];
+                if (at < (uint32_t)kmax) list[at + arrival[q]] = held[q];
+            }
+        each_rest([&](uint64_t w) {
+            if (w != 0 && value(w) >= edge) {
+                const int b = bins.of(value(w), JOIN_BINS);
+                if (hist[b] < (uint32_t)kmax) list[atomicAdd(&rest[b], 1u)] = w;
             }
         });
         __syncthreads();
         for (int i = tid; i < LIST; i += THREADS) {
             const uint64_t w = list[i];
             if (w == 0) break;
-            const int b = bins.of(key_value((uint32_t)(w >> 32)), JOIN_BINS);
-            const uint32_t first = hist[b], last = first + fill[b];
-            uint32_t rank = first;
-            for (uint32_t x = first; x < last; ++x) rank += list[x] > w ? 1u : 0u;
+            const int b = bins.of(value(w), JOIN_BINS);
+            uint32_t rank = hist[b];
+            for (uint32_t x = rank, last = ends[b]; x < last; ++x) rank += list[x] > w ? 1u : 0u;
             if (rank < (uint32_t)THREADS) sorted[rank] = w;
         }
-        __syncthreads();
-        mine = sorted[tid];
     } else {
         // Many values that are equal or nearly so: the kmax-th largest word,
         // digit by digit, and a sort of those from there up.
@@ -497,13 +575,13 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         } else {
             for (int shift = 56; shift >= 0; shift -= 8) {
                 __syncthreads();
-                if (tid < 256) fill[tid] = 0;
+                if (tid < 256) hist[tid] = 0;
                 __syncthreads();
                 each([&](uint64_t w) {
-                    if (w != 0 && (w & mask) == prefix) atomicAdd(&fill[(w >> shift) & 255], 1u);
+                    if (w != 0 && (w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
                 });
                 __syncthreads();
-                if (wave == 0) digit_of_rank(fill, left, chosen);
+                if (wave == 0) digit_of_rank(hist, left, chosen);
                 __syncthreads();
                 prefix |= (uint64_t)chosen[0] << shift;
                 mask |= 255ull << shift;
@@ -511,68 +589,117 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
             }
         }
         each([&](uint64_t w) {
-            if (w >= prefix && key_value((uint32_t)(w >> 32)) >= edge)
-                list[atomicAdd(&taken, 1u)] = w;
+            if (w >= prefix && value(w) >= edge) list[atomicAdd(&taken, 1u)] = w;
         });
         __syncthreads();
-        mine = list[tid];
         int p = 64;
         while (p < (int)taken) p <<= 1;
-        mine = sort_words(mine, p, list);
+        const uint64_t mine = sort_words(list[tid], p, list);
+        sorted[tid] = mine;
     }
+    __syncthreads();
 
-    // the softmax sum over the whole vocabulary, relative to the top
-    double sum = x.top > NEG_INF ? x.sum * exp(below_top(x.top, top) / (double)warm) : 0.0;
-    for (int s = 64 + lane; s < slices; s += 64)
-        if (parts[s].top > NEG_INF)
-            sum += parts[s].sum * exp(below_top(parts[s].top, top) / (double)warm);
-    sum = wave_sum(sum);
-    const bool there = tid < k && mine != 0;
-    const float z = key_value((uint32_t)(mine >> 32));
-    const double w = there ? exp(below_top(z, top) / (double)warm) : 0.0;
-    // Running sums of the candidates' weights; how many candidates there are,
-    // how many come before the sum reaches top_p of all, and how many have
-    // enough weight.
-    double cum = wave_scan(w), all = last_lane(cum);
-    const int in_k = __popcll(__ballot(there));
-    const int in_m = __popcll(__ballot(there && w >= min_p));
-    int j;
-    if (kmax <= 64) {
-        // they are all in the first wave
-        if (wave != 0) return;
-        const int in_p = __popcll(__ballot(there && cum < top_p * all));
-        const int keep = max(1, min(min(in_p + 1, in_m), in_k));
-        const double bound = uniform * __shfl(cum, keep - 1);
-        j = min(__popcll(__ballot(lane < keep && cum <= bound)), keep - 1);
-    } else {
-        const int other = lane & (WAVES - 1);
+    // The draw: four waves, or the first alone if it holds all candidates.
+    const bool single = kmax <= 64 * DRAW;
+    if (wave >= (single ? 1 : 4)) return;
+    uint64_t mine[DRAW];
+    bool there[DRAW];
+    double w[DRAW], cum[DRAW], run = 0.0;
+    int in_k = 0, in_m = 0;
+#pragma unroll
+    for (int i = 0; i < DRAW; ++i) {
+        mine[i] = sorted[tid * DRAW + i];
+        there[i] = tid * DRAW + i < k && mine[i] != 0;
+        w[i] = there[i] ? exp(below_top(value(mine[i]), top) / (double)warm) : 0.0;
+        run += w[i];
+        cum[i] = run;
+        in_k += __popcll(__ballot(there[i]));
+        in_m += __popcll(__ballot(there[i] && w[i] >= min_p));
+    }
+    // running sums of the candidates' weights
+    const double through = wave_scan(run);
+    double before = through - run, all = last_lane(through);
+    if (!single) {
         if (lane == 0) {
             wave_d[wave] = all;
             wave_i[0][wave] = in_k;
             wave_i[1][wave] = in_m;
         }
         __syncthreads();
-        const double part = lane < WAVES ? wave_d[other] : 0.0;
-        all = wave_sum(part);
-        cum += wave_sum(lane < wave ? part : 0.0);
-        const int in_p = __popcll(__ballot(there && cum < top_p * all));
+        all = 0.0;
+        in_k = in_m = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (x < wave) before += wave_d[x];
+            all += wave_d[x];
+            in_k += wave_i[0][x];
+            in_m += wave_i[1][x];
+        }
+    }
+    // how many come before the sum reaches top_p of all
+    int in_p = 0;
+#pragma unroll
+    for (int i = 0; i < DRAW; ++i) {
+        cum[i] += before;
+        in_p += __popcll(__ballot(there[i] && cum[i] < top_p * all));
+    }
+    if (!single) {
         if (lane == 0) wave_i[2][wave] = in_p;
         __syncthreads();
-        const int count = wave_sum(lane < WAVES ? wave_i[0][other] : 0);
-        const int large_n = wave_sum(lane < WAVES ? wave_i[1][other] : 0);
-        const int short_n = wave_sum(lane < WAVES ? wave_i[2][other] : 0) + 1;
-        const int keep = max(1, min(min(short_n, large_n), count));
-        if (tid == keep - 1) kept = cum;
-        __syncthreads();
-        const int passed = __popcll(__ballot(tid < keep && cum <= uniform * kept));
-        if (lane == 0) wave_i[0][wave] = passed;
-        __syncthreads();
-        j = min(wave_sum(lane < WAVES ? wave_i[0][other] : 0), keep - 1);
+        in_p = wave_i[2][0] + wave_i[2][1] + wave_i[2][2] + wave_i[2][3];
     }
-    if (!(t > 0.0f)) j = 0;
-    if (tid == j) {
-        a.ids[row] = (int32_t)~(uint32_t)mine;
-        a.logprobs[row] = (float)(below_top(z, top) / (double)warm - log(sum));
+    const int keep = max(1, min(min(in_p + 1, in_m), in_k));
+#pragma unroll
+    for (int i = 0; i < DRAW; ++i)
+        if (tid * DRAW + i == keep - 1) kept = cum[i];
+    if (single) wave_fence();
+    else __syncthreads();
+    const double bound = uniform * kept;
+    int j = 0;
+#pragma unroll
+    for (int i = 0; i < DRAW; ++i)
+        j += __popcll(__ballot(tid * DRAW + i < keep && cum[i] <= bound));
+    if (!single) {
+        if (lane == 0) wave_i[0][wave] = j;
+        __syncthreads();
+        j = wave_i[0][0] + wave_i[0][1] + wave_i[0][2] + wave_i[0][3];
+    }
+    j = t > 0.0f ? min(j, keep - 1) : 0;
+#pragma unroll
+    for (int i = 0; i < DRAW; ++i)
+        if (tid * DRAW + i == j) {
+            a.ids[row] = (int32_t)~(uint32_t)mine[i];
+            a.logprobs[row] = (float)(below_top(value(mine[i]), top) / (double)warm -
+                                      log(whole.sum));
+        }
+}
+
+// max_top_k = 1: the largest of the slices' best words; one wave per row.
+constexpr int FT = 256;
+__global__ __launch_bounds__(FT) void first_kernel(PickArgs a, int slices, const Part *parts,
+                                                   const uint64_t *found) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row = (int64_t)blockIdx.x * (FT / 64) + (threadIdx.x >> 6);
+    if (row >= a.rows) return;  // no barrier follows
+    const int cap = slice_cap(1);
+    parts += row * slices;
+    found += row * slices * cap;
+    const Part first = lane_part(parts, slices);
+    uint64_t best = lane < slices ? found[lane * cap] : 0ull;
+    const float warm = warmth(parameter(a.temperature, row, 1.0f, a.uniform));
+    if (first.count == 0) best = 0;
+    for (int s = 64 + lane; s < slices; s += 64) {
+        const uint64_t w = found[s * cap];
+        if (parts[s].count > 0 && w > best) best = w;
+    }
+    const RowParts r = join_parts(parts, slices, first, warm);
+    // the high words' largest, then the low words' largest among those
+    const uint32_t high = (uint32_t)wave_max((int)((uint32_t)(best >> 32) ^ 0x80000000u)) ^ 0x80000000u;
+    const uint32_t low = (uint32_t)(best >> 32) == high ? (uint32_t)best : 0u;
+    const uint32_t token = ~((uint32_t)wave_max((int)(low ^ 0x80000000u)) ^ 0x80000000u);
+    if (lane == 0) {
+        a.ids[row] = high != 0u ? (int32_t)token : -1;
+        a.logprobs[row] = high != 0u ? (float)-log(r.sum) : NEG_INF;
     }
 }
 
@@ -589,10 +716,11 @@ size_t parts_bytes(int64_t rows, int slices) {
     return ((size_t)rows * slices * sizeof(Part) + 255) / 256 * 256;
 }
 
-template <typename T, int THREADS, int VALUES, int GROUP>
+template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST = false>
 void run_slices(const PickArgs &a, int slices, Part *parts, uint64_t *found, hipStream_t stream) {
     const dim3 grid((unsigned)a.rows, (unsigned)slices);
-    slice_kernel<T, THREADS, VALUES, GROUP><<<grid, THREADS, 0, stream>>>(a, parts, found);
+    slice_kernel<T, THREADS, VALUES, GROUP, FIRST>
+        <<<grid, THREADS, 0, stream>>>(a, parts, found);
 }
 
 template <typename T>
@@ -601,11 +729,19 @@ void run(const PickArgs &a, hipStream_t stream) {
     Part *parts = static_cast<Part *>(a.workspace);
     uint64_t *found = reinterpret_cast<uint64_t *>(static_cast<char *>(a.workspace) +
                                                    parts_bytes(a.rows, slices));
+    const bool wide = wide_slices(a.rows, a.vocab);
+    if (a.max_top_k == 1) {
+        if (wide) run_slices<T, 512, 32, 32, true>(a, slices, parts, found, stream);
+        else run_slices<T, 256, 8, 8, true>(a, slices, parts, found, stream);
+        first_kernel<<<(unsigned)((a.rows + FT / 64 - 1) / (FT / 64)), FT, 0, stream>>>(
+            a, slices, parts, found);
+        return;
+    }
     // Groups of the histogram: at least four for each of max_top_k, so that
     // the k-th largest group bounds the k-th value closely (of values without
     // order about 1.15 k lie above it).
-    if (wide_slices(a.rows, a.vocab)) {
-        if (a.max_top_k <= 256) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
+    if (wide) {
+        if (a.max_top_k <= 128) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
         else run_slices<T, 512, 32, 4>(a, slices, parts, found, stream);
     } else {
         if (a.max_top_k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);

@@ -249,6 +249,17 @@ __device__ __forceinline__ void clear_counts(const RouteArgs &a) {
         for (int e = threadIdx.x; e < a.experts; e += RT) a.counts[e] = 0;
 }
 
+// Or, where the launch is one workgroup, counts the experts of all tokens,
+// whose ids it has written itself.
+__device__ __forceinline__ void count_here(const RouteArgs &a) {
+    __syncthreads();
+    const int n = (int)a.tokens * a.opt.top_k;
+    for (int i = threadIdx.x; i < n; i += RT) {
+        const int id = a.ids[i];
+        if (id >= 0) atomicAdd(a.counts + id, 1);
+    }
+}
+
 template <typename T>
 __global__ __launch_bounds__(RT) void exact_kernel(RouteArgs a) {
     __shared__ ExactSpace<NMS_ROUTE_MAX_EXPERTS> space[RWAVES];
@@ -501,6 +512,7 @@ __global__ __launch_bounds__(RT) void quick_kernel(RouteArgs a, int group_lanes)
         id = exact_token<T>(a, one, space[threadIdx.x >> 6]);
         write_token<T, 64>(a, one, true, lane, id, __shfl(top, first), __shfl(sum, first));
     }
+    if (a.counts != nullptr && gridDim.x == 1) count_here(a);
 }
 
 // Adds the experts of ids[0..n) to the counts; a single workgroup writes them.
@@ -676,11 +688,13 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
 
 // ----------------------------------------------------------------- launches
 
+// Each returns whether the launch has counted the experts.
 template <typename T, int LANES, int VALUES>
-void run_quick(const RouteArgs &a, int group_lanes, hipStream_t stream) {
+bool run_quick(const RouteArgs &a, int group_lanes, hipStream_t stream) {
     constexpr int per = RWAVES * (64 / LANES);
-    quick_kernel<T, LANES, VALUES>
-        <<<(unsigned)((a.tokens + per - 1) / per), RT, 0, stream>>>(a, group_lanes);
+    const unsigned grid = (unsigned)((a.tokens + per - 1) / per);
+    quick_kernel<T, LANES, VALUES><<<grid, RT, 0, stream>>>(a, group_lanes);
+    return grid == 1;
 }
 
 // Whether quick_kernel<., lanes, values> holds the shape, and over how many
@@ -695,14 +709,15 @@ bool holds(const RouteArgs &a, int lanes, int values, int *group_lanes) {
 }
 
 template <typename T>
-void run_route(const RouteArgs &a, hipStream_t stream) {
+bool run_route(const RouteArgs &a, hipStream_t stream) {
     int g = 1;
-    if (holds(a, 16, 4, &g)) run_quick<T, 16, 4>(a, g, stream);
-    else if (holds(a, 16, 8, &g)) run_quick<T, 16, 8>(a, g, stream);
-    else if (holds(a, 16, 16, &g)) run_quick<T, 16, 16>(a, g, stream);
-    else if (holds(a, 64, 4, &g)) run_quick<T, 64, 4>(a, g, stream);
-    else if (holds(a, 64, 16, &g)) run_quick<T, 64, 16>(a, g, stream);
-    else exact_kernel<T><<<(unsigned)((a.tokens + RWAVES - 1) / RWAVES), RT, 0, stream>>>(a);
+    if (holds(a, 16, 4, &g)) return run_quick<T, 16, 4>(a, g, stream);
+    if (holds(a, 16, 8, &g)) return run_quick<T, 16, 8>(a, g, stream);
+    if (holds(a, 16, 16, &g)) return run_quick<T, 16, 16>(a, g, stream);
+    if (holds(a, 64, 4, &g)) return run_quick<T, 64, 4>(a, g, stream);
+    if (holds(a, 64, 16, &g)) return run_quick<T, 64, 16>(a, g, stream);
+    exact_kernel<T><<<(unsigned)((a.tokens + RWAVES - 1) / RWAVES), RT, 0, stream>>>(a);
+    return false;
 }
 
 template <typename T, int LANES, int VALUES>
@@ -722,12 +737,13 @@ void run_back(const RouteBackArgs &a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
+    bool counted = false;
     if (a.tokens > 0) {
-        if (a.dtype == NMS_F32) run_route<float>(a, stream);
-        else if (a.dtype == NMS_F16) run_route<half_t>(a, stream);
-        else run_route<bf16_t>(a, stream);
+        if (a.dtype == NMS_F32) counted = run_route<float>(a, stream);
+        else if (a.dtype == NMS_F16) counted = run_route<half_t>(a, stream);
+        else counted = run_route<bf16_t>(a, stream);
     }
-    if (a.counts != nullptr) {
+    if (a.counts != nullptr && !counted) {
         const int64_t n = a.tokens * a.opt.top_k, groups = (n + COUNTED - 1) / COUNTED;
         count_kernel<<<(unsigned)(groups < 1 ? 1 : groups > 256 ? 256 : groups), CT, 0, stream>>>(
             a.ids, n, a.experts, a.counts);

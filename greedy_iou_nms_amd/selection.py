@@ -16,7 +16,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check, _lib, _OnDevice, _raw_stream
+from . import Workspace, _check, _default_workspace, _lib, _OnDevice, _raw_stream
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # nms_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}  # NMS_ROUTE_SOFTMAX, NMS_ROUTE_SIGMOID
@@ -297,13 +297,15 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     ref = None if rules is None else rules._for(rows, vocab, device)
     with _OnDevice(device):
         nbytes = pick_workspace_size(rows, vocab, max_top_k)
-        # from torch's allocator, not a kept Workspace: calls on other streams
-        # and captured graphs must not share one
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        # kept per thread and stream; a captured call takes one of its own from
+        # the graph's memory, so that no two graphs share it
+        stream = _raw_stream(device)
+        kept = (Workspace(device) if torch.cuda.is_current_stream_capturing()
+                else _default_workspace(device, stream))
+        buf = kept.get(nbytes, device)
         ids = torch.empty(rows, dtype=torch.int32, device=device)
         logprobs = torch.empty(rows, dtype=f32, device=device)
         _check(_lib.nms_pick_tokens(logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, stride,
                                     ref, u, t, k, p, m, max_top_k, ids.data_ptr(),
-                                    logprobs.data_ptr(), buf.data_ptr(), nbytes,
-                                    _raw_stream(device)))
+                                    logprobs.data_ptr(), buf.data_ptr(), nbytes, stream))
     return ids, logprobs
