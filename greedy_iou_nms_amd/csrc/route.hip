@@ -12,10 +12,10 @@
 // value's distance from the token's largest and 10 bits of the index, so that
 // a comparison, a sort step and a maximum over lanes are one or two
 // instructions each.  It knows how far a key may be off; a token with two
-// candidates that its keys cannot order, and that are not equal, is chosen by
-// exact_token, in binary64 (about one in 500 where scores have no ties).
-// exact_kernel is exact_token for every token, for shapes that the first form
-// does not hold.
+// candidates that its keys cannot order, and that are not equal, is chosen
+// again from binary64 scores, by its wave (about one token in 500 where scores
+// have no ties).  exact_kernel does all in binary64, a wave per token, for
+// shapes that the first form does not hold.
 #include "select_internal.h"
 
 namespace gnms {
@@ -86,11 +86,10 @@ __device__ __forceinline__ double exp_below(float z, float top, EXP e) {
 
 // ------------------------------------------------- one token, in binary64
 
-// What a wave needs of LDS for rows of up to N experts.
-template <int N>
+// What a wave needs of LDS for it.
 struct ExactSpace {
-    double c[N];
-    uint8_t kept[N];
+    double c[NMS_ROUTE_MAX_EXPERTS];
+    uint8_t kept[NMS_ROUTE_MAX_EXPERTS];
 };
 
 // The largest value above -infinity that the lanes know, and the lowest place
@@ -109,8 +108,8 @@ __device__ __forceinline__ void wave_best(double &v, int &at) {
 
 // Chooses the experts of token t: lane i gets the i-th one's index, or -1.
 // Every loop is over LDS and rolled, so that it takes few registers.
-template <typename T, int N>
-__device__ __forceinline__ int exact_token(const RouteArgs &a, int64_t t, ExactSpace<N> &x) {
+template <typename T>
+__device__ __forceinline__ int exact_token(const RouteArgs &a, int64_t t, ExactSpace &x) {
     const int lane = threadIdx.x & 63;
     const int E = a.experts, G = a.opt.groups, size = E / G;
     const T *row = static_cast<const T *>(a.logits) + t * a.row_stride;
@@ -262,7 +261,7 @@ __device__ __forceinline__ void count_here(const RouteArgs &a) {
 
 template <typename T>
 __global__ __launch_bounds__(RT) void exact_kernel(RouteArgs a) {
-    __shared__ ExactSpace<NMS_ROUTE_MAX_EXPERTS> space[RWAVES];
+    __shared__ ExactSpace space[RWAVES];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * RWAVES + wave;
     clear_counts(a);
@@ -314,12 +313,90 @@ __device__ __forceinline__ uint32_t short_key(T v) {
     return to_f32(v) > NEG_INF ? k : 0u;
 }
 
+// 1 / x for x in [1, infinity].
+__device__ __forceinline__ double inverse_of(double x) {
+    double r = __builtin_amdgcn_rcp(x);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    return x < 1.0e300 ? r : 0.0;
+}
+
+// The choice of quick_kernel for a wave's tokens, from binary64 scores (good
+// to 2^-40): lane i of a token gets its i-th expert, or -1.  z: the lane's
+// logits, -infinity where there is none; bias: the lane's, or 0.
+template <int LANES, int VALUES>
+__device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z,
+                                              const float *bias, float top, double sum,
+                                              int group_lanes) {
+    const int lane = threadIdx.x & 63, sub = lane % LANES;
+    const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX, biased = a.bias != nullptr;
+    const double share = inverse_of(sum);
+    double r[VALUES];  // what the experts are ordered by
+    double b0 = LOWEST, b1 = LOWEST;
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j) {
+        double c = softmax ? exp_below(z[j], top, [](double v) { return exp_of(v); }) * share
+                           : inverse_of(1.0 + exp_of(-(double)z[j]));
+        c += (double)bias[j];
+        if (!(z[j] > NEG_INF && c > LOWEST)) c = LOWEST;
+        b1 = c > b0 ? b0 : c > b1 ? c : b1;
+        b0 = c > b0 ? c : b0;
+        r[j] = biased || c == LOWEST ? c : (double)z[j];
+    }
+    if (a.opt.groups > 1) {
+        auto merge = [&](double o0, double o1) {
+            b1 = fmax(fmin(b0, o0), fmax(b1, o1));
+            b0 = fmax(b0, o0);
+        };
+        if (group_lanes >= 2) merge(dpp<0xB1, 0xf>(b0, b0), dpp<0xB1, 0xf>(b1, b1));
+        if (group_lanes >= 4) merge(dpp<0x4E, 0xf>(b0, b0), dpp<0x4E, 0xf>(b1, b1));
+        if (group_lanes >= 8) merge(dpp<0x141, 0xf>(b0, b0), dpp<0x141, 0xf>(b1, b1));
+        if (group_lanes >= 16) merge(dpp<0x140, 0xf>(b0, b0), dpp<0x140, 0xf>(b1, b1));
+        if (group_lanes >= 32) merge(__shfl_xor(b0, 16), __shfl_xor(b1, 16));
+        const double score = a.opt.group_top == 2 && b1 > LOWEST ? b0 + b1 : b0;
+        int before = 0;
+        for (int o = group_lanes; o < LANES; o += group_lanes) {
+            const int from = (sub + o) % LANES;
+            const double other = __shfl(score, lane - sub + from);
+            before += other > score || (other == score && from < sub) ? 1 : 0;
+        }
+        if (before >= a.opt.kept_groups) {
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) r[j] = LOWEST;
+        }
+    }
+    int mine = -1;
+#pragma unroll 1
+    for (int i = 0; i < a.opt.top_k; ++i) {
+        double v = r[0];
+        int at = sub * VALUES;
+#pragma unroll
+        for (int j = 1; j < VALUES; ++j)
+            if (r[j] > v) {
+                v = r[j];
+                at = sub * VALUES + j;
+            }
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) {
+            const double v2 = __shfl_xor(v, d);
+            const int at2 = __shfl_xor(at, d);
+            const bool take = v2 > v || (v2 == v && at2 < at);
+            v = take ? v2 : v;
+            at = take ? at2 : at;
+        }
+        if (sub == i && v > LOWEST) mine = at;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j)
+            if (at == sub * VALUES + j) r[j] = LOWEST;
+    }
+    return mine;
+}
+
 // LANES lanes share a token, VALUES experts each: lane l has the experts
 // VALUES * l and on.  top_k is at most LANES.
 template <typename T, int LANES, int VALUES>
-__global__ __launch_bounds__(RT) void quick_kernel(RouteArgs a, int group_lanes) {
+__global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lanes) {
     constexpr int TOKENS = 64 / LANES;  // per wave
-    __shared__ ExactSpace<LANES * VALUES> space[RWAVES];
     const int lane = threadIdx.x & 63, sub = lane % LANES;
     const int64_t t = ((int64_t)blockIdx.x * RWAVES + (threadIdx.x >> 6)) * TOKENS + lane / LANES;
     const bool inside = t < a.tokens;
@@ -362,20 +439,31 @@ __global__ __launch_bounds__(RT) void quick_kernel(RouteArgs a, int group_lanes)
     // Keys.  margin: two candidates whose q differ by no more may be in either
     // order, unless they are equal; negative: the keys are exact.
     uint32_t key[VALUES];
+    float bias[VALUES];
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j) bias[j] = 0.0f;
     int margin = 0;
-    bool bad = false;  // the token needs exact_token
+    bool bad = false;  // the token has to be chosen exactly
     if (scored) {
         // c in float32: a sigmoid or a softmax share is off by less than
         // 3 * 2^-23, and its sum with a bias by |c| 2^-24 more; the scale is
         // 2^22, and q is rounded twice
+        if (a.bias != nullptr) {
+            if (e0 + VALUES <= E) {
+                __builtin_memcpy(bias, a.bias + e0, sizeof(bias));
+            } else {
+#pragma unroll
+                for (int j = 0; j < VALUES; ++j) bias[j] = e0 + j < E ? a.bias[e0 + j] : 0.0f;
+            }
+        }
         float c[VALUES], c_top = NEG_INF;
-        const float share = (float)(1.0 / sum);
+        const float share = (float)inverse_of(sum);
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) {
             const float s = softmax ? __builtin_amdgcn_exp2f((z[j] - top) * 1.44269504f) * share
                                     : __builtin_amdgcn_rcpf(
                                           1.0f + __builtin_amdgcn_exp2f(z[j] * -1.44269504f));
-            c[j] = s + (a.bias != nullptr && e0 + j < E ? a.bias[e0 + j] : 0.0f);
+            c[j] = s + bias[j];
             if (!(z[j] > NEG_INF && c[j] > NEG_INF)) c[j] = NEG_INF;
             c_top = fmaxf(c_top, c[j]);
         }
@@ -504,14 +592,11 @@ __global__ __launch_bounds__(RT) void quick_kernel(RouteArgs a, int group_lanes)
     } else {
         bad = false;
     }
-    if (!live) id = -1;
-    write_token<T, LANES>(a, tok, inside && !bad, sub, id, top, sum);
-    for (uint64_t left = __ballot(bad && sub == 0); left != 0ull; left &= left - 1ull) {
-        const int first = __builtin_ctzll(left);
-        const int64_t one = __shfl((long long)tok, first);
-        id = exact_token<T>(a, one, space[threadIdx.x >> 6]);
-        write_token<T, 64>(a, one, true, lane, id, __shfl(top, first), __shfl(sum, first));
+    if (__ballot(bad) != 0ull) {
+        const int exact = choose_exactly<LANES, VALUES>(a, z, bias, top, sum, group_lanes);
+        if (bad) id = exact;
     }
+    write_token<T, LANES>(a, tok, inside, sub, live ? id : -1, top, sum);
     if (a.counts != nullptr && gridDim.x == 1) count_here(a);
 }
 
