@@ -78,6 +78,14 @@ __device__ __forceinline__ double exp_of(double x) {
     return __builtin_amdgcn_ldexp(p, (int)n);
 }
 
+// 1 / x for x from 1e-290, to 2^-50; 0 from 1e300 on.
+__device__ __forceinline__ double inverse_of(double x) {
+    double r = __builtin_amdgcn_rcp(x);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+    return x < 1.0e300 ? r : 0.0;
+}
+
 // exp(z - top), 1 at z = top (infinite ones too), 0 at -infinity.
 template <typename EXP>
 __device__ __forceinline__ double exp_below(float z, float top, EXP e) {
@@ -219,7 +227,9 @@ __device__ __forceinline__ void write_token(const RouteArgs &a, int64_t t, bool 
         w = id >= 0 ? 1.0 / (1.0 + e(-(double)z)) : 0.0;
         sum = a.opt.renormalise ? all_sum<LANES>(w) : 1.0;
     }
-    w = sum > 0.0 ? w / sum : 0.0;
+    // (a quotient where the inverse is out of range)
+    if (__builtin_expect(__ballot(!(sum > 1.0e-290)) == 0ull, 1)) w *= inverse_of(sum);
+    else w = sum > 0.0 ? w / sum : 0.0;
     if (write && place < a.opt.top_k) {
         a.ids[t * a.opt.top_k + place] = id;
         a.weights[t * a.opt.top_k + place] = (float)(w * (double)a.opt.scale);
@@ -302,6 +312,14 @@ __device__ __forceinline__ uint32_t with_index(uint32_t q, int e) {
     return q << INDEX_BITS | (INDEX_MASK - (uint32_t)e);
 }
 
+// A whole number from a float at most Q_TOP; 0 below 1 and for a NaN, as
+// v_cvt_u32_f32 gives (C leaves it open).
+__device__ __forceinline__ uint32_t saturated(float q) {
+    uint32_t r;
+    asm("v_cvt_u32_f32 %0, %1" : "=v"(r) : "v"(q));
+    return r;
+}
+
 // The 16-bit types' order in 16 bits (-0 folded onto +0), 0 for -infinity and
 // NaN.
 template <typename T>
@@ -311,14 +329,6 @@ __device__ __forceinline__ uint32_t short_key(T v) {
     if (u == 0x8000u) u = 0;
     const uint32_t k = (u & 0x8000u) ? (uint16_t)~u : (uint32_t)(u | 0x8000u);
     return to_f32(v) > NEG_INF ? k : 0u;
-}
-
-// 1 / x for x in [1, infinity].
-__device__ __forceinline__ double inverse_of(double x) {
-    double r = __builtin_amdgcn_rcp(x);
-    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
-    r = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
-    return x < 1.0e300 ? r : 0.0;
 }
 
 // The choice of quick_kernel for a wave's tokens, from binary64 scores (good
@@ -416,15 +426,20 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
     }
     float z[VALUES], top = NEG_INF;
 #pragma unroll
-    for (int j = 0; j < VALUES; ++j) {
-        const float v = to_f32(raw[j]);
-        z[j] = v > NEG_INF ? v : NEG_INF;
-        top = fmaxf(top, z[j]);
-    }
+    for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw[j]);
     const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX;
     const bool grouped = a.opt.groups > 1, scored = a.bias != nullptr || grouped;
     const bool whole = softmax && (scored || !a.opt.renormalise);
-    top = unordered(all_max<LANES>(ordered(top)));
+    // the largest logit, where scores or keys are relative to it
+    const bool relative = whole || (!scored && sizeof(T) == 4);
+    if (relative) {
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) {
+            z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
+            top = fmaxf(top, z[j]);
+        }
+        top = unordered(all_max<LANES>(ordered(top)));
+    }
 
     // the softmax sum, which the weights need to 2^-24 and better
     double sum = 1.0;
@@ -457,42 +472,44 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
             }
         }
         float c[VALUES], c_top = NEG_INF;
-        const float share = (float)inverse_of(sum);
+        if (softmax) {
+            const float share = (float)inverse_of(sum);
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j)
+                c[j] = __builtin_amdgcn_exp2f((z[j] - top) * 1.44269504f) * share;
+        } else {
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j)
+                c[j] = __builtin_amdgcn_rcpf(1.0f +
+                                             __builtin_amdgcn_exp2f(z[j] * -1.44269504f));
+        }
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) {
-            const float s = softmax ? __builtin_amdgcn_exp2f((z[j] - top) * 1.44269504f) * share
-                                    : __builtin_amdgcn_rcpf(
-                                          1.0f + __builtin_amdgcn_exp2f(z[j] * -1.44269504f));
-            c[j] = s + bias[j];
-            if (!(z[j] > NEG_INF && c[j] > NEG_INF)) c[j] = NEG_INF;
+            c[j] = z[j] > NEG_INF ? c[j] + bias[j] : NEG_INF;
             c_top = fmaxf(c_top, c[j]);
         }
         c_top = unordered(all_max<LANES>(ordered(c_top)));
-        bad = !(fabsf(c_top) < 64.0f) || !(fabsf(top) < 3.0e38f);
+        bad = !(fabsf(c_top) < 64.0f) || (softmax && !(fabsf(top) < 3.0e38f));
         margin = 8 + (int)fabsf(bad ? 0.0f : c_top);
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) {
-            const float q = fmaxf((c[j] - c_top) * 4194304.0f + (float)Q_TOP, 1.0f);
-            key[j] = c[j] > NEG_INF ? with_index((uint32_t)q, e0 + j) : 0u;
-        }
+        for (int j = 0; j < VALUES; ++j)
+            key[j] = with_index(saturated(__builtin_fmaf(c[j] - c_top, 4194304.0f, (float)Q_TOP)),
+                                e0 + j);
+        if (c_top == NEG_INF) bad = false;
     } else if (sizeof(T) == 2) {
         margin = -1;
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) {
-            const uint32_t q = short_key(raw[j]);
-            key[j] = q != 0u ? with_index(q, e0 + j) : 0u;
+            key[j] = with_index(short_key(raw[j]), e0 + j);
         }
     } else {
         // z down to 64 below the top, monotone: only equal q are open
-        bad = !(fabsf(top) < 3.0e38f);
+        bad = !(fabsf(top) < 3.0e38f) && top != NEG_INF;
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) {
-            const float q = fmaxf((z[j] - top) * 65536.0f + (float)Q_TOP, 1.0f);
-            key[j] = z[j] > NEG_INF ? with_index((uint32_t)q, e0 + j) : 0u;
-        }
+        for (int j = 0; j < VALUES; ++j)
+            key[j] = with_index(saturated(__builtin_fmaf(z[j] - top, 65536.0f, (float)Q_TOP)),
+                                e0 + j);
     }
-    // a row without eligible experts has nothing to choose from
-    if (top == NEG_INF) bad = false;
     sort_keys<VALUES>(key);
 
     if (grouped) {
@@ -514,7 +531,7 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         const uint32_t q0 = b0 >> INDEX_BITS, q1 = b1 >> INDEX_BITS;
         // a group with one expert where others sum two, or one that reaches
         // the keys' end
-        if (group && q0 != 0u && (q0 <= 1u || (two && q1 <= 1u))) bad = true;
+        if (group && two && q0 != 0u && q1 == 0u) bad = true;
         const uint32_t score = group ? q0 + (two ? q1 : 0u) : 0u;
         const uint32_t ranked = score << 6 | (uint32_t)(63 - g);
         int larger = 0;
@@ -533,7 +550,7 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         // how close the choice of the groups was
         const uint32_t least = all_min<LANES>(kept ? score : 0xffffffffu);
         const uint32_t most = all_max<LANES>(kept ? 0u : score);
-        if (most != 0u && least - most <= (uint32_t)(2 * margin)) bad = true;
+        if (least - most <= (uint32_t)(2 * margin)) bad = true;
         if (!kept) {
 #pragma unroll
             for (int j = 0; j < VALUES; ++j) key[j] = 0u;
@@ -541,7 +558,7 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
     }
 
     // The largest key of all lanes, top_k times; the lane that has it moves
-    // its next one up.
+    // its next one up.  Keys without a value are below 2^INDEX_BITS.
     uint32_t mine = 0u, last = 0u;
     bool close = false;
     auto next = [&]() -> uint32_t {
@@ -551,15 +568,23 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
             for (int j = 0; j + 1 < VALUES; ++j) key[j] = key[j + 1];
             key[VALUES - 1] = 0u;
         }
-        return m;
+        return m <= INDEX_MASK ? 0u : m;
     };
     for (int i = 0; i < k; ++i) {
         const uint32_t m = next();
-        // an end of the keys that a candidate lies at, or two that are close
-        close |= m != 0u && ((int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin && i > 0);
-        if (margin >= 0 && m != 0u && (m >> INDEX_BITS) <= 1u) bad = true;
+        close |= i > 0 && m != 0u && (int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin;
         if (sub == i) mine = m;
         last = m;
+    }
+    // Nothing left, or nearly at the keys' end: there is no further eligible
+    // expert, or one below what keys reach.
+    const bool at_end = margin >= 0 && (int)(last >> INDEX_BITS) <= margin;
+    if (__ballot(at_end) != 0ull) {
+        bool low = false;
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j)
+            low |= z[j] > NEG_INF && bias[j] > NEG_INF && e0 + j < E;
+        if (at_end && low) bad = true;
     }
     int id = mine != 0u ? (int)(INDEX_MASK - (mine & INDEX_MASK)) : -1;
     // Candidates that are close must be equal, in their logits and biases; the
@@ -593,6 +618,8 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         bad = false;
     }
     if (__ballot(bad) != 0ull) {
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
         const int exact = choose_exactly<LANES, VALUES>(a, z, bias, top, sum, group_lanes);
         if (bad) id = exact;
     }
