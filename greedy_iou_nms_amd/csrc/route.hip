@@ -27,14 +27,39 @@ constexpr double LOWEST = -__builtin_inf();
 
 // ---------------------------------------- reductions over 4 .. 64 lanes
 
+// A DPP move that reaches every lane (permutations and mirrors within 16
+// lanes), which the compiler can make part of the instruction that uses it.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ int moved(int v) {
+    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float moved(float v) {
+    return __int_as_float(moved<CTRL>(__float_as_int(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t x = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)moved<CTRL>((uint32_t)(x >> 32)) << 32 |
+                                            moved<CTRL>((uint32_t)x)));
+}
+
+constexpr int XOR1 = 0xB1, XOR2 = 0x4E;            // quads permuted
+constexpr int MIRROR8 = 0x141, MIRROR16 = 0x140;   // lanes in reverse order
+constexpr int ROTATE = 0x120;                      // + n: by n lanes within 16
+
 // Combines with every lane of the aligned N lanes; the result is in all of
 // them.  Mirrors serve as butterfly steps once the halves agree.
 template <int N, typename V, typename F>
 __device__ __forceinline__ V all_lanes(V v, F f) {
-    if (N >= 2) v = f(v, dpp<0xB1, 0xf>(v, v));    // lane ^ 1
-    if (N >= 4) v = f(v, dpp<0x4E, 0xf>(v, v));    // lane ^ 2
-    if (N >= 8) v = f(v, dpp<0x141, 0xf>(v, v));   // mirrored in 8
-    if (N >= 16) v = f(v, dpp<0x140, 0xf>(v, v));  // mirrored in 16
+    if (N >= 2) v = f(v, moved<XOR1>(v));
+    if (N >= 4) v = f(v, moved<XOR2>(v));
+    if (N >= 8) v = f(v, moved<MIRROR8>(v));
+    if (N >= 16) v = f(v, moved<MIRROR16>(v));
     if (N >= 32) v = f(v, __shfl_xor(v, 16));
     if (N >= 64) v = f(v, __shfl_xor(v, 32));
     return v;
@@ -86,10 +111,11 @@ __device__ __forceinline__ double inverse_of(double x) {
     return x < 1.0e300 ? r : 0.0;
 }
 
-// exp(z - top), 1 at z = top (infinite ones too), 0 at -infinity.
+// exp(z - top), 1 at z = top (infinite ones too); no branches.
 template <typename EXP>
 __device__ __forceinline__ double exp_below(float z, float top, EXP e) {
-    return z == top ? 1.0 : z == NEG_INF ? 0.0 : e((double)z - (double)top);
+    const double d = (double)z - (double)top;
+    return e(z == top ? 0.0 : d);
 }
 
 // ------------------------------------------------- one token, in binary64
@@ -358,10 +384,10 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z
             b1 = fmax(fmin(b0, o0), fmax(b1, o1));
             b0 = fmax(b0, o0);
         };
-        if (group_lanes >= 2) merge(dpp<0xB1, 0xf>(b0, b0), dpp<0xB1, 0xf>(b1, b1));
-        if (group_lanes >= 4) merge(dpp<0x4E, 0xf>(b0, b0), dpp<0x4E, 0xf>(b1, b1));
-        if (group_lanes >= 8) merge(dpp<0x141, 0xf>(b0, b0), dpp<0x141, 0xf>(b1, b1));
-        if (group_lanes >= 16) merge(dpp<0x140, 0xf>(b0, b0), dpp<0x140, 0xf>(b1, b1));
+        if (group_lanes >= 2) merge(moved<XOR1>(b0), moved<XOR1>(b1));
+        if (group_lanes >= 4) merge(moved<XOR2>(b0), moved<XOR2>(b1));
+        if (group_lanes >= 8) merge(moved<MIRROR8>(b0), moved<MIRROR8>(b1));
+        if (group_lanes >= 16) merge(moved<MIRROR16>(b0), moved<MIRROR16>(b1));
         if (group_lanes >= 32) merge(__shfl_xor(b0, 16), __shfl_xor(b1, 16));
         const double score = a.opt.group_top == 2 && b1 > LOWEST ? b0 + b1 : b0;
         int before = 0;
@@ -520,10 +546,10 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
             b1 = max(min(b0, o0), max(b1, o1));
             b0 = max(b0, o0);
         };
-        if (group_lanes >= 2) merge(dpp<0xB1, 0xf>(b0, b0), dpp<0xB1, 0xf>(b1, b1));
-        if (group_lanes >= 4) merge(dpp<0x4E, 0xf>(b0, b0), dpp<0x4E, 0xf>(b1, b1));
-        if (group_lanes >= 8) merge(dpp<0x141, 0xf>(b0, b0), dpp<0x141, 0xf>(b1, b1));
-        if (group_lanes >= 16) merge(dpp<0x140, 0xf>(b0, b0), dpp<0x140, 0xf>(b1, b1));
+        if (group_lanes >= 2) merge(moved<XOR1>(b0), moved<XOR1>(b1));
+        if (group_lanes >= 4) merge(moved<XOR2>(b0), moved<XOR2>(b1));
+        if (group_lanes >= 8) merge(moved<MIRROR8>(b0), moved<MIRROR8>(b1));
+        if (group_lanes >= 16) merge(moved<MIRROR16>(b0), moved<MIRROR16>(b1));
         if (group_lanes >= 32) merge(__shfl_xor(b0, 16), __shfl_xor(b1, 16));
         const int g = sub / group_lanes;
         const bool group = g < a.opt.groups;
@@ -537,7 +563,7 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         int larger = 0;
         if (LANES == 16) {
 #define GNMS_ROTATE(N) \
-    if (((N) & (group_lanes - 1)) == 0) larger += dpp<0x120 + N, 0xf>(ranked, ranked) > ranked ? 1 : 0;
+    if (((N) & (group_lanes - 1)) == 0) larger += moved<ROTATE + N>(ranked) > ranked ? 1 : 0;
             GNMS_ROTATE(1) GNMS_ROTATE(2) GNMS_ROTATE(3) GNMS_ROTATE(4) GNMS_ROTATE(5)
             GNMS_ROTATE(6) GNMS_ROTATE(7) GNMS_ROTATE(8) GNMS_ROTATE(9) GNMS_ROTATE(10)
             GNMS_ROTATE(11) GNMS_ROTATE(12) GNMS_ROTATE(13) GNMS_ROTATE(14) GNMS_ROTATE(15)
