@@ -11,11 +11,10 @@
 // Two forms.  quick_kernel makes the choice on 32-bit keys, 22 bits of the
 // value's distance from the token's largest and 10 bits of the index, so that
 // a comparison, a sort step and a maximum over lanes are one or two
-// instructions each.  It knows how far a key may be off; a token with two
-// candidates that its keys cannot order, and that are not equal, is chosen
-// again from binary64 scores, by its wave (about one token in 500 where scores
-// have no ties).  exact_kernel does all in binary64, a wave per token, for
-// shapes that the first form does not hold.
+// instructions each.  It knows how far a key may be off; where candidates or
+// groups are closer than that (in about one token of 500, where scores have no
+// ties), it orders these few from binary64 scores.  exact_kernel does all in
+// binary64, a wave per token, for shapes that the first form does not hold.
 #include "select_internal.h"
 
 namespace gnms {
@@ -357,6 +356,14 @@ __device__ __forceinline__ uint32_t short_key(T v) {
     return to_f32(v) > NEG_INF ? k : 0u;
 }
 
+// The binary64 score of one expert of a token, good to 2^-40.
+__device__ __forceinline__ double exact_score(bool softmax, float z, float top, double share,
+                                              float bias) {
+    const double s = softmax ? exp_below(z, top, [](double v) { return exp_of(v); }) * share
+                             : inverse_of(1.0 + exp_of(-(double)z));
+    return s + (double)bias;
+}
+
 // The choice of quick_kernel for a wave's tokens, from binary64 scores (good
 // to 2^-40): lane i of a token gets its i-th expert, or -1.  z: the lane's
 // logits, -infinity where there is none; bias: the lane's, or 0.
@@ -371,9 +378,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z
     double b0 = LOWEST, b1 = LOWEST;
 #pragma unroll
     for (int j = 0; j < VALUES; ++j) {
-        double c = softmax ? exp_below(z[j], top, [](double v) { return exp_of(v); }) * share
-                           : inverse_of(1.0 + exp_of(-(double)z[j]));
-        c += (double)bias[j];
+        double c = exact_score(softmax, z[j], top, share, bias[j]);
         if (!(z[j] > NEG_INF && c > LOWEST)) c = LOWEST;
         b1 = c > b0 ? b0 : c > b1 ? c : b1;
         b0 = c > b0 ? c : b0;
@@ -572,11 +577,40 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
             for (int o = group_lanes; o < LANES; o += group_lanes)
                 larger += __shfl(ranked, (lane + o) & 63) > ranked ? 1 : 0;
         }
-        const bool kept = score > 0u && larger < a.opt.kept_groups;
+        bool kept = score > 0u && larger < a.opt.kept_groups;
         // how close the choice of the groups was
         const uint32_t least = all_min<LANES>(kept ? score : 0xffffffffu);
         const uint32_t most = all_max<LANES>(kept ? 0u : score);
-        if (least - most <= (uint32_t)(2 * margin)) bad = true;
+        const bool near_groups = least - most <= (uint32_t)(2 * margin);
+        if (__ballot(near_groups) != 0ull) {
+            // the groups' sums in binary64; a third expert that may be among
+            // a group's best two leaves it to choose_exactly
+            const double share = inverse_of(sum);
+            auto exact_of = [&](uint32_t m) -> double {
+                const int e = (int)(INDEX_MASK - (m & INDEX_MASK));
+                if (m <= INDEX_MASK) return LOWEST;
+                return exact_score(softmax, to_f32(row[e]), top, share,
+                                   a.bias != nullptr ? a.bias[e] : 0.0f);
+            };
+            const double s0 = exact_of(b0), s1 = two ? exact_of(b1) : 0.0;
+            const double exact = group ? s0 + s1 : LOWEST;
+            bool third = false;
+            const uint32_t lowest = (two ? q1 : q0) - min(two ? q1 : q0, (uint32_t)margin);
+#pragma unroll
+            for (int j = 0; j < 3 && j < VALUES; ++j)
+                third |= key[j] != b0 && !(two && key[j] == b1) &&
+                         (key[j] >> INDEX_BITS) >= lowest && lowest > 0u;
+            int before = 0;
+            for (int o = group_lanes; o < LANES; o += group_lanes) {
+                const int from = (sub + o) % LANES;
+                const double other = __shfl(exact, lane - sub + from);
+                before += other > exact || (other == exact && from < sub) ? 1 : 0;
+            }
+            if (near_groups) {
+                kept = score > 0u && before < a.opt.kept_groups;
+                if (group && (third || lowest == 0u)) bad = true;
+            }
+        }
         if (!kept) {
 #pragma unroll
             for (int j = 0; j < VALUES; ++j) key[j] = 0u;
@@ -596,11 +630,32 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         }
         return m <= INDEX_MASK ? 0u : m;
     };
+    // whether m, which comes after last, may belong before it
+    auto near_last = [&](uint32_t m) {
+        return m != 0u && (int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin;
+    };
     for (int i = 0; i < k; ++i) {
         const uint32_t m = next();
-        close |= i > 0 && m != 0u && (int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin;
+        close |= i > 0 && near_last(m);
         if (sub == i) mine = m;
         last = m;
+    }
+    // those that may belong among them: near the last, or near one that is
+    int candidates = k;
+    if (margin >= 0) {
+        uint32_t m = next();
+        bool open = near_last(m);
+        while (__ballot(open) != 0ull) {
+            if (open) {
+                close = true;
+                if (candidates == LANES) bad = true;  // no lane to hold it
+                else if (sub == candidates) mine = m;
+                candidates = min(candidates + 1, LANES);
+                last = m;
+            }
+            m = next();
+            open = open && !bad && near_last(m);
+        }
     }
     // Nothing left, or nearly at the keys' end: there is no further eligible
     // expert, or one below what keys reach.
@@ -613,36 +668,29 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         if (at_end && low) bad = true;
     }
     int id = mine != 0u ? (int)(INDEX_MASK - (mine & INDEX_MASK)) : -1;
-    // Candidates that are close must be equal, in their logits and biases; the
-    // one after the last, too, and those that are equal to it.
-    auto equal = [&](int x, int y) {
-        return to_f32(row[x]) == to_f32(row[y]) &&
-               (a.bias == nullptr || a.bias[x] == a.bias[y]);
-    };
-    if (margin >= 0) {
-        bool open = last != 0u && !bad;
-        while (__ballot(open) != 0ull) {
-            const uint32_t m = next();
-            open = open && m != 0u &&
-                   (int)((last >> INDEX_BITS) - (m >> INDEX_BITS)) <= margin;
-            if (open && !equal((int)(INDEX_MASK - (last & INDEX_MASK)),
-                               (int)(INDEX_MASK - (m & INDEX_MASK)))) {
-                bad = true;
-                open = false;
-            }
+    if (margin >= 0 && __ballot(close) != 0ull) {
+        // the candidates' order in binary64, equal ones by their index
+        const int e = mine != 0u ? id : INDEX_MASK + 1 + sub;
+        double v = LOWEST;
+        if (mine != 0u) {
+            const float ze = to_f32(row[e]);
+            v = a.bias != nullptr
+                    ? exact_score(softmax, ze, top, inverse_of(sum), a.bias[e])
+                    : (double)ze;
         }
-        if (__ballot(close) != 0ull) {
-            const uint32_t after = __shfl_down(mine, 1);
-            if (sub + 1 < k && after != 0u &&
-                (int)((mine >> INDEX_BITS) - (after >> INDEX_BITS)) <= margin &&
-                !equal(id, (int)(INDEX_MASK - (after & INDEX_MASK))))
-                bad = true;
+        int before = 0;
+        for (int o = 0; o < LANES; ++o) {
+            const double other = __shfl(v, lane - sub + o);
+            const int other_e = __shfl(e, lane - sub + o);
+            before += other > v || (other == v && other_e < e) ? 1 : 0;
         }
-        // any lane of the token
-        bad = all_max<LANES>((int)(live && bad)) != 0;
-    } else {
-        bad = false;
+        // every lane's place is another's
+        const int sorted = __builtin_amdgcn_ds_permute((lane - sub + before) * 4, e);
+        if (close) id = sorted <= (int)INDEX_MASK ? sorted : -1;
     }
+    if (sub >= k) id = -1;
+    if (margin >= 0) bad = all_max<LANES>((int)(live && bad)) != 0;  // any lane of the token
+    else bad = false;
     if (__ballot(bad) != 0ull) {
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
