@@ -16,7 +16,10 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import Workspace, _check, _default_workspace, _lib, _OnDevice, _raw_stream
+from . import Workspace, _check, _default_workspace, _lib, _raw_stream
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = torch.cuda.is_current_stream_capturing
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # nms_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}  # NMS_ROUTE_SOFTMAX, NMS_ROUTE_SIGMOID
@@ -41,6 +44,22 @@ class _LogitRules(ctypes.Structure):  # nms_logit_rules
 
 def _address(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+def _matrix(t, name: str) -> Tuple[int, int, int, int]:
+    """(nms_dtype, rows, columns, row stride) of a matrix of a floating type on
+    a GPU device.  The checks are those of _rows, which says what is wrong."""
+    try:
+        rows, columns = t.shape
+        stride, inner = t.stride()
+        code = _DTYPES[t.dtype]
+    except (AttributeError, KeyError, TypeError, ValueError):
+        code = None
+    if code is None or not t.is_cuda or inner != 1 or (rows > 1 and stride < columns):
+        stride = _rows(t, name)
+        rows, columns = t.shape
+        code = _DTYPES[t.dtype]
+    return code, rows, columns, stride
 
 
 def _rows(t, name: str, device=None, shape=None, dtype=None) -> int:
@@ -77,15 +96,16 @@ def _vector(t, name: str, n: int, dtype, device) -> Optional[int]:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
+    if (t.dtype is dtype and t.device == device and t.shape == (n,) and
+            (n < 2 or t.stride() == (1,))):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s must be on %s (got %s)" % (name, device, t.device))
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError("%s must have shape (%d,)" % (name, n))
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 # ------------------------------------------------------------------- routing
@@ -94,9 +114,9 @@ def _vector(t, name: str, n: int, dtype, device) -> Optional[int]:
 def _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top):
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
-    return _RouteOptions(_SCORES[score], int(top_k), int(bool(renormalise)), float(scale),
-                         int(groups), int(groups if kept_groups is None else kept_groups),
-                         int(group_top))
+    return ctypes.byref(_RouteOptions(
+        _SCORES[score], int(top_k), int(bool(renormalise)), float(scale), int(groups),
+        int(groups if kept_groups is None else kept_groups), int(group_top)))
 
 
 def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
@@ -113,22 +133,26 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     experts ``kept_groups`` (default: all) may be chosen from; ``live`` (bool
     or uint8, one per token) marks padded rows with 0.  A place that no expert
     is left for holds id -1 and weight 0."""
-    stride = _rows(logits, "logits")
-    tokens, experts = logits.shape
+    code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return route_experts(logits, top_k, score, bias, groups, kept_groups, group_top,
+                                 renormalise, scale, live, counts)
     options = _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top)
-    b = _vector(bias, "bias", experts, torch.float32, device)
-    alive = _vector(live, "live", tokens, torch.bool if live is not None and
-                    live.dtype is torch.bool else torch.uint8, device)
-    with _OnDevice(device):
-        # a call that will be refused allocates no negative shape
-        shape = (tokens, max(options.top_k, 0))
-        ids = torch.empty(shape, dtype=torch.int32, device=device)
-        weights = torch.empty(shape, dtype=torch.float32, device=device)
-        count = torch.empty(experts, dtype=torch.int32, device=device) if counts else None
-        _check(_lib.nms_route_experts(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts,
-                                      stride, b, alive, ctypes.byref(options), ids.data_ptr(),
-                                      weights.data_ptr(), _address(count), _raw_stream(device)))
+    b = None if bias is None else _vector(bias, "bias", experts, torch.float32, device)
+    alive = None if live is None else _vector(
+        live, "live", tokens, torch.bool if live.dtype is torch.bool else torch.uint8, device)
+    # a call that will be refused allocates no negative shape
+    shape = (tokens, max(int(top_k), 0))
+    ids = torch.empty(shape, dtype=torch.int32, device=device)
+    weights = torch.empty(shape, dtype=torch.float32, device=device)
+    count = torch.empty(experts, dtype=torch.int32, device=device) if counts else None
+    status = _lib.nms_route_experts(logits.data_ptr(), code, tokens, experts, stride, b, alive,
+                                    options, ids.data_ptr(), weights.data_ptr(),
+                                    _address(count), _raw_stream(device))
+    if status:
+        _check(status)
     return (ids, weights, count) if counts else (ids, weights)
 
 
@@ -139,26 +163,34 @@ def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights
     forward call's ``ids`` and the gradient of its weights; a tensor like
     ``logits`` (or ``out``).  The choice of the experts, and so the bias, has
     no gradient."""
-    stride = _rows(logits, "logits")
-    tokens, experts = logits.shape
+    code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a matrix of shape (tokens, top_k)")
-    shape = torch.Size((tokens, ids.shape[1]))
-    for t, name, dtype in ((ids, "ids", torch.int32), (grad_weights, "grad_weights",
-                                                       torch.float32)):
-        _rows(t, name, device, shape, dtype)
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    options = _route_options(score, ids.shape[1], renormalise, scale, 1, 1, 1)
-    with _OnDevice(device):
-        if out is None:
-            out = torch.empty((tokens, experts), dtype=logits.dtype, device=device)
+    top_k = ids.shape[1]
+    if not (ids.dtype is torch.int32 and ids.device == device and ids.is_contiguous() and
+            ids.shape[0] == tokens and isinstance(grad_weights, torch.Tensor) and
+            grad_weights.dtype is torch.float32 and grad_weights.device == device and
+            grad_weights.shape == ids.shape and grad_weights.is_contiguous()):
+        shape = torch.Size((tokens, top_k))
+        _rows(ids, "ids", device, shape, torch.int32)
+        _rows(grad_weights, "grad_weights", device, shape, torch.float32)
+        raise ValueError("ids and grad_weights must be contiguous")
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return route_experts_backward(logits, ids, grad_weights, score, renormalise, scale,
+                                          out)
+    options = _route_options(score, top_k, renormalise, scale, 1, 1, 1)
+    if out is None:
+        out = torch.empty((tokens, experts), dtype=logits.dtype, device=device)
+        out_stride = experts
+    else:
         out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
-        _check(_lib.nms_route_experts_backward(
-            logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, stride, ids.data_ptr(),
-            grad_weights.data_ptr(), ctypes.byref(options), out.data_ptr(), out_stride,
-            _raw_stream(device)))
+    status = _lib.nms_route_experts_backward(
+        logits.data_ptr(), code, tokens, experts, stride, ids.data_ptr(), grad_weights.data_ptr(),
+        options, out.data_ptr(), out_stride, _raw_stream(device))
+    if status:
+        _check(status)
     return out
 
 
@@ -251,16 +283,21 @@ def adjust_logits(logits: torch.Tensor, rules: LogitRules,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The logits under the rules, a tensor like ``logits`` (or ``out``, which
     may be ``logits`` itself and must not overlap it otherwise)."""
-    stride = _rows(logits, "logits")
-    rows, vocab = logits.shape
+    code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
     ref = rules._for(rows, vocab, device)
-    with _OnDevice(device):
-        if out is None:
-            out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return adjust_logits(logits, rules, out)
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        out_stride = vocab
+    else:
         out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
-        _check(_lib.nms_adjust_logits(logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, stride,
-                                      ref, out.data_ptr(), out_stride, _raw_stream(device)))
+    status = _lib.nms_adjust_logits(logits.data_ptr(), code, rows, vocab, stride, ref,
+                                    out.data_ptr(), out_stride, _raw_stream(device))
+    if status:
+        _check(status)
     return out
 
 
@@ -283,29 +320,32 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     and ``top_k`` int32, one per row (top_k up to ``max_top_k``, at most
     1024).  The logprob is that of the token under the softmax over all
     allowed tokens.  A row without an allowed token gets -1 and -infinity."""
-    stride = _rows(logits, "logits")
-    rows, vocab = logits.shape
+    code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
     if uniform is None:
         raise TypeError("uniform must be a torch tensor")
     f32 = torch.float32
     u = _vector(uniform, "uniform", rows, f32, device)
-    t = _vector(temperature, "temperature", rows, f32, device)
-    k = _vector(top_k, "top_k", rows, torch.int32, device)
-    p = _vector(top_p, "top_p", rows, f32, device)
-    m = _vector(min_p, "min_p", rows, f32, device)
+    t = None if temperature is None else _vector(temperature, "temperature", rows, f32, device)
+    k = None if top_k is None else _vector(top_k, "top_k", rows, torch.int32, device)
+    p = None if top_p is None else _vector(top_p, "top_p", rows, f32, device)
+    m = None if min_p is None else _vector(min_p, "min_p", rows, f32, device)
     ref = None if rules is None else rules._for(rows, vocab, device)
-    with _OnDevice(device):
-        nbytes = pick_workspace_size(rows, vocab, max_top_k)
-        # kept per thread and stream; a captured call takes one of its own from
-        # the graph's memory, so that no two graphs share it
-        stream = _raw_stream(device)
-        kept = (Workspace(device) if torch.cuda.is_current_stream_capturing()
-                else _default_workspace(device, stream))
-        buf = kept.get(nbytes, device)
-        ids = torch.empty(rows, dtype=torch.int32, device=device)
-        logprobs = torch.empty(rows, dtype=f32, device=device)
-        _check(_lib.nms_pick_tokens(logits.data_ptr(), _DTYPES[logits.dtype], rows, vocab, stride,
-                                    ref, u, t, k, p, m, max_top_k, ids.data_ptr(),
-                                    logprobs.data_ptr(), buf.data_ptr(), nbytes, stream))
+    if device.index != _current_device():
+        with torch.cuda.device(device):
+            return pick_tokens(logits, uniform, max_top_k, temperature, top_k, top_p, min_p,
+                               rules)
+    nbytes = pick_workspace_size(rows, vocab, max_top_k)
+    # kept per thread and stream; a captured call takes one of its own from
+    # the graph's memory, so that no two graphs share it
+    stream = _raw_stream(device)
+    kept = Workspace(device) if _capturing() else _default_workspace(device, stream)
+    buf = kept.get(nbytes, device)
+    ids = torch.empty(rows, dtype=torch.int32, device=device)
+    logprobs = torch.empty(rows, dtype=f32, device=device)
+    status = _lib.nms_pick_tokens(logits.data_ptr(), code, rows, vocab, stride, ref, u, t, k, p, m,
+                                  max_top_k, ids.data_ptr(), logprobs.data_ptr(),
+                                  buf.data_ptr(), nbytes, stream)
+    if status:
+        _check(status)
     return ids, logprobs
