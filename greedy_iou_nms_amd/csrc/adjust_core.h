@@ -67,23 +67,20 @@ __device__ __forceinline__ RowRules row_rules(const nms_logit_rules &u, int64_t 
     return r;
 }
 
-// A thread's first entries of the history, which it loads before it knows
-// how many are in use.
-constexpr int EARLY = 4;
-struct EarlyHistory {
-    int v[EARLY];
+// Four neighbouring entries of a history from i on; -1 past its capacity.
+struct FourTokens {
+    int v[4];
 };
 
-template <int THREADS>
-__device__ __forceinline__ EarlyHistory early_history(const nms_logit_rules &u, int64_t row) {
-    EarlyHistory e;
-    const int32_t *history = u.history + row * u.history_stride;
+__device__ __forceinline__ FourTokens load4(const int32_t *history, int i, int capacity) {
+    FourTokens f;
+    if (i + 4 <= capacity) {
+        __builtin_memcpy(&f, history + i, sizeof(f));
+    } else {
 #pragma unroll
-    for (int q = 0; q < EARLY; ++q) {
-        const int i = q * THREADS + (int)threadIdx.x;
-        e.v[q] = i < (int)u.history_capacity ? history[i] : -1;
+        for (int c = 0; c < 4; ++c) f.v[c] = i + c < capacity ? history[i + c] : -1;
     }
-    return e;
+    return f;
 }
 
 // Where the word of a slice's token lies: threads read the words of eight
@@ -116,14 +113,14 @@ __device__ __forceinline__ float replaced(const nms_logit_rules &u, const RowRul
 template <int THREADS, int SLICE>
 __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowRules &r,
                                             int64_t row, int lo, int size,
-                                            const EarlyHistory &early, uint32_t *word,
+                                            const FourTokens &early, uint32_t *word,
                                             uint32_t *bit) {
     const int tid = threadIdx.x;
     const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < SLICE / 4 / THREADS; ++i)
         reinterpret_cast<uint4 *>(word)[i * THREADS + tid] = none;
-    if (tid < SLICE / 32) bit[tid] = 0;
+    for (int i = tid; i < SLICE / 32; i += THREADS) bit[i] = 0;
     __syncthreads();
     if (u.bias_count > 0) {
         const int32_t *ids = u.bias_ids + row * u.bias_stride;
@@ -136,27 +133,29 @@ __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowR
         }
         __syncthreads();
     }
-    auto count = [&](int i, int v) {
-        const unsigned at = (unsigned)v - (unsigned)lo;
-        if (i < r.length && at < (unsigned)size) {
-            uint32_t *w = &word[slot<SLICE>(at)];
-            if (i < r.prompt) atomicOr(w, RULE_SEEN);
-            else atomicAdd(w, 1u);
-            atomicOr(&bit[at >> 5], 1u << (at & 31u));
+    auto count = [&](int i, const FourTokens &f) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const unsigned at = (unsigned)f.v[c] - (unsigned)lo;
+            if (i + c < r.length && at < (unsigned)size) {
+                uint32_t *w = &word[slot<SLICE>(at)];
+                if (i + c < r.prompt) atomicOr(w, RULE_SEEN);
+                else atomicAdd(w, 1u);
+                atomicOr(&bit[at >> 5], 1u << (at & 31u));
+            }
         }
     };
-#pragma unroll
-    for (int q = 0; q < EARLY; ++q) count(q * THREADS + tid, early.v[q]);
+    // the first entries are here already; the others four loads at a time
+    constexpr int STEP = 4 * THREADS, DEEP = 4;
+    count(4 * tid, early);
     const int32_t *history = u.history + row * u.history_stride;
-    for (int i0 = EARLY * THREADS; i0 < r.length; i0 += EARLY * THREADS) {
-        int v[EARLY];
+    for (int i0 = STEP + 4 * tid; i0 < r.length; i0 += DEEP * STEP) {
+        FourTokens f[DEEP];
 #pragma unroll
-        for (int q = 0; q < EARLY; ++q) {
-            const int i = i0 + q * THREADS + tid;
-            v[q] = i < r.length ? history[i] : -1;
-        }
+        for (int q = 0; q < DEEP; ++q)
+            f[q] = load4(history, i0 + q * STEP, (int)u.history_capacity);
 #pragma unroll
-        for (int q = 0; q < EARLY; ++q) count(i0 + q * THREADS + tid, v[q]);
+        for (int q = 0; q < DEEP; ++q) count(i0 + q * STEP, f[q]);
     }
     __syncthreads();
 }

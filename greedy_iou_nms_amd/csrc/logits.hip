@@ -15,7 +15,9 @@ __global__ __launch_bounds__(THREADS, 8) void adjust_kernel(AdjustArgs a) {
     const int64_t row = blockIdx.x;
     const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
-    const EarlyHistory early = early_history<THREADS>(a.rules, row);
+    // a thread's first entries, before it knows how many are in use
+    const FourTokens early = load4(a.rules.history + row * a.rules.history_stride,
+                                   4 * (int)threadIdx.x, (int)a.rules.history_capacity);
     const RowRules r = row_rules(a.rules, row, readable(a.logits));
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + lo;
@@ -49,6 +51,7 @@ void run(const AdjustArgs &a, hipStream_t stream) {
 template <typename T>
 void choose(const AdjustArgs &a, hipStream_t stream) {
     if (a.rows * ((a.vocab + 16383) / 16384) >= 256) run<T, 1024, 16>(a, stream);
+    else if (a.rules.history_capacity > 4096) run<T, 1024, 8>(a, stream);
     else run<T, 256, 8>(a, stream);
 }
 

@@ -131,7 +131,7 @@ __device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t lef
 // the slice's first largest token, without a histogram (1.1 us of a slice's
 // 4.8 where little else runs).
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
-__global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(PickArgs a, Part *parts,
+__global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(PickArgs a, Part *parts,
                                                            uint64_t *found) {
     constexpr int SLICE = THREADS * VALUES;
     constexpr int WAVES = THREADS / 64;
@@ -148,7 +148,9 @@ __global__ __launch_bounds__(THREADS, THREADS == 512 ? 4 : 8) void slice_kernel(
     const int64_t part = row * gridDim.y + blockIdx.y;
     const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
-    const EarlyHistory early = early_history<THREADS>(a.rules, row);
+    // a thread's first entries, before it knows how many are in use
+    const FourTokens early = load4(a.rules.history + row * a.rules.history_stride,
+                                   4 * (int)threadIdx.x, (int)a.rules.history_capacity);
     const RowRules r = row_rules(a.rules, row, a.uniform);
     const float warm = warmth(parameter(a.temperature, row, 1.0f, a.uniform));
     const float c = fminf(1.4426950408889634f / warm, 3.0e38f);
@@ -703,12 +705,18 @@ __global__ __launch_bounds__(FT) void first_kernel(PickArgs a, int slices, const
     }
 }
 
-// Whether a row is split into slices of 16384 tokens, or of 2048 so that
-// small batches fill the GPU.
-bool wide_slices(int64_t rows, int vocab) { return rows * ((vocab + 16383) / 16384) >= 256; }
+// How a row is split: slices of 16384 tokens where these fill the GPU; else of
+// 2048, or with a history that every slice's threads would read for long
+// (more than 16 entries each) of 8192 with four times the threads.
+enum Split { WIDE, LONG, SMALL };
 
-int slices_of(int64_t rows, int vocab) {
-    const int slice = wide_slices(rows, vocab) ? 16384 : 2048;
+Split split_of(int64_t rows, int vocab, int64_t history) {
+    if (rows * ((vocab + 16383) / 16384) >= 256) return WIDE;
+    return history > 4096 ? LONG : SMALL;
+}
+
+int slices_of(Split s, int vocab) {
+    const int slice = s == WIDE ? 16384 : s == LONG ? 8192 : 2048;
     return (vocab + slice - 1) / slice;
 }
 
@@ -725,13 +733,14 @@ void run_slices(const PickArgs &a, int slices, Part *parts, uint64_t *found, hip
 
 template <typename T>
 void run(const PickArgs &a, hipStream_t stream) {
-    const int slices = slices_of(a.rows, a.vocab);
+    const Split split = split_of(a.rows, a.vocab, a.rules.history_capacity);
+    const int slices = slices_of(split, a.vocab);
     Part *parts = static_cast<Part *>(a.workspace);
     uint64_t *found = reinterpret_cast<uint64_t *>(static_cast<char *>(a.workspace) +
                                                    parts_bytes(a.rows, slices));
-    const bool wide = wide_slices(a.rows, a.vocab);
     if (a.max_top_k == 1) {
-        if (wide) run_slices<T, 512, 32, 32, true>(a, slices, parts, found, stream);
+        if (split == WIDE) run_slices<T, 512, 32, 32, true>(a, slices, parts, found, stream);
+        else if (split == LONG) run_slices<T, 1024, 8, 8, true>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 8, true>(a, slices, parts, found, stream);
         first_kernel<<<(unsigned)((a.rows + FT / 64 - 1) / (FT / 64)), FT, 0, stream>>>(
             a, slices, parts, found);
@@ -740,9 +749,12 @@ void run(const PickArgs &a, hipStream_t stream) {
     // Groups of the histogram: at least four for each of max_top_k, so that
     // the k-th largest group bounds the k-th value closely (of values without
     // order about 1.15 k lie above it).
-    if (wide) {
+    if (split == WIDE) {
         if (a.max_top_k <= 128) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
         else run_slices<T, 512, 32, 4>(a, slices, parts, found, stream);
+    } else if (split == LONG) {
+        if (a.max_top_k <= 256) run_slices<T, 1024, 8, 8>(a, slices, parts, found, stream);
+        else run_slices<T, 1024, 8, 2>(a, slices, parts, found, stream);
     } else {
         if (a.max_top_k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 1>(a, slices, parts, found, stream);
@@ -759,7 +771,9 @@ void run(const PickArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t pick_workspace_bytes(int64_t rows, int vocab, int max_top_k) {
-    const int slices = slices_of(rows, vocab);
+    // the finest split that these sizes may take (the history is not known)
+    const Split split = split_of(rows, vocab, 0);
+    const int slices = slices_of(split, vocab);
     return parts_bytes(rows, slices) + (size_t)rows * slices * slice_cap(max_top_k) * 8;
 }
 
