@@ -143,7 +143,8 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
     __shared__ uint32_t taken, chosen[2];
     __shared__ unsigned long long greatest;
     __shared__ float bound[EDGES];
-    const int tid = threadIdx.x, wave = tid >> 6;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    static_assert(WAVES >= EDGES, "a wave for each bound");
     const int64_t row = blockIdx.x;
     const int64_t part = row * gridDim.y + blockIdx.y;
     const int lo = (int)blockIdx.y * SLICE;
@@ -255,15 +256,12 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
     for (int g = 0; g < VALUES / GROUP; ++g)
         if (m[g] > NEG_INF) atomicAdd(&hist[bins.of(m[g], BINS)], 1u);
     __syncthreads();
-    if (wave == 0) {
-        const Ranks<BINS / 64> ranks(hist);
-#pragma unroll
-        for (int i = 0; i < EDGES; ++i) {
-            const int b = ranks.bin((uint32_t)(k + (1 << i) - 1) >> i);
-            if (tid == 0) bound[i] = b < 0 ? NEG_INF : bins.edge(b);
-        }
-        if (tid == 0) lowest = ordered(__builtin_inff());
+    if (wave < EDGES) {
+        // a wave per bound
+        const int b = Ranks<BINS / 64>(hist).bin((uint32_t)(k + (1 << wave) - 1) >> wave);
+        if ((tid & 63) == 0) bound[wave] = b < 0 ? NEG_INF : bins.edge(b);
     }
+    if (tid == 0) lowest = ordered(__builtin_inff());
     __syncthreads();
     // at least k values lie at the bound or above; without one, all values
     // are candidates
