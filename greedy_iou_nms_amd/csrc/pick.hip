@@ -1,11 +1,11 @@
 // Picking the next token of every row from its adjusted logits.
 //
-// Two launches.  slice_kernel: one workgroup per (row, slice of the
+// Two steps.  slice_kernel: one workgroup per (row, slice of the
 // vocabulary) adjusts the slice once (adjust_core.h), keeps its values in
 // registers, and writes those among which its largest max_top_k are, with the
 // slice's part of the softmax sum (a maximum and a sum relative to it).
 // join_kernel: one workgroup per row takes the largest max_top_k of all
-// slices, sorts them, and draws.
+// slices, sorts them, and draws.  whole_kernel does both in one launch.
 //
 // A candidate is a 64-bit word: the order-preserving key of its value above,
 // the complement of its token below, so that the words of a row are all
@@ -130,21 +130,26 @@ __device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t lef
 // share an entry in the histogram (their largest).  FIRST is for max_top_k = 1:
 // the slice's first largest token, without a histogram (1.1 us of a slice's
 // 4.8 where little else runs).
+template <int THREADS, int VALUES>
+struct SliceSpace {  // in LDS
+    uint32_t word[THREADS * VALUES];  // the rules, then the values
+    uint32_t bit[THREADS * VALUES / 32];
+    uint32_t hist[BINS];
+    float wave_top[THREADS / 64], wave_sums[THREADS / 64];
+    float bound[EDGES];
+    unsigned long long greatest;
+    int highest, lowest;  // as ordered()
+    uint32_t taken, chosen[2];
+};
+
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
-__global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(PickArgs a, Part *parts,
-                                                           uint64_t *found) {
+__device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *found,
+                                      SliceSpace<THREADS, VALUES> &x) {
     constexpr int SLICE = THREADS * VALUES;
     constexpr int WAVES = THREADS / 64;
-    __shared__ uint32_t word[SLICE];  // the rules, then the values
-    __shared__ uint32_t bit[SLICE / 32];
-    __shared__ uint32_t hist[BINS];
-    __shared__ float wave_top[WAVES], wave_sums[WAVES];
-    __shared__ int highest, lowest;  // as ordered()
-    __shared__ uint32_t taken, chosen[2];
-    __shared__ unsigned long long greatest;
-    __shared__ float bound[EDGES];
+    uint32_t *word = x.word, *bit = x.bit, *hist = x.hist;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    static_assert(WAVES >= EDGES, "a wave for each bound");
+    static_assert(WAVES >= EDGES, "a wave for each x.bound");
     const int64_t row = blockIdx.x;
     const int64_t part = row * gridDim.y + blockIdx.y;
     const int lo = (int)blockIdx.y * SLICE;
@@ -159,10 +164,10 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
     const Raw<T, THREADS, VALUES> raw(r, lo, size, in);
     for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
     if (tid == 0) {
-        taken = 0;
-        greatest = 0;
-        highest = ordered(NEG_INF);
-        lowest = ordered(__builtin_inff());
+        x.taken = 0;
+        x.greatest = 0;
+        x.highest = ordered(NEG_INF);
+        x.lowest = ordered(__builtin_inff());
     }
     if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word, bit);
     else __syncthreads();
@@ -170,10 +175,10 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
     adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, word, bit, z);
     // The groups' largest values and the wave's, and the softmax sum relative
     // to that: exp2(z c - top c), one multiply-add and one exponential a value,
-    // where the rounding of top c is a factor of all terms and is taken out of
+    // where the rounding of top c is a factor of all terms and is x.taken out of
     // the sum.  A NaN, an infinite top, a c of 0 or a product of 2^24 and more
-    // show in the sum or in what is taken out; then the values are gone over
-    // again, with a NaN made -infinity and each difference taken by itself.
+    // show in the sum or in what is x.taken out; then the values are gone over
+    // again, with a NaN made -infinity and each difference x.taken by itself.
     float m[VALUES / GROUP], top, sum;
     for (bool again = false;; again = true) {
         if (again) {
@@ -219,21 +224,21 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
         if (m[g] > NEG_INF) least = min(least, ordered(m[g]));
     least = wave_min(least);
     if ((tid & 63) == 0) {
-        wave_top[wave] = top;
-        wave_sums[wave] = sum;
-        atomicMax(&highest, ordered(top));
-        atomicMin(&lowest, least);
+        x.wave_top[wave] = top;
+        x.wave_sums[wave] = sum;
+        atomicMax(&x.highest, ordered(top));
+        atomicMin(&x.lowest, least);
     }
     __syncthreads();
-    top = unordered(highest);
+    top = unordered(x.highest);
     const int k = a.max_top_k, cap = slice_cap(k);
     found += part * cap;
     // the slice's softmax sum from its waves', and what else it says; wave 0
     auto finish = [&](uint32_t count, float e0, float e1, float e2, float e3, float least_found) {
-        const float wt = tid < WAVES ? wave_top[tid & (WAVES - 1)] : NEG_INF;
+        const float wt = tid < WAVES ? x.wave_top[tid & (WAVES - 1)] : NEG_INF;
         double all = 0.0;
         if (wt > NEG_INF)
-            all = (double)wave_sums[tid & (WAVES - 1)] *
+            all = (double)x.wave_sums[tid & (WAVES - 1)] *
                   (wt == top ? 1.0 : (double)__builtin_amdgcn_exp2f((wt - top) * c));
         all = wave_sum(all);
         if (tid == 0) parts[part] = Part{top, count, all, {e0, e1, e2, e3}, least_found, 0.0f};
@@ -245,27 +250,27 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
             for (int j = VALUES - 1; j >= 0; --j)
                 if (z[j] == top) best = candidate(z[j], lo + token_at<THREADS>(j));
         }
-        if (best != 0) atomicMax(&greatest, (unsigned long long)best);
+        if (best != 0) atomicMax(&x.greatest, (unsigned long long)best);
         __syncthreads();
-        if (tid == 0) found[0] = greatest;
+        if (tid == 0) found[0] = x.greatest;
         if (wave == 0) finish(top > NEG_INF ? 1u : 0u, top, top, top, top, top);
         return;
     }
-    const Bins bins(unordered(lowest), top, BINS);
+    const Bins bins(unordered(x.lowest), top, BINS);
 #pragma unroll
     for (int g = 0; g < VALUES / GROUP; ++g)
         if (m[g] > NEG_INF) atomicAdd(&hist[bins.of(m[g], BINS)], 1u);
     __syncthreads();
     if (wave < EDGES) {
-        // a wave per bound
+        // a wave per x.bound
         const int b = Ranks<BINS / 64>(hist).bin((uint32_t)(k + (1 << wave) - 1) >> wave);
-        if ((tid & 63) == 0) bound[wave] = b < 0 ? NEG_INF : bins.edge(b);
+        if ((tid & 63) == 0) x.bound[wave] = b < 0 ? NEG_INF : bins.edge(b);
     }
-    if (tid == 0) lowest = ordered(__builtin_inff());
+    if (tid == 0) x.lowest = ordered(__builtin_inff());
     __syncthreads();
-    // at least k values lie at the bound or above; without one, all values
+    // at least k values lie at the x.bound or above; without one, all values
     // are candidates
-    const float first = bound[0];
+    const float first = x.bound[0];
     float edge = fminf(fmaxf(first, -3.402823466e38f), 3.402823466e38f);
     if (edge == 0.0f) edge = -1.0e-38f;  // so that -0 is not below it
     // bit j: z[j] >= edge, the sign of a difference that is no NaN
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
     const uint32_t mine = (uint32_t)__popc(hits);
     const uint32_t through = wave_scan(mine);
     uint32_t to = 0;
-    if ((tid & 63) == 63) to = atomicAdd(&taken, through);
+    if ((tid & 63) == 63) to = atomicAdd(&x.taken, through);
     to = last_lane(to) + through - mine;
     // the candidate of the thread's j-th token
     auto own = [&](int j) -> uint64_t {
@@ -297,11 +302,11 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
         for (int j = 0; j < VALUES; ++j)
             if (z[j] > NEG_INF) low = fminf(low, z[j]);
         low = wave_min(low);
-        if ((tid & 63) == 0) atomicMin(&lowest, ordered(low));
+        if ((tid & 63) == 0) atomicMin(&x.lowest, ordered(low));
     }
     __syncthreads();
-    if (first == NEG_INF) edge = unordered(lowest);
-    if (taken > (uint32_t)cap) {
+    if (first == NEG_INF) edge = unordered(x.lowest);
+    if (x.taken > (uint32_t)cap) {
         // Equal values, or a spread that the bins do not resolve: the k-th
         // largest word, digit by digit from the top, and exactly k of them.
         uint64_t prefix = 0, mask = 0;
@@ -315,22 +320,30 @@ __global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(Pi
                 if (w != 0 && (w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
             }
             __syncthreads();
-            if (wave == 0) digit_of_rank(hist, left, chosen);
-            if (tid == 0) taken = 0;
+            if (wave == 0) digit_of_rank(hist, left, x.chosen);
+            if (tid == 0) x.taken = 0;
             __syncthreads();
-            prefix |= (uint64_t)chosen[0] << shift;
+            prefix |= (uint64_t)x.chosen[0] << shift;
             mask |= 255ull << shift;
-            left = chosen[1];
+            left = x.chosen[1];
         }
 #pragma unroll 1
         for (int j = 0; j < VALUES; ++j) {
             const uint64_t w = own(j);
-            if (w >= prefix) found[atomicAdd(&taken, 1u)] = w;
+            if (w >= prefix) found[atomicAdd(&x.taken, 1u)] = w;
         }
         edge = key_value((uint32_t)(prefix >> 32));
         __syncthreads();
     }
-    if (wave == 0) finish(taken, first, bound[1], bound[2], bound[3], edge);
+    if (wave == 0) finish(x.taken, first, x.bound[1], x.bound[2], x.bound[3], edge);
+}
+
+template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
+__global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(PickArgs a,
+                                                                              Part *parts,
+                                                                              uint64_t *found) {
+    __shared__ SliceSpace<THREADS, VALUES> space;
+    slice<T, THREADS, VALUES, GROUP, FIRST>(a, parts, found, space);
 }
 
 // --------------------------------------------------------------------- join
@@ -417,24 +430,29 @@ __device__ __forceinline__ Part lane_part(const Part *parts, int slices) {
 }
 
 template <int THREADS>
-__global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, uint32_t inverse,
-                                                       const Part *parts, const uint64_t *found) {
+struct JoinSpace {  // in LDS
+    uint64_t list[THREADS + CROWDED], sorted[THREADS];
+    // per bin: its count of held candidates, then its first place; its count
+    // of the rest, then the next place of the rest; and its end
+    uint32_t hist[JOIN_BINS], rest[JOIN_BINS], ends[JOIN_BINS];
+    RowParts whole;
+    double wave_d[4], kept;
+    uint32_t wave_u[THREADS / 64];
+    int wave_i[3][4];
+    uint32_t taken, crowded, inside, chosen[2];
+};
+
+template <int THREADS>
+__device__ __forceinline__ void join(const PickArgs &a, int64_t row, int slices, uint32_t inverse,
+                                     const Part *parts, const uint64_t *found,
+                                     JoinSpace<THREADS> &x) {
     constexpr int WAVES = THREADS / 64;
     constexpr int HELD = JOIN_HELD;
     constexpr int PER = JOIN_BINS / THREADS;  // bins per thread
     constexpr int DRAW = THREADS / 256;       // candidates per thread that draws
     constexpr int LIST = THREADS + CROWDED;
-    __shared__ uint64_t list[LIST], sorted[THREADS];
-    // per bin: its count of held candidates, then its first place; its count
-    // of the rest, then the next place of the rest; and its end
-    __shared__ uint32_t hist[JOIN_BINS], rest[JOIN_BINS], ends[JOIN_BINS];
-    __shared__ RowParts whole;
-    __shared__ uint32_t wave_u[WAVES];
-    __shared__ double wave_d[4];
-    __shared__ int wave_i[3][4];
-    __shared__ uint32_t taken, crowded, inside, chosen[2];
-    __shared__ double kept;
-    const int64_t row = blockIdx.x;
+    uint64_t *list = x.list, *sorted = x.sorted;
+    uint32_t *hist = x.hist, *rest = x.rest, *ends = x.ends;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kmax = a.max_top_k, cap = slice_cap(kmax);
@@ -481,17 +499,17 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         rest[i * THREADS + tid] = 0;
     }
     if (tid == 0) {
-        taken = 0;
-        crowded = 0;
+        x.taken = 0;
+        x.crowded = 0;
     }
     sorted[tid] = 0;
     for (int i = tid; i < LIST; i += THREADS) list[i] = 0;
     if (wave == 0) {
         const RowParts r = join_parts(parts, slices, first, warm);
-        if (lane == 0) whole = r;
+        if (lane == 0) x.whole = r;
     }
     __syncthreads();
-    const float top = whole.top, edge = whole.edge;
+    const float top = x.whole.top, edge = x.whole.edge;
     if (!(top > NEG_INF)) {
         if (tid == 0) {
             a.ids[row] = -1;
@@ -526,23 +544,23 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         bin_sum += all_count[i];
     }
     uint32_t start = wave_scan(bin_sum);
-    if (lane == 63) wave_u[wave] = start;
+    if (lane == 63) x.wave_u[wave] = start;
     __syncthreads();
     start -= bin_sum;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) start += w < wave ? wave_u[w] : 0u;
+    for (int w = 0; w < WAVES; ++w) start += w < wave ? x.wave_u[w] : 0u;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int b = JOIN_BINS - 1 - tid * PER - i;
         hist[b] = start;
         rest[b] = start + held_count[i];
-        if (start < (uint32_t)kmax && all_count[i] > (uint32_t)CROWDED) crowded = 1;
+        if (start < (uint32_t)kmax && all_count[i] > (uint32_t)CROWDED) x.crowded = 1;
         start += all_count[i];
         ends[b] = start;
     }
-    if (tid == THREADS - 1) inside = start;
+    if (tid == THREADS - 1) x.inside = start;
     __syncthreads();
-    if (crowded == 0) {
+    if (x.crowded == 0) {
         // a bin that starts before kmax ends before LIST
 #pragma unroll
         for (int q = 0; q < HELD; ++q)
@@ -562,7 +580,7 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
             if (w == 0) break;
             const int b = bins.of(value(w), JOIN_BINS);
             uint32_t rank = hist[b];
-            for (uint32_t x = rank, last = ends[b]; x < last; ++x) rank += list[x] > w ? 1u : 0u;
+            for (uint32_t y = rank, last = ends[b]; y < last; ++y) rank += list[y] > w ? 1u : 0u;
             if (rank < (uint32_t)THREADS) sorted[rank] = w;
         }
     } else {
@@ -570,7 +588,7 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         // digit by digit, and a sort of those from there up.
         uint64_t prefix = 0, mask = 0;
         uint32_t left = (uint32_t)kmax;
-        if (inside <= (uint32_t)kmax) {
+        if (x.inside <= (uint32_t)kmax) {
             prefix = 1;
         } else {
             for (int shift = 56; shift >= 0; shift -= 8) {
@@ -581,19 +599,19 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
                     if (w != 0 && (w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
                 });
                 __syncthreads();
-                if (wave == 0) digit_of_rank(hist, left, chosen);
+                if (wave == 0) digit_of_rank(hist, left, x.chosen);
                 __syncthreads();
-                prefix |= (uint64_t)chosen[0] << shift;
+                prefix |= (uint64_t)x.chosen[0] << shift;
                 mask |= 255ull << shift;
-                left = chosen[1];
+                left = x.chosen[1];
             }
         }
         each([&](uint64_t w) {
-            if (w >= prefix && value(w) >= edge) list[atomicAdd(&taken, 1u)] = w;
+            if (w >= prefix && value(w) >= edge) list[atomicAdd(&x.taken, 1u)] = w;
         });
         __syncthreads();
         int p = 64;
-        while (p < (int)taken) p <<= 1;
+        while (p < (int)x.taken) p <<= 1;
         const uint64_t mine = sort_words(list[tid], p, list);
         sorted[tid] = mine;
     }
@@ -621,19 +639,19 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
     double before = through - run, all = last_lane(through);
     if (!single) {
         if (lane == 0) {
-            wave_d[wave] = all;
-            wave_i[0][wave] = in_k;
-            wave_i[1][wave] = in_m;
+            x.wave_d[wave] = all;
+            x.wave_i[0][wave] = in_k;
+            x.wave_i[1][wave] = in_m;
         }
         __syncthreads();
         all = 0.0;
         in_k = in_m = 0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (x < wave) before += wave_d[x];
-            all += wave_d[x];
-            in_k += wave_i[0][x];
-            in_m += wave_i[1][x];
+        for (int y = 0; y < 4; ++y) {
+            if (y < wave) before += x.wave_d[y];
+            all += x.wave_d[y];
+            in_k += x.wave_i[0][y];
+            in_m += x.wave_i[1][y];
         }
     }
     // how many come before the sum reaches top_p of all
@@ -644,25 +662,25 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         in_p += __popcll(__ballot(there[i] && cum[i] < top_p * all));
     }
     if (!single) {
-        if (lane == 0) wave_i[2][wave] = in_p;
+        if (lane == 0) x.wave_i[2][wave] = in_p;
         __syncthreads();
-        in_p = wave_i[2][0] + wave_i[2][1] + wave_i[2][2] + wave_i[2][3];
+        in_p = x.wave_i[2][0] + x.wave_i[2][1] + x.wave_i[2][2] + x.wave_i[2][3];
     }
     const int keep = max(1, min(min(in_p + 1, in_m), in_k));
 #pragma unroll
     for (int i = 0; i < DRAW; ++i)
-        if (tid * DRAW + i == keep - 1) kept = cum[i];
+        if (tid * DRAW + i == keep - 1) x.kept = cum[i];
     if (single) wave_fence();
     else __syncthreads();
-    const double bound = uniform * kept;
+    const double bound = uniform * x.kept;
     int j = 0;
 #pragma unroll
     for (int i = 0; i < DRAW; ++i)
         j += __popcll(__ballot(tid * DRAW + i < keep && cum[i] <= bound));
     if (!single) {
-        if (lane == 0) wave_i[0][wave] = j;
+        if (lane == 0) x.wave_i[0][wave] = j;
         __syncthreads();
-        j = wave_i[0][0] + wave_i[0][1] + wave_i[0][2] + wave_i[0][3];
+        j = x.wave_i[0][0] + x.wave_i[0][1] + x.wave_i[0][2] + x.wave_i[0][3];
     }
     j = t > 0.0f ? min(j, keep - 1) : 0;
 #pragma unroll
@@ -670,17 +688,21 @@ __global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, u
         if (tid * DRAW + i == j) {
             a.ids[row] = (int32_t)~(uint32_t)mine[i];
             a.logprobs[row] = (float)(below_top(value(mine[i]), top) / (double)warm -
-                                      log(whole.sum));
+                                      log(x.whole.sum));
         }
 }
 
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void join_kernel(PickArgs a, int slices, uint32_t inverse,
+                                                       const Part *parts, const uint64_t *found) {
+    __shared__ JoinSpace<THREADS> space;
+    join<THREADS>(a, blockIdx.x, slices, inverse, parts, found, space);
+}
+
 // max_top_k = 1: the largest of the slices' best words; one wave per row.
-constexpr int FT = 256;
-__global__ __launch_bounds__(FT) void first_kernel(PickArgs a, int slices, const Part *parts,
-                                                   const uint64_t *found) {
+__device__ __forceinline__ void join_first(const PickArgs &a, int64_t row, int slices,
+                                           const Part *parts, const uint64_t *found) {
     const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * (FT / 64) + (threadIdx.x >> 6);
-    if (row >= a.rows) return;  // no barrier follows
     const int cap = slice_cap(1);
     parts += row * slices;
     found += row * slices * cap;
@@ -703,21 +725,56 @@ __global__ __launch_bounds__(FT) void first_kernel(PickArgs a, int slices, const
     }
 }
 
-// How a row is split: slices of 16384 tokens where these fill the GPU; else of
-// 2048, or with a history that every slice's threads would read for long
-// (more than 16 entries each) of 8192 with four times the threads.
-enum Split { WIDE, LONG, SMALL };
+constexpr int FT = 256;
+__global__ __launch_bounds__(FT) void first_kernel(PickArgs a, int slices, const Part *parts,
+                                                   const uint64_t *found) {
+    const int64_t row = (int64_t)blockIdx.x * (FT / 64) + (threadIdx.x >> 6);
+    if (row < a.rows) join_first(a, row, slices, parts, found);
+}
+
+// ------------------------------------------------------ both in one launch
+
+// A row of one slice: its workgroup joins what it has found.  (A row of several
+// slices could be joined by the workgroup that ends last; the fences at device
+// scope that this takes made 14.5 us of what two launches do in 7.1, at 16
+// slices of one row.)
+template <typename T, int VALUES, int GROUP, bool FIRST>
+__global__ __launch_bounds__(1024, 4) void whole_kernel(PickArgs a, uint32_t inverse, Part *parts,
+                                                        uint64_t *found) {
+    __shared__ union {
+        SliceSpace<1024, VALUES> slice;
+        JoinSpace<1024> join;
+    } space;
+    slice<T, 1024, VALUES, GROUP, FIRST>(a, parts, found, space.slice);
+    __syncthreads();
+    if (!FIRST) join<1024>(a, blockIdx.x, 1, inverse, parts, found, space.join);
+    else if (threadIdx.x < 64) join_first(a, blockIdx.x, 1, parts, found);
+}
+
+// How a row is split.  WHOLE: not at all, in one launch, while no more than one
+// workgroup of 1024 threads is wanted per CU.  At 32000 tokens one row with one candidate takes 9.2 us a call so
+// and 11.8 in two launches, which are bound by launching (8.7 and 6.7 replayed
+// in a graph); 256 rows with 1000 candidates 20.2 and 23.6; but 600 rows of
+// 16000 tokens 30.1 and 23.1.
+// WIDE: slices of 16384 tokens, where these fill the GPU.  Else SMALL, of 2048,
+// or LONG, with a history that every slice's threads would read for long (more
+// than 16 entries each), of 8192 with four times the threads: 16 rows of 150001
+// tokens with 65536 entries take 32 us so, 48 in slices of 2048.
+enum Split { WHOLE, WIDE, LONG, SMALL };
+constexpr int WHOLE_MOST = 32768;
 
 Split split_of(int64_t rows, int vocab, int64_t history) {
+    if (vocab <= WHOLE_MOST && rows <= 256) return WHOLE;
     if (rows * ((vocab + 16383) / 16384) >= 256) return WIDE;
     return history > 4096 ? LONG : SMALL;
 }
 
 int slices_of(Split s, int vocab) {
-    const int slice = s == WIDE ? 16384 : s == LONG ? 8192 : 2048;
+    const int slice = s == WHOLE ? WHOLE_MOST : s == WIDE ? 16384 : s == LONG ? 8192 : 2048;
     return (vocab + slice - 1) / slice;
 }
 
+// The workspace: a part per slice, then the candidates.
 size_t parts_bytes(int64_t rows, int slices) {
     return ((size_t)rows * slices * sizeof(Part) + 255) / 256 * 256;
 }
@@ -729,14 +786,23 @@ void run_slices(const PickArgs &a, int slices, Part *parts, uint64_t *found, hip
         <<<grid, THREADS, 0, stream>>>(a, parts, found);
 }
 
+template <typename T, int VALUES, int GROUP, bool FIRST = false>
+void run_whole(const PickArgs &a, uint32_t inverse, Part *parts, uint64_t *found,
+               hipStream_t stream) {
+    whole_kernel<T, VALUES, GROUP, FIRST>
+        <<<(unsigned)a.rows, 1024, 0, stream>>>(a, inverse, parts, found);
+}
+
 template <typename T>
 void run(const PickArgs &a, hipStream_t stream) {
     const Split split = split_of(a.rows, a.vocab, a.rules.history_capacity);
-    const int slices = slices_of(split, a.vocab);
+    const int slices = slices_of(split, a.vocab), k = a.max_top_k;
     Part *parts = static_cast<Part *>(a.workspace);
     uint64_t *found = reinterpret_cast<uint64_t *>(static_cast<char *>(a.workspace) +
                                                    parts_bytes(a.rows, slices));
-    if (a.max_top_k == 1) {
+    const int pieces = (slice_cap(k) + 63) / 64;
+    const uint32_t inverse = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
+    if (k == 1 && split != WHOLE) {
         if (split == WIDE) run_slices<T, 512, 32, 32, true>(a, slices, parts, found, stream);
         else if (split == LONG) run_slices<T, 1024, 8, 8, true>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 8, true>(a, slices, parts, found, stream);
@@ -747,20 +813,34 @@ void run(const PickArgs &a, hipStream_t stream) {
     // Groups of the histogram: at least four for each of max_top_k, so that
     // the k-th largest group bounds the k-th value closely (of values without
     // order about 1.15 k lie above it).
+    if (split == WHOLE) {
+        if (a.vocab <= 8192) {
+            if (k == 1) run_whole<T, 8, 8, true>(a, inverse, parts, found, stream);
+            else if (k <= 256) run_whole<T, 8, 8>(a, inverse, parts, found, stream);
+            else run_whole<T, 8, 2>(a, inverse, parts, found, stream);
+        } else if (a.vocab <= 16384) {
+            if (k == 1) run_whole<T, 16, 16, true>(a, inverse, parts, found, stream);
+            else if (k <= 256) run_whole<T, 16, 16>(a, inverse, parts, found, stream);
+            else run_whole<T, 16, 4>(a, inverse, parts, found, stream);
+        } else {
+            if (k == 1) run_whole<T, 32, 32, true>(a, inverse, parts, found, stream);
+            else if (k <= 256) run_whole<T, 32, 32>(a, inverse, parts, found, stream);
+            else run_whole<T, 32, 8>(a, inverse, parts, found, stream);
+        }
+        return;
+    }
     if (split == WIDE) {
-        if (a.max_top_k <= 128) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
+        if (k <= 128) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
         else run_slices<T, 512, 32, 4>(a, slices, parts, found, stream);
     } else if (split == LONG) {
-        if (a.max_top_k <= 256) run_slices<T, 1024, 8, 8>(a, slices, parts, found, stream);
+        if (k <= 256) run_slices<T, 1024, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 1024, 8, 2>(a, slices, parts, found, stream);
     } else {
-        if (a.max_top_k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
+        if (k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 256, 8, 1>(a, slices, parts, found, stream);
     }
-    const int pieces = (slice_cap(a.max_top_k) + 63) / 64;
-    const uint32_t inverse = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
     // a join of four waves where they hold all candidates
-    if (a.max_top_k <= 256 && slices * pieces <= 4 * JOIN_HELD)
+    if (k <= 256 && slices * pieces <= 4 * JOIN_HELD)
         join_kernel<256><<<(unsigned)a.rows, 256, 0, stream>>>(a, slices, inverse, parts, found);
     else
         join_kernel<1024><<<(unsigned)a.rows, 1024, 0, stream>>>(a, slices, inverse, parts, found);
@@ -770,8 +850,7 @@ void run(const PickArgs &a, hipStream_t stream) {
 
 size_t pick_workspace_bytes(int64_t rows, int vocab, int max_top_k) {
     // the finest split that these sizes may take (the history is not known)
-    const Split split = split_of(rows, vocab, 0);
-    const int slices = slices_of(split, vocab);
+    const int slices = slices_of(split_of(rows, vocab, 0), vocab);
     return parts_bytes(rows, slices) + (size_t)rows * slices * slice_cap(max_top_k) * 8;
 }
 
