@@ -756,21 +756,20 @@ __global__ __launch_bounds__(1024, 4) void whole_kernel(PickArgs a, uint32_t inv
 // and 11.8 in two launches, which are bound by launching (8.7 and 6.7 replayed
 // in a graph); 256 rows with 1000 candidates 20.2 and 23.6; but 600 rows of
 // 16000 tokens 30.1 and 23.1.
-// WIDE: slices of 16384 tokens, where these fill the GPU.  Else SMALL, of 2048,
-// or LONG, with a history that every slice's threads would read for long (more
-// than 16 entries each), of 8192 with four times the threads: 16 rows of 150001
-// tokens with 65536 entries take 32 us so, 48 in slices of 2048.
-enum Split { WHOLE, WIDE, LONG, SMALL };
+// WIDE: slices of 16384 tokens, where these fill the GPU; FINE: else, of 8192
+// with twice the threads.  One row of 131072 tokens takes 15.5 us (64
+// candidates) and 29 us (1000) in slices of 8192, 17 and 74 in slices of 2048;
+// 32 rows 16.0 in slices of 16384, 17.2 in slices of 8192.
+enum Split { WHOLE, WIDE, FINE };
 constexpr int WHOLE_MOST = 32768;
 
-Split split_of(int64_t rows, int vocab, int64_t history) {
+Split split_of(int64_t rows, int vocab) {
     if (vocab <= WHOLE_MOST && rows <= 256) return WHOLE;
-    if (rows * ((vocab + 16383) / 16384) >= 256) return WIDE;
-    return history > 4096 ? LONG : SMALL;
+    return rows * ((vocab + 16383) / 16384) >= 256 ? WIDE : FINE;
 }
 
 int slices_of(Split s, int vocab) {
-    const int slice = s == WHOLE ? WHOLE_MOST : s == WIDE ? 16384 : s == LONG ? 8192 : 2048;
+    const int slice = s == WHOLE ? WHOLE_MOST : s == WIDE ? 16384 : 8192;
     return (vocab + slice - 1) / slice;
 }
 
@@ -795,7 +794,7 @@ void run_whole(const PickArgs &a, uint32_t inverse, Part *parts, uint64_t *found
 
 template <typename T>
 void run(const PickArgs &a, hipStream_t stream) {
-    const Split split = split_of(a.rows, a.vocab, a.rules.history_capacity);
+    const Split split = split_of(a.rows, a.vocab);
     const int slices = slices_of(split, a.vocab), k = a.max_top_k;
     Part *parts = static_cast<Part *>(a.workspace);
     uint64_t *found = reinterpret_cast<uint64_t *>(static_cast<char *>(a.workspace) +
@@ -804,8 +803,7 @@ void run(const PickArgs &a, hipStream_t stream) {
     const uint32_t inverse = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
     if (k == 1 && split != WHOLE) {
         if (split == WIDE) run_slices<T, 512, 32, 32, true>(a, slices, parts, found, stream);
-        else if (split == LONG) run_slices<T, 1024, 8, 8, true>(a, slices, parts, found, stream);
-        else run_slices<T, 256, 8, 8, true>(a, slices, parts, found, stream);
+        else run_slices<T, 1024, 8, 8, true>(a, slices, parts, found, stream);
         first_kernel<<<(unsigned)((a.rows + FT / 64 - 1) / (FT / 64)), FT, 0, stream>>>(
             a, slices, parts, found);
         return;
@@ -832,12 +830,9 @@ void run(const PickArgs &a, hipStream_t stream) {
     if (split == WIDE) {
         if (k <= 128) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
         else run_slices<T, 512, 32, 4>(a, slices, parts, found, stream);
-    } else if (split == LONG) {
+    } else {
         if (k <= 256) run_slices<T, 1024, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 1024, 8, 2>(a, slices, parts, found, stream);
-    } else {
-        if (k <= 64) run_slices<T, 256, 8, 8>(a, slices, parts, found, stream);
-        else run_slices<T, 256, 8, 1>(a, slices, parts, found, stream);
     }
     // a join of four waves where they hold all candidates
     if (k <= 256 && slices * pieces <= 4 * JOIN_HELD)
@@ -849,8 +844,7 @@ void run(const PickArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t pick_workspace_bytes(int64_t rows, int vocab, int max_top_k) {
-    // the finest split that these sizes may take (the history is not known)
-    const int slices = slices_of(split_of(rows, vocab, 0), vocab);
+    const int slices = slices_of(split_of(rows, vocab), vocab);
     return parts_bytes(rows, slices) + (size_t)rows * slices * slice_cap(max_top_k) * 8;
 }
 
