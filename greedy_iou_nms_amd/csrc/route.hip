@@ -370,7 +370,7 @@ __device__ __forceinline__ double exact_score(bool softmax, float z, float top, 
 template <int LANES, int VALUES>
 __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z,
                                               const float *bias, float top, double sum,
-                                              int group_lanes) {
+                                              int e0, int group_lanes) {
     const int lane = threadIdx.x & 63, sub = lane % LANES;
     const bool softmax = a.opt.score == NMS_ROUTE_SOFTMAX, biased = a.bias != nullptr;
     const double share = inverse_of(sum);
@@ -410,12 +410,12 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z
 #pragma unroll 1
     for (int i = 0; i < a.opt.top_k; ++i) {
         double v = r[0];
-        int at = sub * VALUES;
+        int at = e0;
 #pragma unroll
         for (int j = 1; j < VALUES; ++j)
             if (r[j] > v) {
                 v = r[j];
-                at = sub * VALUES + j;
+                at = e0 + j;
             }
 #pragma unroll
         for (int d = 1; d < LANES; d <<= 1) {
@@ -428,13 +428,14 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z
         if (sub == i && v > LOWEST) mine = at;
 #pragma unroll
         for (int j = 0; j < VALUES; ++j)
-            if (at == sub * VALUES + j) r[j] = LOWEST;
+            if (v > LOWEST && r[j] == v && at == e0 + j) r[j] = LOWEST;
     }
     return mine;
 }
 
-// LANES lanes share a token, VALUES experts each: lane l has the experts
-// VALUES * l and on.  top_k is at most LANES.
+// LANES lanes share a token, VALUES experts each.  A group of experts (all of
+// them, where there are none) has group_lanes lanes, a power of two, the last
+// of which may have places that are empty.  top_k is at most LANES.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lanes) {
     constexpr int TOKENS = 64 / LANES;  // per wave
@@ -443,17 +444,21 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
     const bool inside = t < a.tokens;
     const int64_t tok = inside ? t : a.tokens - 1;
     const bool live = inside && (a.live == nullptr || a.live[tok] != 0);
-    const int E = a.experts, k = a.opt.top_k, e0 = sub * VALUES;
+    const int E = a.experts, k = a.opt.top_k, size = E / a.opt.groups;
+    // the lane's experts: e0 .. limit - 1, at most VALUES of them
+    const int g = sub / group_lanes, e0 = g * size + sub % group_lanes * VALUES;
+    const int limit = g < a.opt.groups ? (g + 1) * size : 0;
     const T *row = static_cast<const T *>(a.logits) + tok * a.row_stride;
     clear_counts(a);
 
-    // the lane's logits, past the row -infinity
+    // the lane's logits, -infinity in empty places
     T raw[VALUES];
-    if (e0 + VALUES <= E) {
+    if (e0 + VALUES <= limit) {
         __builtin_memcpy(raw, row + e0, sizeof(raw));
     } else {
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) raw[j] = e0 + j < E ? row[e0 + j] : from_f32<T>(NEG_INF);
+        for (int j = 0; j < VALUES; ++j)
+            raw[j] = e0 + j < limit ? row[e0 + j] : from_f32<T>(NEG_INF);
     }
     float z[VALUES], top = NEG_INF;
 #pragma unroll
@@ -495,11 +500,11 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         // 3 * 2^-23, and its sum with a bias by |c| 2^-24 more; the scale is
         // 2^22, and q is rounded twice
         if (a.bias != nullptr) {
-            if (e0 + VALUES <= E) {
+            if (e0 + VALUES <= limit) {
                 __builtin_memcpy(bias, a.bias + e0, sizeof(bias));
             } else {
 #pragma unroll
-                for (int j = 0; j < VALUES; ++j) bias[j] = e0 + j < E ? a.bias[e0 + j] : 0.0f;
+                for (int j = 0; j < VALUES; ++j) bias[j] = e0 + j < limit ? a.bias[e0 + j] : 0.0f;
             }
         }
         float c[VALUES], c_top = NEG_INF;
@@ -556,7 +561,6 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         if (group_lanes >= 8) merge(moved<MIRROR8>(b0), moved<MIRROR8>(b1));
         if (group_lanes >= 16) merge(moved<MIRROR16>(b0), moved<MIRROR16>(b1));
         if (group_lanes >= 32) merge(__shfl_xor(b0, 16), __shfl_xor(b1, 16));
-        const int g = sub / group_lanes;
         const bool group = g < a.opt.groups;
         const bool two = a.opt.group_top == 2;
         const uint32_t q0 = b0 >> INDEX_BITS, q1 = b1 >> INDEX_BITS;
@@ -664,7 +668,7 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
         bool low = false;
 #pragma unroll
         for (int j = 0; j < VALUES; ++j)
-            low |= z[j] > NEG_INF && bias[j] > NEG_INF && e0 + j < E;
+            low |= z[j] > NEG_INF && bias[j] > NEG_INF;
         if (at_end && low) bad = true;
     }
     int id = mine != 0u ? (int)(INDEX_MASK - (mine & INDEX_MASK)) : -1;
@@ -694,7 +698,7 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
     if (__ballot(bad) != 0ull) {
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
-        const int exact = choose_exactly<LANES, VALUES>(a, z, bias, top, sum, group_lanes);
+        const int exact = choose_exactly<LANES, VALUES>(a, z, bias, top, sum, e0, group_lanes);
         if (bad) id = exact;
     }
     write_token<T, LANES>(a, tok, inside, sub, live ? id : -1, top, sum);
@@ -887,11 +891,12 @@ bool run_quick(const RouteArgs &a, int group_lanes, hipStream_t stream) {
 // lanes a group lies.
 bool holds(const RouteArgs &a, int lanes, int values, int *group_lanes) {
     if (a.experts > lanes * values || a.opt.top_k > lanes) return false;
-    *group_lanes = 1;
+    *group_lanes = lanes;
     if (a.opt.groups == 1) return true;
-    const int size = a.experts / a.opt.groups, n = size / values;
+    int n = 1;
+    while (n * values < a.experts / a.opt.groups) n *= 2;
     *group_lanes = n;
-    return size % values == 0 && n >= 1 && (n & (n - 1)) == 0 && a.opt.groups * n <= lanes;
+    return a.opt.groups * n <= lanes;
 }
 
 template <typename T>

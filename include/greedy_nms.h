@@ -434,7 +434,7 @@ typedef enum nms_dtype { NMS_F32 = 0, NMS_F16 = 1, NMS_BF16 = 2 } nms_dtype;
 #define NMS_ROUTE_SIGMOID 1
 #define NMS_ROUTE_MAX_EXPERTS 1024
 #define NMS_ROUTE_MAX_TOP_K 64
-#define NMS_ROUTE_MAX_TOKENS (1 << 30)
+#define NMS_ROUTE_MAX_TOKENS (1 << 24)
 
 typedef struct nms_route_options {
     int score;       /* NMS_ROUTE_SOFTMAX or NMS_ROUTE_SIGMOID */
@@ -465,7 +465,8 @@ typedef struct nms_route_options {
  * Then the first top_k experts by descending c (without bias by descending
  * z), every tie to the lower index.  Their weights are scale * s, divided by
  * the sum of the chosen s if renormalise is set (for softmax: the softmax of
- * the chosen logits; all 0 where that sum is 0), rounded once to float32.
+ * the chosen logits; all 0 where that sum is 0), in float32, off by at most
+ * 2^-21 of the value.
  * Places that no expert is left for, and all places of a padded row, hold id
  * -1 and weight 0.
  * Returns NMS_OK, NMS_INVALID_ARG, NMS_TOO_LARGE (experts or tokens above the
@@ -568,7 +569,9 @@ nms_status nms_pick_workspace_size(int64_t rows, int64_t vocab, int max_top_k, s
  * w >= min_p, at least the first.  The token is the first of them at which
  * the running sum passes uniform times their sum.  Its logprob is
  * log(exp(z / t) / sum over all tokens of exp(z / t)), with t = 1 where the
- * temperature is 0.  A row without candidates gets id -1, logprob -infinity.
+ * temperature is 0; the sum is made of float32 terms, which leaves the logprob
+ * off by at most 7e-6 and its rounding.  A row without candidates gets id -1
+ * and logprob -infinity.
  * Returns NMS_OK, NMS_INVALID_ARG, NMS_WORKSPACE_TOO_SMALL, NMS_TOO_LARGE or
  * NMS_HIP_ERROR.
  */

@@ -115,7 +115,8 @@ def row_parameters(rng, B, k):
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("B,V,L", [(1, 1, 1), (2, 2, 3), (3, 63, 10), (3, 64, 50), (2, 65, 1),
                                    (5, 1000, 200), (2, 8191, 333), (2, 16384, 2000),
-                                   (3, 16385, 70), (2, 40001, 5000), (1, 100003, 30)])
+                                   (3, 16385, 70), (2, 40001, 5000), (1, 100003, 30),
+                                   (5, 131073, 600), (40, 114700, 900), (300, 17, 4097)])
 def test_adjust_sizes(B, V, L, dtype):
     rng = np.random.default_rng([B, V, L])
     note("adjust %d %d %d %s" % (B, V, L, dtype))
@@ -351,6 +352,33 @@ def test_pick_many_rows():
     z, zf = make_logits(rng, 700, 700, "bf16")
     u = make_rules(rng, 700, 700, L=50)
     check_pick(z, plain.adjust(zf, **u), rules=gpu_rules(700, u), **row_parameters(rng, 700, 12))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,V,k", [(70, 65537, 1), (70, 65537, 33), (52, 81921, 700),
+                                   (257, 20000, 20), (40, 40000, 1000), (3, 140001, 1)])
+def test_pick_rows_of_several_slices(B, V, k, dtype):
+    rng = np.random.default_rng([B, V, k])
+    z, zf = make_logits(rng, B, V, dtype)
+    u = make_rules(rng, B, V, L=800)
+    check_pick(z, plain.adjust(zf, **u), rules=gpu_rules(V, u), **row_parameters(rng, B, k))
+
+
+@pytest.mark.parametrize("B,V", [(2, 30000), (2, 90000), (70, 65537)])
+@pytest.mark.parametrize("k", [1, 50, 900])
+def test_pick_outliers_and_crowds(B, V, k):
+    """A few values far above, crowds of equal ones, and masks by the lowest
+    value of the type, whose distance no bin resolves."""
+    rng = np.random.default_rng([B, V, k])
+    z = rng.normal(size=(B, V)).astype(np.float32)
+    z[0, ::7] = 1.25
+    z[0, 5] = 3e38
+    z[1] = np.finfo(np.float32).min
+    z[1, rng.integers(0, V, size=k // 2 + 1)] = 1.0
+    z[1, V - 1] = 1e30
+    for b in range(2, B):
+        z[b, rng.random(V) < 0.99] = np.finfo(np.float32).min
+    check_pick(torch.from_numpy(z), z, uniform=rng.random(B).astype(np.float32), max_top_k=k)
 
 
 def test_pick_no_rows():

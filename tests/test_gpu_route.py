@@ -69,7 +69,9 @@ def test_sizes(T, E, k, score, dtype):
                                           (70, 256, 8, 8, 4), (7, 256, 4, 64, 5),
                                           (4, 1024, 16, 128, 20), (3, 30, 1, 30, 7),
                                           (8, 160, 6, 8, 3), (5, 1000, 9, 10, 1),
-                                          (6, 512, 8, 4, 4), (3, 1024, 4, 1024, 9)])
+                                          (6, 512, 8, 4, 4), (3, 1024, 4, 1024, 9),
+                                          (9, 12, 5, 2, 1), (5, 286, 10, 2, 2), (7, 160, 6, 8, 5),
+                                          (4, 165, 3, 11, 6), (6, 34, 4, 17, 9), (3, 990, 8, 3, 2)])
 def test_groups(T, E, k, G, kept, score):
     rng = np.random.default_rng([T, E, G])
     z, zd = make_logits(rng, T, E, "f32")
@@ -212,6 +214,24 @@ def test_gradient_of_empty_and_masked_places(renormalise, score):
     g = rng.normal(size=(8, 5)).astype(np.float32)
     g[ids < 0] = np.nan   # nothing of an empty place may get through
     check_back(torch.from_numpy(z), z.astype(np.float64), ids, g, score, renormalise, 2.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("E", [9, 200, 700])
+def test_gradient_of_an_index_that_comes_twice(E, renormalise, score):
+    """w_i = s[id_i] / sum over the places: every place adds its term."""
+    rng = np.random.default_rng(E)
+    z = rng.normal(size=(6, E)).astype(np.float32)
+    ids = rng.integers(0, 4, size=(6, 20)).astype(np.int32)
+    ids[0] = 3
+    g = rng.normal(size=(6, 20)).astype(np.float32)
+    check_back(torch.from_numpy(z), z.astype(np.float64), ids, g, score, renormalise, 1.0)
+    dev = device()
+    on = [torch.from_numpy(a).to(dev) for a in (z, ids, g)]
+    first = lib().route_experts_backward(*on, score, renormalise)
+    for _ in range(5):
+        assert torch.equal(first, lib().route_experts_backward(*on, score, renormalise))
 
 
 def test_gradient_against_differences_of_the_forward():
