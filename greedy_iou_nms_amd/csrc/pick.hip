@@ -149,7 +149,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     constexpr int WAVES = THREADS / 64;
     uint32_t *word = x.word, *bit = x.bit, *hist = x.hist;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    static_assert(WAVES >= EDGES, "a wave for each x.bound");
+    static_assert(WAVES >= EDGES, "a wave for each bound");
     const int64_t row = blockIdx.x;
     const int64_t part = row * gridDim.y + blockIdx.y;
     const int lo = (int)blockIdx.y * SLICE;
@@ -175,10 +175,10 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, word, bit, z);
     // The groups' largest values and the wave's, and the softmax sum relative
     // to that: exp2(z c - top c), one multiply-add and one exponential a value,
-    // where the rounding of top c is a factor of all terms and is x.taken out of
+    // where the rounding of top c is a factor of all terms and is taken out of
     // the sum.  A NaN, an infinite top, a c of 0 or a product of 2^24 and more
-    // show in the sum or in what is x.taken out; then the values are gone over
-    // again, with a NaN made -infinity and each difference x.taken by itself.
+    // show in the sum or in what is taken out; then the values are gone over
+    // again, with a NaN made -infinity and each difference taken by itself.
     float m[VALUES / GROUP], top, sum;
     for (bool again = false;; again = true) {
         if (again) {
@@ -262,13 +262,13 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
         if (m[g] > NEG_INF) atomicAdd(&hist[bins.of(m[g], BINS)], 1u);
     __syncthreads();
     if (wave < EDGES) {
-        // a wave per x.bound
+        // a wave per bound
         const int b = Ranks<BINS / 64>(hist).bin((uint32_t)(k + (1 << wave) - 1) >> wave);
         if ((tid & 63) == 0) x.bound[wave] = b < 0 ? NEG_INF : bins.edge(b);
     }
     if (tid == 0) x.lowest = ordered(__builtin_inff());
     __syncthreads();
-    // at least k values lie at the x.bound or above; without one, all values
+    // at least k values lie at the bound or above; without one, all values
     // are candidates
     const float first = x.bound[0];
     float edge = fminf(fmaxf(first, -3.402823466e38f), 3.402823466e38f);

@@ -831,10 +831,22 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
             for (int j = 0; j < VALUES; ++j) z[j] *= inverse;
         }
     } else {
-        float weighted = 0.0f;
+        // shares of the chosen scores' sum, each score divided by exp(m) first,
+        // m = min(largest chosen logit, 0): below -88 a score itself is under
+        // float32's range, its share and its gradient are not
+        float m = 0.0f;
+        if (a.opt.renormalise) {
+#pragma unroll
+            for (int q = 0; q < CHOSEN; ++q) top = fmaxf(top, zc[q]);
+            m = fminf(unordered(all_max<LANES>(ordered(top))), 0.0f);
+        }
+        float weighted = 0.0f, rest[CHOSEN];  // rest: 1 - score
 #pragma unroll
         for (int q = 0; q < CHOSEN; ++q) {
-            s[q] = zc[q] == NEG_INF ? 0.0f : 1.0f / (1.0f + expf(-zc[q]));
+            rest[q] = 1.0f / (1.0f + expf(zc[q]));
+            s[q] = zc[q] == NEG_INF ? 0.0f
+                   : zc[q] > 0.0f   ? 1.0f / (1.0f + expf(-zc[q]))
+                                    : expf(zc[q] - m) * rest[q];
             total += s[q];
             weighted += g[q] * s[q];
         }
@@ -846,11 +858,8 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
             total = 1.0f;
         }
 #pragma unroll
-        for (int q = 0; q < CHOSEN; ++q) {
-            // s (1 - s)
-            const float slope = s[q] == 0.0f ? 0.0f : s[q] / (1.0f + expf(zc[q]));
-            d[q] = total > 0.0f ? (g[q] - inner) / total * slope : 0.0f;
-        }
+        for (int q = 0; q < CHOSEN; ++q)
+            d[q] = total > 0.0f ? (g[q] - inner) * (s[q] / total) * rest[q] : 0.0f;
     }
 #pragma unroll
     for (int q = 0; q < CHOSEN; ++q)

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 from typing import Optional, Tuple
 
 import torch
@@ -108,12 +109,23 @@ def _vector(t, name: str, n: int, dtype, device) -> Optional[int]:
     raise ValueError("%s must be contiguous" % name)
 
 
+def _int32(v, name: str) -> None:
+    """ctypes would cut what does not fit a C int."""
+    if not -2 ** 31 <= operator.index(v) < 2 ** 31:
+        raise ValueError("%s is out of range (got %d)" % (name, v))
+
+
 # ------------------------------------------------------------------- routing
 
 @functools.lru_cache(maxsize=256)
 def _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top):
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
+    _int32(top_k, "top_k")
+    _int32(groups, "groups")
+    _int32(group_top, "group_top")
+    if kept_groups is not None:
+        _int32(kept_groups, "kept_groups")
     return ctypes.byref(_RouteOptions(
         _SCORES[score], int(top_k), int(bool(renormalise)), float(scale), int(groups),
         int(groups if kept_groups is None else kept_groups), int(group_top)))
@@ -142,9 +154,10 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     options = _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top)
     b = None if bias is None else _vector(bias, "bias", experts, torch.float32, device)
     alive = None if live is None else _vector(
-        live, "live", tokens, torch.bool if live.dtype is torch.bool else torch.uint8, device)
+        live, "live", tokens, torch.bool if getattr(live, "dtype", None) is torch.bool
+        else torch.uint8, device)
     # a call that will be refused allocates no negative shape
-    shape = (tokens, max(int(top_k), 0))
+    shape = (tokens, max(top_k, 0))
     ids = torch.empty(shape, dtype=torch.int32, device=device)
     weights = torch.empty(shape, dtype=torch.float32, device=device)
     count = torch.empty(experts, dtype=torch.int32, device=device) if counts else None
@@ -161,7 +174,8 @@ def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights
                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of ``route_experts``' weights in its logits, from the
     forward call's ``ids`` and the gradient of its weights; a tensor like
-    ``logits`` (or ``out``).  The choice of the experts, and so the bias, has
+    ``logits`` (or ``out``, which may be ``logits`` itself and must not overlap
+    it otherwise).  The choice of the experts, and so the bias, has
     no gradient."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
@@ -279,13 +293,19 @@ class LogitRules:
         return self._ref
 
 
+def _rules(rules, rows: int, vocab: int, device) -> object:
+    if not isinstance(rules, LogitRules):
+        raise TypeError("rules must be LogitRules")
+    return rules._for(rows, vocab, device)
+
+
 def adjust_logits(logits: torch.Tensor, rules: LogitRules,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The logits under the rules, a tensor like ``logits`` (or ``out``, which
     may be ``logits`` itself and must not overlap it otherwise)."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
-    ref = rules._for(rows, vocab, device)
+    ref = _rules(rules, rows, vocab, device)
     if device.index != _current_device():
         with torch.cuda.device(device):
             return adjust_logits(logits, rules, out)
@@ -303,6 +323,8 @@ def adjust_logits(logits: torch.Tensor, rules: LogitRules,
 
 @functools.lru_cache(maxsize=256)
 def pick_workspace_size(rows: int, vocab: int, max_top_k: int) -> int:
+    """The bytes of workspace that ``pick_tokens`` takes."""
+    _int32(max_top_k, "max_top_k")
     out = ctypes.c_size_t(0)
     _check(_lib.nms_pick_workspace_size(rows, vocab, max_top_k, ctypes.byref(out)))
     return int(out.value)
@@ -330,7 +352,7 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     k = None if top_k is None else _vector(top_k, "top_k", rows, torch.int32, device)
     p = None if top_p is None else _vector(top_p, "top_p", rows, f32, device)
     m = None if min_p is None else _vector(min_p, "min_p", rows, f32, device)
-    ref = None if rules is None else rules._for(rows, vocab, device)
+    ref = None if rules is None else _rules(rules, rows, vocab, device)
     if device.index != _current_device():
         with torch.cuda.device(device):
             return pick_tokens(logits, uniform, max_top_k, temperature, top_k, top_p, min_p,

@@ -487,7 +487,8 @@ nms_status nms_route_experts(const void *logits, nms_dtype dtype, int64_t tokens
  *   grad_weights  device float[tokens * top_k]: the gradient of the weights.
  *   grad_logits   device, tokens rows of `experts` elements of dtype,
  *                 grad_stride elements apart; every element is written
- *                 (0 in rows without a chosen expert).
+ *                 (0 in rows without a chosen expert); may be logits, with
+ *                 the same stride, and must not overlap it otherwise.
  * Computed in float32, rounded once.  Returns as nms_route_experts.
  */
 nms_status nms_route_experts_backward(const void *logits, nms_dtype dtype, int64_t tokens,

@@ -347,6 +347,19 @@ def test_pick_strided_and_offset_rows():
         check_pick(one, zf[1:2], **row_parameters(rng, 1, 20))
 
 
+def test_rows_more_than_2_to_31_elements_apart():
+    rng = np.random.default_rng(16)
+    stride, V = 2 ** 31 + 40, 33000
+    flat = torch.empty(2 * stride + V, dtype=torch.bfloat16, device=device())
+    apart = flat.as_strided((3, V), (stride, 1))
+    z, zf = make_logits(rng, 3, V, "bf16")
+    u = make_rules(rng, 3, V, L=30)
+    apart.copy_(z)
+    check_pick(apart, plain.adjust(zf, **u), rules=gpu_rules(V, u), **row_parameters(rng, 3, 20))
+    assert lib().adjust_logits(apart, gpu_rules(V, u), out=apart) is apart
+    same(apart, plain.adjust(zf, **u))
+
+
 def test_pick_many_rows():
     rng = np.random.default_rng(14)
     z, zf = make_logits(rng, 700, 700, "bf16")
@@ -562,6 +575,12 @@ def test_refusals():
         with pytest.raises(g.NMSError) as e:
             g.pick_tokens(z, u, max_top_k=k)
         assert e.value.status == "NMS_INVALID_ARG"
+    with pytest.raises(ValueError):
+        g.pick_tokens(z, u, max_top_k=2 ** 32 + 5)
+    with pytest.raises(TypeError):
+        g.pick_tokens(z, u, rules={"repetition": u})
+    with pytest.raises(TypeError):
+        g.adjust_logits(z, None)
     with pytest.raises(TypeError):
         g.pick_tokens(z, None)
     with pytest.raises(ValueError):

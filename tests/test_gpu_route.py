@@ -160,6 +160,20 @@ def test_no_tokens():
     assert lib().route_experts_backward(z, ids, w).shape == (0, 16)
 
 
+def test_rows_more_than_2_to_31_elements_apart():
+    rng = np.random.default_rng(15)
+    stride = 2 ** 31 + 24
+    flat = torch.empty(2 * stride + 64, dtype=torch.bfloat16, device=device())
+    apart = flat.as_strided((3, 64), (stride, 1))
+    z, zd = make_logits(rng, 3, 64, "bf16")
+    apart.copy_(z)
+    check_route(apart, zd, top_k=6, score="sigmoid")
+    ids, w = lib().route_experts(apart, 6)
+    want = lib().route_experts_backward(z.to(device()), ids, w)
+    assert lib().route_experts_backward(apart, ids, w, out=apart) is apart
+    assert torch.equal(apart, want)
+
+
 def test_many_tokens():
     rng = np.random.default_rng(8)
     z, zd = make_logits(rng, 3001, 72, "bf16")
@@ -214,6 +228,21 @@ def test_gradient_of_empty_and_masked_places(renormalise, score):
     g = rng.normal(size=(8, 5)).astype(np.float32)
     g[ids < 0] = np.nan   # nothing of an empty place may get through
     check_back(torch.from_numpy(z), z.astype(np.float64), ids, g, score, renormalise, 2.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("offset", [-90.0, -200.0, -600.0, 90.0])
+def test_gradient_of_far_logits(offset, renormalise, score, dtype):
+    """Scores that float32 does not hold, shares of their sum that it does."""
+    rng = np.random.default_rng(int(abs(offset)))
+    z, zd = make_logits(rng, 8, 40, dtype)
+    z = (z.float() + offset).to(z.dtype)
+    zd = z.double().numpy()
+    ids, _, _ = plain.route(zd, 6, score)
+    g = rng.normal(size=(8, 6)).astype(np.float32)
+    check_back(z, zd, ids, g, score, renormalise, 1.0)
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -307,6 +336,14 @@ def test_refusals():
     assert e.value.status == "NMS_TOO_LARGE"
     with pytest.raises(ValueError):
         g.route_experts(z, 2, score="relu")
+    for kw in (dict(top_k=2 ** 32 + 2), dict(top_k=2, groups=2 ** 32 + 1),
+               dict(top_k=2, kept_groups=2 ** 32 + 1), dict(top_k=2, group_top=2 ** 32 + 1)):
+        with pytest.raises(ValueError):
+            g.route_experts(z, **kw)
+    with pytest.raises(TypeError):
+        g.route_experts(z, 2.5)
+    with pytest.raises(TypeError):
+        g.route_experts(z, 2, live=[1, 1, 1, 1])
     with pytest.raises(TypeError):
         g.route_experts(z.double(), 2)
     with pytest.raises(ValueError):
