@@ -736,8 +736,9 @@ static_assert(CT == NMS_ROUTE_MAX_EXPERTS, "a thread per expert");
 //   sigmoid                    w_i = scale s_i / D, D = 1 or sum of chosen s:
 //       dz_j = scale (g_j - [renormalised] sum_i g_i s_i / D) / D s_j (1 - s_j)
 // Only the first needs the whole row.  LANES lanes share a token, VALUES
-// experts each; the chosen experts' terms go to their places through LDS, one
-// after another, so that an index that comes twice adds up in a fixed order.
+// experts each; the chosen experts' terms go to their places through LDS, all
+// at once, or one after another where an index comes twice, so that it adds up
+// in a fixed order.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
     constexpr int TOKENS = 64 / LANES;            // per wave
@@ -788,17 +789,17 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
 #pragma unroll
     for (int j = 0; j < VALUES; ++j) place[mine][e0 + j] = 0.0f;
 
+    // exp(v - top) by the exponential instruction: the product with log2 e is
+    // rounded to 2^-24 of itself, as the difference is
+    constexpr float LOG2E = 1.44269504f;
     const auto share = [](float v, float top) {
-        return v == top ? 1.0f : v == NEG_INF ? 0.0f : expf(v - top);
+        return v == top ? 1.0f : __builtin_amdgcn_exp2f((v - top) * LOG2E);
     };
     float top = NEG_INF, total = 0.0f, inner = 0.0f, s[CHOSEN], d[CHOSEN];
     if (softmax) {
         if (whole) {
 #pragma unroll
-            for (int j = 0; j < VALUES; ++j) {
-                z[j] = z[j] > NEG_INF ? z[j] : NEG_INF;
-                top = fmaxf(top, z[j]);
-            }
+            for (int j = 0; j < VALUES; ++j) top = fmaxf(top, z[j]);
         } else {
 #pragma unroll
             for (int q = 0; q < CHOSEN; ++q) top = fmaxf(top, zc[q]);
@@ -807,16 +808,32 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
 #pragma unroll
         for (int q = 0; q < CHOSEN; ++q) s[q] = zc[q] == NEG_INF ? 0.0f : share(zc[q], top);
         if (whole) {
+            // a NaN or an infinite top shows in the sum, which is 1 at least
+            // else; then every term is looked at
+            const float base = fabsf(top) < __builtin_inff() ? top : 0.0f;
+            float p[VALUES];
 #pragma unroll
             for (int j = 0; j < VALUES; ++j) {
-                z[j] = z[j] == NEG_INF ? 0.0f : share(z[j], top);
-                total += z[j];
+                p[j] = __builtin_amdgcn_exp2f((z[j] - base) * LOG2E);
+                total += p[j];
             }
+            total = all_sum<LANES>(total);
+            if (__ballot(!(total < 3.0e38f)) != 0ull) {
+                total = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VALUES; ++j) {
+                    p[j] = z[j] > NEG_INF ? share(z[j], top) : 0.0f;
+                    total += p[j];
+                }
+                total = all_sum<LANES>(total);
+            }
+#pragma unroll
+            for (int j = 0; j < VALUES; ++j) z[j] = p[j];
         } else {
 #pragma unroll
             for (int q = 0; q < CHOSEN; ++q) total += s[q];
+            total = all_sum<LANES>(total);
         }
-        total = all_sum<LANES>(total);
         const float inverse = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
         for (int q = 0; q < CHOSEN; ++q) {
@@ -833,7 +850,8 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
     } else {
         // shares of the chosen scores' sum, each score divided by exp(m) first,
         // m = min(largest chosen logit, 0): below -88 a score itself is under
-        // float32's range, its share and its gradient are not
+        // float32's range, its share and its gradient are not.  From -709.78
+        // down a score is 0 in binary64 too, and so are the forward's weights.
         float m = 0.0f;
         if (a.opt.renormalise) {
 #pragma unroll
@@ -844,9 +862,9 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
 #pragma unroll
         for (int q = 0; q < CHOSEN; ++q) {
             rest[q] = 1.0f / (1.0f + expf(zc[q]));
-            s[q] = zc[q] == NEG_INF ? 0.0f
-                   : zc[q] > 0.0f   ? 1.0f / (1.0f + expf(-zc[q]))
-                                    : expf(zc[q] - m) * rest[q];
+            s[q] = zc[q] <= -709.78271f ? 0.0f
+                   : zc[q] > 0.0f       ? 1.0f / (1.0f + expf(-zc[q]))
+                                        : expf(zc[q] - m) * rest[q];
             total += s[q];
             weighted += g[q] * s[q];
         }
@@ -861,12 +879,30 @@ __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
         for (int q = 0; q < CHOSEN; ++q)
             d[q] = total > 0.0f ? (g[q] - inner) * (s[q] / total) * rest[q] : 0.0f;
     }
+    // Every chosen place keeps the number of one term that goes there: where
+    // each term finds its own, no index comes twice.
+    bool twice = false;
+    wave_fence();
 #pragma unroll
     for (int q = 0; q < CHOSEN; ++q)
-        for (int l = 0; l < LANES && q * LANES + l < k; ++l) {
-            wave_fence();
-            if (sub == l && id[q] >= 0) place[mine][id[q]] += d[q];
-        }
+        if (id[q] >= 0) place[mine][id[q]] = (float)(q * LANES + sub);
+    wave_fence();
+#pragma unroll
+    for (int q = 0; q < CHOSEN; ++q)
+        if (id[q] >= 0) twice |= place[mine][id[q]] != (float)(q * LANES + sub);
+    wave_fence();
+    const bool in_turn = __ballot(twice) != 0ull;
+#pragma unroll
+    for (int q = 0; q < CHOSEN; ++q)
+        if (id[q] >= 0) place[mine][id[q]] = in_turn ? 0.0f : d[q];
+    if (in_turn) {
+#pragma unroll
+        for (int q = 0; q < CHOSEN; ++q)
+            for (int l = 0; l < LANES && q * LANES + l < k; ++l) {
+                wave_fence();
+                if (sub == l && id[q] >= 0) place[mine][id[q]] += d[q];
+            }
+    }
     wave_fence();
     if (!inside) return;
     T out[VALUES];

@@ -230,6 +230,22 @@ def test_gradient_of_empty_and_masked_places(renormalise, score):
     check_back(torch.from_numpy(z), z.astype(np.float64), ids, g, score, renormalise, 2.0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("E", [20, 600])
+def test_gradient_of_infinite_logits(E, renormalise, score):
+    rng = np.random.default_rng(E + 1)
+    z = rng.normal(size=(6, E)).astype(np.float32)
+    z[0, 3] = np.inf
+    z[1, [2, 11]] = np.inf
+    z[2, 5:] = np.finfo(np.float32).min
+    z[3] = np.finfo(np.float32).min
+    z[4, 7] = np.finfo(np.float32).max
+    ids, _, _ = plain.route(z.astype(np.float64), 4, score)
+    g = rng.normal(size=(6, 4)).astype(np.float32)
+    check_back(torch.from_numpy(z), z.astype(np.float64), ids, g, score, renormalise, 1.0)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalise", [False, True])
