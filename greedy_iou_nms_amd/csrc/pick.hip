@@ -339,9 +339,8 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
 }
 
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
-__global__ __launch_bounds__(THREADS, VALUES == 32 ? 4 : 8) void slice_kernel(PickArgs a,
-                                                                              Part *parts,
-                                                                              uint64_t *found) {
+__global__ __launch_bounds__(THREADS, 8) void slice_kernel(PickArgs a, Part *parts,
+                                                           uint64_t *found) {
     __shared__ SliceSpace<THREADS, VALUES> space;
     slice<T, THREADS, VALUES, GROUP, FIRST>(a, parts, found, space);
 }
@@ -751,26 +750,25 @@ __global__ __launch_bounds__(1024, 4) void whole_kernel(PickArgs a, uint32_t inv
     else if (threadIdx.x < 64) join_first(a, blockIdx.x, 1, parts, found);
 }
 
-// How a row is split.  WHOLE: not at all, in one launch, while no more than one
-// workgroup of 1024 threads is wanted per CU.  At 32000 tokens one row with one candidate takes 9.2 us a call so
-// and 11.8 in two launches, which are bound by launching (8.7 and 6.7 replayed
-// in a graph); 256 rows with 1000 candidates 20.2 and 23.6; but 600 rows of
-// 16000 tokens 30.1 and 23.1.
-// WIDE: slices of 16384 tokens, where these fill the GPU; FINE: else, of 8192
-// with twice the threads.  One row of 131072 tokens takes 15.5 us (64
-// candidates) and 29 us (1000) in slices of 8192, 17 and 74 in slices of 2048;
-// 32 rows 16.0 in slices of 16384, 17.2 in slices of 8192.
-enum Split { WHOLE, WIDE, FINE };
+// How a row is split.  Not at all, in one launch, while no more than one
+// workgroup of 1024 threads is wanted per CU: at 32000 tokens one row with one
+// candidate takes 9.2 us a call so and 11.8 in two launches, which are bound by
+// launching (8.7 and 6.7 replayed in a graph); 256 rows with 1000 candidates
+// 20.2 and 23.6; but 600 rows of 16000 tokens 30.1 and 22.0.
+// Else in slices of 16384 tokens, or of 8192 where the vocabulary has no more
+// (300 rows of 8000 with 50 candidates: 15.9 us, and 17.0 in one of 16384).
+// Slices of 8192 have twice the candidates to join and every slice reads the
+// whole history: 17 rows of 131072 with 1000 candidates take 33 us in them and
+// 23 in slices of 16384, 256 rows 93 and 59; one row with 50 candidates 15.0
+// and 14.6.  512 threads with 32 tokens each made 65 us of the 59.
 constexpr int WHOLE_MOST = 32768;
 
-Split split_of(int64_t rows, int vocab) {
-    if (vocab <= WHOLE_MOST && rows <= 256) return WHOLE;
-    return rows * ((vocab + 16383) / 16384) >= 256 ? WIDE : FINE;
-}
+bool whole(int64_t rows, int vocab) { return vocab <= WHOLE_MOST && rows <= 256; }
 
-int slices_of(Split s, int vocab) {
-    const int slice = s == WHOLE ? WHOLE_MOST : s == WIDE ? 16384 : 8192;
-    return (vocab + slice - 1) / slice;
+int slice_of(int vocab) { return vocab <= 8192 ? 8192 : 16384; }
+
+int slices_of(int64_t rows, int vocab) {
+    return whole(rows, vocab) ? 1 : (vocab + slice_of(vocab) - 1) / slice_of(vocab);
 }
 
 // The workspace: a part per slice, then the candidates.
@@ -794,15 +792,15 @@ void run_whole(const PickArgs &a, uint32_t inverse, Part *parts, uint64_t *found
 
 template <typename T>
 void run(const PickArgs &a, hipStream_t stream) {
-    const Split split = split_of(a.rows, a.vocab);
-    const int slices = slices_of(split, a.vocab), k = a.max_top_k;
+    const bool one = whole(a.rows, a.vocab), wide = slice_of(a.vocab) == 16384;
+    const int slices = slices_of(a.rows, a.vocab), k = a.max_top_k;
     Part *parts = static_cast<Part *>(a.workspace);
     uint64_t *found = reinterpret_cast<uint64_t *>(static_cast<char *>(a.workspace) +
                                                    parts_bytes(a.rows, slices));
     const int pieces = (slice_cap(k) + 63) / 64;
     const uint32_t inverse = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
-    if (k == 1 && split != WHOLE) {
-        if (split == WIDE) run_slices<T, 512, 32, 32, true>(a, slices, parts, found, stream);
+    if (k == 1 && !one) {
+        if (wide) run_slices<T, 1024, 16, 16, true>(a, slices, parts, found, stream);
         else run_slices<T, 1024, 8, 8, true>(a, slices, parts, found, stream);
         first_kernel<<<(unsigned)((a.rows + FT / 64 - 1) / (FT / 64)), FT, 0, stream>>>(
             a, slices, parts, found);
@@ -811,7 +809,7 @@ void run(const PickArgs &a, hipStream_t stream) {
     // Groups of the histogram: at least four for each of max_top_k, so that
     // the k-th largest group bounds the k-th value closely (of values without
     // order about 1.15 k lie above it).
-    if (split == WHOLE) {
+    if (one) {
         if (a.vocab <= 8192) {
             if (k == 1) run_whole<T, 8, 8, true>(a, inverse, parts, found, stream);
             else if (k <= 256) run_whole<T, 8, 8>(a, inverse, parts, found, stream);
@@ -827,9 +825,9 @@ void run(const PickArgs &a, hipStream_t stream) {
         }
         return;
     }
-    if (split == WIDE) {
-        if (k <= 128) run_slices<T, 512, 32, 32>(a, slices, parts, found, stream);
-        else run_slices<T, 512, 32, 4>(a, slices, parts, found, stream);
+    if (wide) {
+        if (k <= 256) run_slices<T, 1024, 16, 16>(a, slices, parts, found, stream);
+        else run_slices<T, 1024, 16, 4>(a, slices, parts, found, stream);
     } else {
         if (k <= 256) run_slices<T, 1024, 8, 8>(a, slices, parts, found, stream);
         else run_slices<T, 1024, 8, 2>(a, slices, parts, found, stream);
@@ -844,7 +842,7 @@ void run(const PickArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t pick_workspace_bytes(int64_t rows, int vocab, int max_top_k) {
-    const int slices = slices_of(split_of(rows, vocab), vocab);
+    const int slices = slices_of(rows, vocab);
     return parts_bytes(rows, slices) + (size_t)rows * slices * slice_cap(max_top_k) * 8;
 }
 
