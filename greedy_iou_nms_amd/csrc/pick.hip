@@ -430,7 +430,7 @@ __device__ __forceinline__ Part lane_part(const Part *parts, int slices) {
 
 template <int THREADS>
 struct JoinSpace {  // in LDS
-    uint64_t list[THREADS + CROWDED], sorted[THREADS];
+    uint64_t list[THREADS + CROWDED + 4], sorted[THREADS];
     // per bin: its count of held candidates, then its first place; its count
     // of the rest, then the next place of the rest; and its end
     uint32_t hist[JOIN_BINS], rest[JOIN_BINS], ends[JOIN_BINS];
@@ -579,7 +579,11 @@ __device__ __forceinline__ void join(const PickArgs &a, int64_t row, int slices,
             if (w == 0) break;
             const int b = bins.of(value(w), JOIN_BINS);
             uint32_t rank = hist[b];
-            for (uint32_t y = rank, last = ends[b]; y < last; ++y) rank += list[y] > w ? 1u : 0u;
+            // four at a time, of which the last may lie past the bin
+            for (uint32_t y = rank, last = ends[b]; y < last; y += 4)
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c)
+                    rank += list[y + c] > w && y + c < last ? 1u : 0u;
             if (rank < (uint32_t)THREADS) sorted[rank] = w;
         }
     } else {
