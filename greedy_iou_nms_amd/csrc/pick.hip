@@ -142,6 +142,12 @@ struct SliceSpace {  // in LDS
     uint32_t taken, chosen[2];
 };
 
+// Instructions bound it: a wave (1024 tokens) issues 230 for the values, the
+// maximum and the softmax sum, 120 more to find 50 candidates, 240 to find
+// 1000, 155 for a history of 4096, 40 for biases and 25 for a mask.  256 rows
+// of 131072 bfloat16 logits with all of these take 50.5 us, 38 of them issuing,
+// where reading the 72 MB takes 14; 64 rows of 100003 float32 logits with 50
+// candidates 12.6 us (reading: 5).
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
 __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *found,
                                       SliceSpace<THREADS, VALUES> &x) {
@@ -441,6 +447,10 @@ struct JoinSpace {  // in LDS
     uint32_t taken, crowded, inside, chosen[2];
 };
 
+// Latency bounds it, a chain of loads, seven barriers and the exponentials:
+// 6.6 us for 64 rows with 50 candidates, of which 1.8 are the loads and 1 the
+// slices' sums.  256 rows with 1000 candidates of each of 8 slices take 15.4
+// us, 5 of them to read the 19 MB of candidates.
 template <int THREADS>
 __device__ __forceinline__ void join(const PickArgs &a, int64_t row, int slices, uint32_t inverse,
                                      const Part *parts, const uint64_t *found,

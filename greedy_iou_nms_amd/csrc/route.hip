@@ -436,6 +436,14 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z
 // LANES lanes share a token, VALUES experts each.  A group of experts (all of
 // them, where there are none) has group_lanes lanes, a power of two, the last
 // of which may have places that are empty.  top_k is at most LANES.
+//
+// A token's row is read once, in one load per lane, and everything after it
+// stays in registers: what bounds a large call is the instructions (Batcher's
+// sort per lane, then top_k maxima over the lanes), not memory.  16384 tokens
+// of 256 float32 experts in 8 groups, top 8: 11.2 us, where reading them takes
+// 3.3 us; 5003 of 60 float16 experts, top 4: 4.3 us; a decode step of 8 tokens
+// 3.5 us, all of it latency.  16 lanes rather than a wave per token leave four
+// tokens' steps to share each instruction.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lanes) {
     constexpr int TOKENS = 64 / LANES;  // per wave
@@ -706,6 +714,11 @@ __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lan
 }
 
 // Adds the experts of ids[0..n) to the counts; a single workgroup writes them.
+// A launch of its own: 2 to 4 us on the GPU behind quick_kernel (131072 ids of
+// 256 experts 3.8 us) and 3.3 us of the caller's time.  Routing all tokens in
+// one workgroup that counts them itself saves 2.5 us of an eager call of 64
+// tokens and 64 experts, but takes 6.2 us in a graph where the two launches
+// take 4.9, and 20 for 7 at 128 tokens of 256 experts.
 constexpr int CT = 1024, COUNTED = 4096;  // threads; ids per workgroup
 __global__ __launch_bounds__(CT) void count_kernel(const int32_t *ids, int64_t n, int experts,
                                                    int32_t *counts) {
@@ -738,7 +751,10 @@ static_assert(CT == NMS_ROUTE_MAX_EXPERTS, "a thread per expert");
 // Only the first needs the whole row.  LANES lanes share a token, VALUES
 // experts each; the chosen experts' terms go to their places through LDS, all
 // at once, or one after another where an index comes twice, so that it adds up
-// in a fixed order.
+// in a fixed order.  32768 tokens of 128 bfloat16 experts, plain softmax: 7.1
+// us, of which 3.8 are instructions (283 per wave of four tokens) and 3.6 would
+// be the reading and writing alone (19 MB); one term after another took 8.9,
+// the library's exponential 8.7.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
     constexpr int TOKENS = 64 / LANES;            // per wave
