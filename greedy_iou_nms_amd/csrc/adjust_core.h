@@ -2,9 +2,9 @@
 // nms_pick_tokens.
 //
 // One word of LDS per token of the slice gathers what the history and the
-// bias list say about it: how often it was generated (20 bits), whether it was
-// seen in the prompt, and the place of its last bias entry plus one (11 bits);
-// one bit per token says whether there is anything.  Then every thread looks
+// bias list say about it: how often it was generated (20 bits) and the place
+// of its last bias entry plus one (11 bits); one bit per token says whether it
+// is in the history, another whether it is in the bias list.  Then every thread looks
 // through the bits of its own tokens, replaces the words of those touched by
 // their adjusted values, and selects between these and the logits.  That is
 // as many rounds as the wave's fullest lane has touched tokens, where
@@ -17,8 +17,6 @@
 namespace gnms {
 
 constexpr uint32_t RULE_COUNT = (1u << 20) - 1u;
-constexpr uint32_t RULE_SEEN = 1u << 20;
-constexpr uint32_t RULE_TOUCHED = RULE_SEEN | RULE_COUNT;  // by the history
 constexpr int RULE_BIAS_SHIFT = 21;
 static_assert(NMS_MAX_HISTORY == RULE_COUNT, "a count fits its field");
 static_assert(NMS_MAX_BIASES < (1 << (32 - RULE_BIAS_SHIFT)), "a place fits its field");
@@ -67,20 +65,27 @@ __device__ __forceinline__ RowRules row_rules(const nms_logit_rules &u, int64_t 
     return r;
 }
 
-// Four neighbouring entries of a history from i on; -1 past its capacity.
+// Four neighbouring entries of a history.
 struct FourTokens {
     int v[4];
 };
 
-__device__ __forceinline__ FourTokens load4(const int32_t *history, int i, int capacity) {
+// A wave's next 256 entries from base on, four per lane; -1 from limit on.
+__device__ __forceinline__ FourTokens load4(const int32_t *history, int base, int limit) {
     FourTokens f;
-    if (i + 4 <= capacity) {
+    const int i = base + 4 * (int)(threadIdx.x & 63);
+    if (base + 256 <= limit) {  // the same for the whole wave
         __builtin_memcpy(&f, history + i, sizeof(f));
     } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) f.v[c] = i + c < capacity ? history[i + c] : -1;
+        for (int c = 0; c < 4; ++c) f.v[c] = i + c < limit ? history[i + c] : -1;
     }
     return f;
+}
+
+// The first of a wave's entries, in the first round.
+__device__ __forceinline__ int wave_entry() {
+    return __builtin_amdgcn_readfirstlane(4 * (int)(threadIdx.x & ~63u));
 }
 
 // Where the word of a slice's token lies: threads read the words of eight
@@ -95,8 +100,8 @@ __device__ __forceinline__ unsigned slot(unsigned at) {
 // The adjusted value of a touched token, but for its mask.  Every operation
 // is one binary32 operation (compiled without contraction).
 __device__ __forceinline__ float replaced(const nms_logit_rules &u, const RowRules &r, int64_t row,
-                                          float z, uint32_t word) {
-    if (word & RULE_TOUCHED) z = z > 0.0f ? z / r.repetition : z * r.repetition;
+                                          float z, bool seen, uint32_t word) {
+    if (seen) z = z > 0.0f ? z / r.repetition : z * r.repetition;
     const uint32_t count = word & RULE_COUNT;
     if (count > 0u) {
         z = z - r.frequency * (float)count;
@@ -107,55 +112,77 @@ __device__ __forceinline__ float replaced(const nms_logit_rules &u, const RowRul
     return z;
 }
 
-// Gathers the rules of the tokens lo..lo+size-1 of the row in word[0..SLICE)
-// and bit[0..SLICE / 32).  Every thread of the workgroup calls it, and it ends
-// with a barrier.
+// What a slice's rules are gathered in: a word per token, and the bits of
+// those in the history and of those in the bias list.
+template <int SLICE>
+struct alignas(16) RuleSpace {
+    uint32_t seen[SLICE / 32], listed[SLICE / 32], word[SLICE];
+};
+
+// Gathers the rules of the tokens lo..lo+size-1 of the row.  early: the first
+// entries, load4 up to the capacity.  Every thread of the workgroup calls it,
+// and it ends with a barrier.
 template <int THREADS, int SLICE>
 __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowRules &r,
                                             int64_t row, int lo, int size,
-                                            const FourTokens &early, uint32_t *word,
-                                            uint32_t *bit) {
+                                            const FourTokens &early, RuleSpace<SLICE> &x) {
     const int tid = threadIdx.x;
     const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < SLICE / 4 / THREADS; ++i)
-        reinterpret_cast<uint4 *>(word)[i * THREADS + tid] = none;
-    for (int i = tid; i < SLICE / 32; i += THREADS) bit[i] = 0;
+        reinterpret_cast<uint4 *>(x.word)[i * THREADS + tid] = none;
+    for (int i = tid; i < SLICE / 32; i += THREADS) x.seen[i] = x.listed[i] = 0;
+    // entries two loads ahead of those that are counted
+    constexpr int STEP = 4 * THREADS, DEEP = 2;
+    const int32_t *history = u.history + row * u.history_stride;
+    const int first = wave_entry();
+    FourTokens next[DEEP];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int q = 0; q < DEEP; ++q) next[q] = load4(history, base + q * STEP, r.length);
+    };
+    if (first + STEP < r.length) load(first + STEP);
     __syncthreads();
     if (u.bias_count > 0) {
         const int32_t *ids = u.bias_ids + row * u.bias_stride;
         for (int i = tid; i < (int)u.bias_count; i += THREADS) {
             const unsigned at = (unsigned)ids[i] - (unsigned)lo;
             if (at < (unsigned)size) {
-                atomicMax(&word[slot<SLICE>(at)], (uint32_t)(i + 1) << RULE_BIAS_SHIFT);
-                atomicOr(&bit[at >> 5], 1u << (at & 31u));
+                atomicMax(&x.word[slot<SLICE>(at)], (uint32_t)(i + 1) << RULE_BIAS_SHIFT);
+                atomicOr(&x.listed[at >> 5], 1u << (at & 31u));
             }
         }
         __syncthreads();
     }
-    auto count = [&](int i, const FourTokens &f) {
+    // a token of the prompt is counted 0 times
+    auto count = [&](int base, const FourTokens &f) {
+        const int i = base + 4 * (tid & 63);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const unsigned at = (unsigned)f.v[c] - (unsigned)lo;
-            if (i + c < r.length && at < (unsigned)size) {
-                uint32_t *w = &word[slot<SLICE>(at)];
-                if (i + c < r.prompt) atomicOr(w, RULE_SEEN);
-                else atomicAdd(w, 1u);
-                atomicOr(&bit[at >> 5], 1u << (at & 31u));
+            if (at < (unsigned)size) {
+                atomicAdd(&x.word[slot<SLICE>(at)], i >= r.prompt - c ? 1u : 0u);
+                atomicOr(&x.seen[at >> 5], 1u << (at & 31u));
             }
         }
     };
-    // the first entries are here already; the others four loads at a time
-    constexpr int STEP = 4 * THREADS, DEEP = 4;
-    count(4 * tid, early);
-    const int32_t *history = u.history + row * u.history_stride;
-    for (int i0 = STEP + 4 * tid; i0 < r.length; i0 += DEEP * STEP) {
-        FourTokens f[DEEP];
+    if (first < r.length) {
+        FourTokens f = early;
+        if (first + 256 > r.length) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (first + 4 * (tid & 63) + c >= r.length) f.v[c] = -1;
+        }
+        count(first, f);
+    }
+    for (int base = first + STEP; base < r.length; base += DEEP * STEP) {
+        FourTokens now[DEEP];
+#pragma unroll
+        for (int q = 0; q < DEEP; ++q) now[q] = next[q];
+        if (base + DEEP * STEP < r.length) load(base + DEEP * STEP);
 #pragma unroll
         for (int q = 0; q < DEEP; ++q)
-            f[q] = load4(history, i0 + q * STEP, (int)u.history_capacity);
-#pragma unroll
-        for (int q = 0; q < DEEP; ++q) count(i0 + q * STEP, f[q]);
+            if (base + q * STEP < r.length) count(base + q * STEP, now[q]);
     }
     __syncthreads();
 }
@@ -205,8 +232,9 @@ struct Raw {
 template <typename T, int THREADS, int VALUES>
 __device__ __forceinline__ void adjusted(const nms_logit_rules &u, const RowRules &r, int64_t row,
                                          const T *in, const Raw<T, THREADS, VALUES> &raw,
-                                         uint32_t *word, const uint32_t *bit, float *z) {
+                                         RuleSpace<THREADS * VALUES> &x, float *z) {
     constexpr int SLICE = THREADS * VALUES;
+    uint32_t *word = x.word;
     const int tid = threadIdx.x;
 #pragma unroll
     for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw.logits[j / 8].v[j % 8]);
@@ -217,18 +245,22 @@ __device__ __forceinline__ void adjusted(const nms_logit_rules &u, const RowRule
     };
     auto bit_of = [](uint32_t bits, int j) { return (int)(bits << (31 - j)) >> 31; };
     if (r.words) {
-        uint32_t touched = 0;
+        uint32_t seen = 0, listed = 0;
 #pragma unroll
-        for (int g = 0; g < VALUES / 8; ++g)
-            touched |= (uint32_t)reinterpret_cast<const uint8_t *>(bit)[g * THREADS + tid]
-                       << (8 * g);
+        for (int g = 0; g < VALUES / 8; ++g) {
+            const int at = g * THREADS + tid;
+            seen |= (uint32_t)reinterpret_cast<const uint8_t *>(x.seen)[at] << (8 * g);
+            listed |= (uint32_t)reinterpret_cast<const uint8_t *>(x.listed)[at] << (8 * g);
+        }
+        const uint32_t touched = seen | listed;
         if (touched != 0u) {
             uint32_t left = touched;
             do {
                 const int j = __builtin_ctz(left), at = token_at<THREADS>(j);
                 left &= left - 1u;
-                uint32_t *x = word + slot<SLICE>((unsigned)at);
-                *x = __float_as_uint(replaced(u, r, row, to_f32(in[at]), *x));
+                uint32_t *w = word + slot<SLICE>((unsigned)at);
+                *w = __float_as_uint(
+                    replaced(u, r, row, to_f32(in[at]), (seen >> j & 1u) != 0u, *w));
             } while (left != 0u);
 #pragma unroll
             for (int q = 0; q < VALUES / 4; ++q) {

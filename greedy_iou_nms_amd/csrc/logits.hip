@@ -14,20 +14,20 @@ namespace {
 template <typename T, int THREADS, int VALUES>
 __global__ __launch_bounds__(THREADS, 8) void adjust_kernel(AdjustArgs a) {
     constexpr int SLICE = THREADS * VALUES;
-    __shared__ uint32_t word[SLICE], bit[SLICE / 32];
+    __shared__ RuleSpace<SLICE> rules;
     const int64_t row = blockIdx.x;
     const int lo = (int)blockIdx.y * SLICE;
     const int size = min(SLICE, a.vocab - lo);
     // a thread's first entries, before it knows how many are in use
     const FourTokens early = load4(a.rules.history + row * a.rules.history_stride,
-                                   4 * (int)threadIdx.x, (int)a.rules.history_capacity);
+                                   wave_entry(), (int)a.rules.history_capacity);
     const RowRules r = row_rules(a.rules, row, readable(a.logits));
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + lo;
     const Raw<T, THREADS, VALUES> raw(r, lo, size, in);
-    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word, bit);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, rules);
     float z[VALUES];
-    adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, word, bit, z);
+    adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, rules, z);
 #pragma unroll
     for (int g = 0; g < VALUES / 8; ++g) {
         const int at = token_at<THREADS>(8 * g);

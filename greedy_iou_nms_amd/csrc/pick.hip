@@ -132,8 +132,7 @@ __device__ __forceinline__ void digit_of_rank(const uint32_t *hist, uint32_t lef
 // 4.8 where little else runs).
 template <int THREADS, int VALUES>
 struct SliceSpace {  // in LDS
-    uint32_t word[THREADS * VALUES];  // the rules, then the values
-    uint32_t bit[THREADS * VALUES / 32];
+    RuleSpace<THREADS * VALUES> rules;  // their words then hold the values
     uint32_t hist[BINS];
     float wave_top[THREADS / 64], wave_sums[THREADS / 64];
     float bound[EDGES];
@@ -153,7 +152,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
                                       SliceSpace<THREADS, VALUES> &x) {
     constexpr int SLICE = THREADS * VALUES;
     constexpr int WAVES = THREADS / 64;
-    uint32_t *word = x.word, *bit = x.bit, *hist = x.hist;
+    uint32_t *word = x.rules.word, *hist = x.hist;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     static_assert(WAVES >= EDGES, "a wave for each bound");
     const int64_t row = blockIdx.x;
@@ -162,7 +161,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     const int size = min(SLICE, a.vocab - lo);
     // a thread's first entries, before it knows how many are in use
     const FourTokens early = load4(a.rules.history + row * a.rules.history_stride,
-                                   4 * (int)threadIdx.x, (int)a.rules.history_capacity);
+                                   wave_entry(), (int)a.rules.history_capacity);
     const RowRules r = row_rules(a.rules, row, a.uniform);
     const float warm = warmth(parameter(a.temperature, row, 1.0f, a.uniform));
     const float c = fminf(1.4426950408889634f / warm, 3.0e38f);
@@ -175,10 +174,10 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
         x.highest = ordered(NEG_INF);
         x.lowest = ordered(__builtin_inff());
     }
-    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, word, bit);
+    if (r.words) slice_rules<THREADS, SLICE>(a.rules, r, row, lo, size, early, x.rules);
     else __syncthreads();
     float z[VALUES];
-    adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, word, bit, z);
+    adjusted<T, THREADS, VALUES>(a.rules, r, row, in, raw, x.rules, z);
     // The groups' largest values and the wave's, and the softmax sum relative
     // to that: exp2(z c - top c), one multiply-add and one exponential a value,
     // where the rounding of top c is a factor of all terms and is taken out of
