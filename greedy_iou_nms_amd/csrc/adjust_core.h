@@ -89,12 +89,11 @@ __device__ __forceinline__ int wave_entry() {
 }
 
 // Where the word of a slice's token lies: threads read the words of eight
-// neighbouring tokens as two quarters, and a wave's quarters lie side by side
-// (eight neighbouring words per lane would put every other lane on the same
-// LDS banks).
-template <int SLICE>
+// neighbouring tokens as two quarters of four, and every other eight lanes have
+// theirs exchanged (a wave's first quarters, 32 bytes apart, would else lie on
+// half of the LDS banks).
 __device__ __forceinline__ unsigned slot(unsigned at) {
-    return ((at >> 2) & 1u) * (SLICE / 2) + (at >> 3) * 4 + (at & 3u);
+    return at ^ (at >> 4 & 4u);
 }
 
 // The adjusted value of a touched token, but for its mask.  Every operation
@@ -148,7 +147,7 @@ __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowR
         for (int i = tid; i < (int)u.bias_count; i += THREADS) {
             const unsigned at = (unsigned)ids[i] - (unsigned)lo;
             if (at < (unsigned)size) {
-                atomicMax(&x.word[slot<SLICE>(at)], (uint32_t)(i + 1) << RULE_BIAS_SHIFT);
+                atomicMax(&x.word[slot(at)], (uint32_t)(i + 1) << RULE_BIAS_SHIFT);
                 atomicOr(&x.listed[at >> 5], 1u << (at & 31u));
             }
         }
@@ -161,7 +160,7 @@ __device__ __forceinline__ void slice_rules(const nms_logit_rules &u, const RowR
         for (int c = 0; c < 4; ++c) {
             const unsigned at = (unsigned)f.v[c] - (unsigned)lo;
             if (at < (unsigned)size) {
-                atomicAdd(&x.word[slot<SLICE>(at)], i >= r.prompt - c ? 1u : 0u);
+                atomicAdd(&x.word[slot(at)], i >= r.prompt - c ? 1u : 0u);
                 atomicOr(&x.seen[at >> 5], 1u << (at & 31u));
             }
         }
@@ -233,7 +232,6 @@ template <typename T, int THREADS, int VALUES>
 __device__ __forceinline__ void adjusted(const nms_logit_rules &u, const RowRules &r, int64_t row,
                                          const T *in, const Raw<T, THREADS, VALUES> &raw,
                                          RuleSpace<THREADS * VALUES> &x, float *z) {
-    constexpr int SLICE = THREADS * VALUES;
     uint32_t *word = x.word;
     const int tid = threadIdx.x;
 #pragma unroll
@@ -258,14 +256,14 @@ __device__ __forceinline__ void adjusted(const nms_logit_rules &u, const RowRule
             do {
                 const int j = __builtin_ctz(left), at = token_at<THREADS>(j);
                 left &= left - 1u;
-                uint32_t *w = word + slot<SLICE>((unsigned)at);
+                uint32_t *w = word + slot((unsigned)at);
                 *w = __float_as_uint(
                     replaced(u, r, row, to_f32(in[at]), (seen >> j & 1u) != 0u, *w));
             } while (left != 0u);
 #pragma unroll
             for (int q = 0; q < VALUES / 4; ++q) {
                 float w[4];
-                __builtin_memcpy(w, word + slot<SLICE>((unsigned)token_at<THREADS>(4 * q)), 16);
+                __builtin_memcpy(w, word + slot((unsigned)token_at<THREADS>(4 * q)), 16);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     z[4 * q + j] = select(bit_of(touched, 4 * q + j), w[j], z[4 * q + j]);

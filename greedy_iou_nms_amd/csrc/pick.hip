@@ -220,7 +220,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
 #pragma unroll
         for (int q = 0; q < VALUES / 4; ++q)
             // a copy that can be read by a number of its place
-            __builtin_memcpy(word + slot<SLICE>((unsigned)token_at<THREADS>(4 * q)),
+            __builtin_memcpy(word + slot((unsigned)token_at<THREADS>(4 * q)),
                              z + 4 * q, 16);
     }
     int least = ordered(__builtin_inff());
@@ -292,7 +292,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     // the candidate of the thread's j-th token
     auto own = [&](int j) -> uint64_t {
         const int at = token_at<THREADS>(j);
-        return candidate(__uint_as_float(word[slot<SLICE>((unsigned)at)]), lo + at);
+        return candidate(__uint_as_float(word[slot((unsigned)at)]), lo + at);
     };
     while (hits != 0u) {
         const int j = __builtin_ctz(hits);
