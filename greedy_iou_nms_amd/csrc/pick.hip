@@ -44,6 +44,21 @@ __device__ __forceinline__ uint64_t candidate(float z, int token) {
     return k == 0u ? 0ull : ((uint64_t)k << 32) | (uint32_t)~token;
 }
 
+// The same of a value known to be above -infinity.
+__device__ __forceinline__ uint64_t candidate_of(float z, int token) {
+    const int u = __float_as_int(z + 0.0f);
+    return (uint64_t)(uint32_t)(u ^ ((u >> 31) | (int)0x80000000)) << 32 | (uint32_t)~token;
+}
+
+// The largest of four, in two instructions: fmaxf takes two more to quieten its
+// operands.  A NaN may go through.
+__device__ __forceinline__ float max4(float a, float b, float c, float d) {
+    float m;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(a), "v"(b), "v"(c));
+    asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(m), "v"(d));
+    return m;
+}
+
 // The temperature of the softmax: greedy rows (0, or anything not above it)
 // use 1.
 __device__ __forceinline__ float warmth(float t) { return t > 0.0f ? t : 1.0f; }
@@ -194,8 +209,17 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
 #pragma unroll
         for (int g = 0; g < VALUES / GROUP; ++g) {
             m[g] = z[g * GROUP];
+            if (GROUP >= 4) {
 #pragma unroll
-            for (int j = 1; j < GROUP; ++j) m[g] = fmaxf(m[g], z[g * GROUP + j]);
+                for (int j = 0; j < GROUP; j += 4) {
+                    const float *v = z + g * GROUP + j;
+                    const float w = max4(v[0], v[1], v[2], v[3]);
+                    m[g] = j == 0 ? w : fmaxf(m[g], w);
+                }
+            } else {
+#pragma unroll
+                for (int j = 1; j < GROUP; ++j) m[g] = fmaxf(m[g], z[g * GROUP + j]);
+            }
             top = fmaxf(top, m[g]);
         }
         top = wave_max(top);
@@ -286,19 +310,21 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     hits = ~hits & (uint32_t)((1ull << VALUES) - 1);
     const uint32_t mine = (uint32_t)__popc(hits);
     const uint32_t through = wave_scan(mine);
+    const uint32_t wave_hits = last_lane(through);
     uint32_t to = 0;
-    if ((tid & 63) == 63) to = atomicAdd(&x.taken, through);
-    to = last_lane(to) + through - mine;
+    if ((tid & 63) == 0) to = atomicAdd(&x.taken, wave_hits);
+    to = __builtin_amdgcn_readfirstlane(to) + through - mine;
     // the candidate of the thread's j-th token
     auto own = [&](int j) -> uint64_t {
         const int at = token_at<THREADS>(j);
         return candidate(__uint_as_float(word[slot((unsigned)at)]), lo + at);
     };
     while (hits != 0u) {
-        const int j = __builtin_ctz(hits);
+        const int j = __builtin_ctz(hits), at = token_at<THREADS>(j);
         hits &= hits - 1u;
-        if (to < (uint32_t)cap) found[to] = own(j);
-        ++to;
+        // (what is too much goes to the last place: it is found anew below)
+        found[min(to++, (uint32_t)cap - 1u)] =
+            candidate_of(__uint_as_float(word[slot((unsigned)at)]), lo + at);
     }
     if (first == NEG_INF) {
         // the smallest of them, which the join's bins begin at
