@@ -157,9 +157,9 @@ struct SliceSpace {  // in LDS
 };
 
 // Instructions bound it: a wave (1024 tokens) issues 230 for the values, the
-// maximum and the softmax sum, 120 more to find 50 candidates, 240 to find
-// 1000, 155 for a history of 4096, 40 for biases and 25 for a mask.  256 rows
-// of 131072 bfloat16 logits with all of these take 50.5 us, 38 of them issuing,
+// maximum and the softmax sum, 115 more to find 50 candidates, 210 to find
+// 1000, 150 for a history of 4096, 20 for biases and 25 for a mask.  256 rows
+// of 131072 bfloat16 logits with all of these take 47.5 us, 35 of them issuing,
 // where reading the 72 MB takes 14; 64 rows of 100003 float32 logits with 50
 // candidates 12.6 us (reading: 5).
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
@@ -798,7 +798,7 @@ __global__ __launch_bounds__(1024, 4) void whole_kernel(PickArgs a, uint32_t inv
 // (300 rows of 8000 with 50 candidates: 15.9 us, and 17.0 in one of 16384).
 // Slices of 8192 have twice the candidates to join and every slice reads the
 // whole history: 17 rows of 131072 with 1000 candidates take 33 us in them and
-// 23 in slices of 16384, 256 rows 93 and 59; one row with 50 candidates 15.0
+// 23 in slices of 16384, 256 rows 93 and 59 (55 now); one row with 50 candidates 15.0
 // and 14.6.  512 threads with 32 tokens each made 65 us of the 59.
 constexpr int WHOLE_MOST = 32768;
 
