@@ -83,7 +83,7 @@ def _rows(t, name: str, device=None, shape=None, dtype=None) -> int:
     if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
     rows, columns = t.shape
-    if columns > 1 and t.stride(1) != 1:
+    if rows > 0 and columns > 1 and t.stride(1) != 1:
         raise ValueError("%s must have neighbouring elements in a row" % name)
     stride = t.stride(0)
     if rows > 1 and stride < columns:
@@ -276,7 +276,9 @@ class LogitRules:
             c.allowed_stride = _rows(allowed, "allowed", device, None, torch.int64)
             if allowed.shape[1] < (self.vocab + 63) // 64:
                 raise ValueError("allowed must have %d words per mask" % ((self.vocab + 63) // 64))
-            c.allowed, c.allowed_count = allowed.data_ptr(), allowed.shape[0]
+            # an empty table has no address; it is never read, but the
+            # numbers of its masks count
+            c.allowed, c.allowed_count = allowed.data_ptr() or 8, allowed.shape[0]
             c.allowed_rows = _vector(allowed_rows, "allowed_rows", n, torch.int32, device)
         self._tensors = given
         self._struct = c

@@ -554,11 +554,14 @@ nms_status nms_pick_workspace_size(int64_t rows, int64_t vocab, int max_top_k, s
  * nms_pick_tokens -- the next token of every row, from its logits under the
  * rules (which are applied on the way: adjusted logits are not written).
  *   rules        as for nms_adjust_logits, or NULL: none.
- *   uniform      device float[rows]: one number in [0, 1) per row.
- *   temperature  device float[rows] or NULL (1): t; 0 takes the first token.
+ *   uniform      device float[rows]: one number in [0, 1) per row (below: as
+ *                0; above: the last token that stays).
+ *   temperature  device float[rows] or NULL (1): t; 0 or below takes the first
+ *                token.
  *   top_k        device int32[rows] or NULL (max_top_k): clamped into
  *                1..max_top_k.
- *   top_p, min_p device float[rows] or NULL (1 and 0).
+ *   top_p, min_p device float[rows] or NULL (1 and 0).  Where one of these
+ *                four is not a number, the first token is taken.
  *   max_top_k    1 .. NMS_MAX_TOP_K.
  *   ids          device int32[rows]; logprobs: device float[rows].
  *   workspace    device, 256-byte aligned, nms_pick_workspace_size() bytes.

@@ -9,6 +9,7 @@ additions deep by 64 * 2^-24; the mean of y under the softmax is at most
 log V < 16, so the logarithm of the sum is off by at most
 (32 + 4 + 64) 2^-24 < 7e-6; the value itself is rounded once to float32."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -394,6 +395,26 @@ def test_pick_outliers_and_crowds(B, V, k):
     check_pick(torch.from_numpy(z), z, uniform=rng.random(B).astype(np.float32), max_top_k=k)
 
 
+@pytest.mark.parametrize("V,k", [(30, 5), (9000, 40), (70000, 900), (70000, 1)])
+def test_infinite_temperature_draws_evenly(V, k):
+    rng = np.random.default_rng(V)
+    z, zf = make_logits(rng, 4, V, "f16")
+    z[1, ::3] = -math.inf
+    zf = z.float().numpy()
+    check_pick(z, zf, uniform=rng.random(4).astype(np.float32), max_top_k=k,
+               temperature=np.full(4, np.inf, np.float32))
+
+
+def test_a_table_without_masks():
+    rng = np.random.default_rng(17)
+    z, zf = make_logits(rng, 3, 500, "f32")
+    u = dict(allowed=np.zeros((0, 8), np.int64), allowed_rows=np.array([-1, 0, 3], np.int32))
+    want = plain.adjust(zf, **u)
+    assert np.isfinite(want[0]).all() and np.isinf(want[1:]).all()
+    same(lib().adjust_logits(z.to(device()), gpu_rules(500, u)), want)
+    check_pick(z, want, rules=gpu_rules(500, u), **row_parameters(rng, 3, 9))
+
+
 def test_pick_no_rows():
     dev = device()
     ids, lp = lib().pick_tokens(torch.zeros(0, 10, device=dev), torch.zeros(0, device=dev))
@@ -549,6 +570,39 @@ def test_two_streams_at_the_same_time():
     for i in range(2):
         for ids in got[i]:
             np.testing.assert_array_equal(ids.cpu().numpy(), want[i])
+
+
+def test_threads_at_the_same_time():
+    """Each thread has a stream of its own; calls of different sizes."""
+    dev = device()
+    rng = np.random.default_rng(24)
+    work = []
+    for B, V, k in ((3, 40000, 700), (7, 900, 4), (2, 70000, 1), (30, 20000, 60)):
+        z, zf = make_logits(rng, B, V, "f32")
+        u = make_rules(rng, B, V, L=100)
+        kw = row_parameters(rng, B, k)
+        want, _ = plain.pick(plain.adjust(zf, **u), kw["uniform"], k, kw["temperature"],
+                             kw["top_k"], kw["top_p"], kw["min_p"])
+        on = {n: to_gpu(v) if isinstance(v, np.ndarray) else v for n, v in kw.items()}
+        work.append((z.to(dev), gpu_rules(V, u), on, want))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(first):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = []
+            for i in range(20):
+                z, rules, on, want = work[(first + i) % len(work)]
+                got.append((lib().pick_tokens(z, rules=rules, **on)[0], want))
+            torch.cuda.current_stream().synchronize()
+            wrong.extend(first for ids, want in got if not np.array_equal(ids.cpu().numpy(), want))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
 
 
 def test_results_do_not_depend_on_the_run():
