@@ -156,6 +156,108 @@ struct SliceSpace {  // in LDS
     uint32_t taken, chosen[2];
 };
 
+// The candidates of a slice whose bound lets too many through (equal values,
+// masks of the type's lowest value, largest values side by side): of the values
+// in x.rules.word those among which the k largest are, at most cap.  Their keys
+// are between low and high; each round counts all keys of the range in BINS
+// parts and goes on in the part with the k-th, until what lies at or above it
+// fits, or it is a single key, four rounds at most.  Then its first tokens are
+// taken, so many as are missing.  Returns how many it wrote; x.chosen[0] is the
+// smallest one's key.  64 rows of 131072 with 50 candidates take 49 us where
+// all but 40 tokens have the type's lowest value, and 29 where the rows are
+// sorted (16 at random); a radix selection of the 64-bit words took 245 and 91.
+template <int THREADS, int VALUES>
+__device__ __forceinline__ uint32_t narrowed(SliceSpace<THREADS, VALUES> &x, uint32_t low,
+                                             uint32_t high, int k, int cap, int lo,
+                                             uint64_t *found) {
+    constexpr int WAVES = THREADS / 64, PARTS = VALUES / 8;
+    static_assert(PARTS * WAVES <= 64 && BINS == 512, "a lane per total, nine bits per round");
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t *word = x.rules.word;
+    // f(j, key) with the keys of the thread's tokens
+    auto each = [&](auto f) {
+#pragma unroll 1
+        for (int q = 0; q < VALUES / 4; ++q) {
+            float v[4];
+            __builtin_memcpy(v, word + slot((unsigned)token_at<THREADS>(4 * q)), 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) f(4 * q + c, order_key(v[c]));
+        }
+    };
+    uint32_t range = high - low, above = 0;
+    bool single, fits;
+    do {
+        const int shift = max(0, 23 - __clz(range | 1u));
+        for (int i = tid; i < BINS; i += THREADS) x.hist[i] = 0;
+        __syncthreads();
+        each([&](int, uint32_t key) {
+            const uint32_t d = key - low, b = d >> shift;
+            // the lanes that agree with the first one add once for all
+            const uint64_t in = __ballot(d <= range);
+            if (in == 0ull) return;
+            const int leader = __builtin_ctzll(in);
+            const uint32_t its = (uint32_t)__builtin_amdgcn_readlane((int)b, leader);
+            const uint64_t same = __ballot(d <= range && b == its);
+            if (lane == leader) atomicAdd(&x.hist[its], (uint32_t)__popcll(same));
+            else if (d <= range && b != its) atomicAdd(&x.hist[b], 1u);
+        });
+        __syncthreads();
+        if (wave == 0) {
+            const int b = Ranks<BINS / 64>(x.hist).bin((uint32_t)k - above);
+            uint32_t over = 0;
+            for (int i = b + 1 + lane; i < BINS; i += 64) over += x.hist[i];
+            over = wave_sum(over);
+            if (lane == 0) {
+                x.chosen[0] = low + ((uint32_t)b << shift);
+                x.chosen[1] = above + over;
+                x.chosen[2] = x.hist[b];
+                x.taken = 0;  // (read by all before the first barrier here)
+            }
+        }
+        __syncthreads();
+        low = x.chosen[0];
+        above = x.chosen[1];
+        range = (1u << shift) - 1u;
+        single = shift == 0;
+        fits = above + x.chosen[2] <= (uint32_t)cap;
+    } while (!single && !fits);
+    uint32_t equal = 0;  // bit j: the key is low, and not all of them are taken
+    each([&](int j, uint32_t key) {
+        if (key > low || (fits && key == low))
+            found[atomicAdd(&x.taken, 1u)] =
+                (uint64_t)key << 32 | (uint32_t)~(lo + token_at<THREADS>(j));
+        if (!fits && key == low) equal |= 1u << j;
+    });
+    if (!fits) {
+        // their ranks in the order of the tokens: by part, wave, lane and place
+        uint32_t rank[PARTS];
+#pragma unroll
+        for (int g = 0; g < PARTS; ++g) {
+            const uint32_t n = (uint32_t)__popc(equal >> (8 * g) & 255u);
+            const uint32_t through = wave_scan(n);
+            rank[g] = through - n;
+            if (lane == 63) x.hist[g * WAVES + wave] = through;
+        }
+        __syncthreads();
+        const uint32_t total = lane < PARTS * WAVES ? x.hist[lane] : 0u;
+        const uint32_t before = wave_scan(total) - total;
+        const uint32_t missing = (uint32_t)k - above;
+#pragma unroll
+        for (int g = 0; g < PARTS; ++g) {
+            uint32_t r = rank[g] + (uint32_t)__builtin_amdgcn_readlane((int)before,
+                                                                       g * WAVES + wave);
+            for (uint32_t bits = equal >> (8 * g) & 255u; bits != 0u && r < missing;
+                 bits &= bits - 1u, ++r)
+                found[above + r] =
+                    (uint64_t)low << 32 |
+                    (uint32_t)~(lo + token_at<THREADS>(8 * g + __builtin_ctz(bits)));
+        }
+    }
+    __syncthreads();
+    return fits ? x.taken : (uint32_t)k;
+}
+
 // Instructions bound it: a wave (1024 tokens) issues 230 for the values, the
 // maximum and the softmax sum, 115 more to find 50 candidates, 210 to find
 // 1000, 150 for a history of 4096, 20 for biases and 25 for a mask.  256 rows
@@ -273,13 +375,16 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
         if (tid == 0) parts[part] = Part{top, count, all, {e0, e1, e2, e3}, least_found, 0.0f};
     };
     if (FIRST) {
-        uint64_t best = 0;
-        if (top > NEG_INF) {
+        int mine = 0x7fffffff;
 #pragma unroll
-            for (int j = VALUES - 1; j >= 0; --j)
-                if (z[j] == top) best = candidate(z[j], lo + token_at<THREADS>(j));
+        for (int j = VALUES - 1; j >= 0; --j)
+            if (z[j] == top) mine = lo + token_at<THREADS>(j);
+        // one lane for its wave: many may have it
+        if (top > NEG_INF && __ballot(mine != 0x7fffffff) != 0ull) {
+            mine = wave_min(mine);
+            if ((tid & 63) == 0)
+                atomicMax(&x.greatest, (unsigned long long)candidate_of(top, mine));
         }
-        if (best != 0) atomicMax(&x.greatest, (unsigned long long)best);
         __syncthreads();
         if (tid == 0) found[0] = x.greatest;
         if (wave == 0) finish(top > NEG_INF ? 1u : 0u, top, top, top, top, top);
@@ -314,11 +419,6 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     uint32_t to = 0;
     if ((tid & 63) == 0) to = atomicAdd(&x.taken, wave_hits);
     to = __builtin_amdgcn_readfirstlane(to) + through - mine;
-    // the candidate of the thread's j-th token
-    auto own = [&](int j) -> uint64_t {
-        const int at = token_at<THREADS>(j);
-        return candidate(__uint_as_float(word[slot((unsigned)at)]), lo + at);
-    };
     while (hits != 0u) {
         const int j = __builtin_ctz(hits), at = token_at<THREADS>(j);
         hits &= hits - 1u;
@@ -337,36 +437,12 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     }
     __syncthreads();
     if (first == NEG_INF) edge = unordered(x.lowest);
-    if (x.taken > (uint32_t)cap) {
-        // Equal values, or a spread that the bins do not resolve: the k-th
-        // largest word, digit by digit from the top, and exactly k of them.
-        uint64_t prefix = 0, mask = 0;
-        uint32_t left = (uint32_t)k;
-        for (int shift = 56; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += THREADS) hist[i] = 0;
-            __syncthreads();
-#pragma unroll 1
-            for (int j = 0; j < VALUES; ++j) {
-                const uint64_t w = own(j);
-                if (w != 0 && (w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
-            }
-            __syncthreads();
-            if (wave == 0) digit_of_rank(hist, left, x.chosen);
-            if (tid == 0) x.taken = 0;
-            __syncthreads();
-            prefix |= (uint64_t)x.chosen[0] << shift;
-            mask |= 255ull << shift;
-            left = x.chosen[1];
-        }
-#pragma unroll 1
-        for (int j = 0; j < VALUES; ++j) {
-            const uint64_t w = own(j);
-            if (w >= prefix) found[atomicAdd(&x.taken, 1u)] = w;
-        }
-        edge = key_value((uint32_t)(prefix >> 32));
-        __syncthreads();
+    uint32_t count = x.taken;
+    if (count > (uint32_t)cap) {
+        count = narrowed<THREADS, VALUES>(x, order_key(edge), order_key(top), k, cap, lo, found);
+        edge = key_value(x.chosen[0]);
     }
-    if (wave == 0) finish(x.taken, first, x.bound[1], x.bound[2], x.bound[3], edge);
+    if (wave == 0) finish(count, first, x.bound[1], x.bound[2], x.bound[3], edge);
 }
 
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>

@@ -348,6 +348,33 @@ def test_pick_strided_and_offset_rows():
         check_pick(one, zf[1:2], **row_parameters(rng, 1, 20))
 
 
+@pytest.mark.parametrize("V", [700, 9000, 30000, 70000])
+@pytest.mark.parametrize("k", [1, 2, 50, 1000])
+def test_pick_crowded_rows(V, k):
+    """More equal or neighbouring values at the bound than there is room for."""
+    rng = np.random.default_rng([V, k])
+    z = rng.normal(size=(12, V)).astype(np.float32)
+    low = np.finfo(np.float32).min
+    z[0] = 0.0
+    z[1] = low
+    z[2, 40:] = low
+    z[3, :V - 40] = low
+    z[4] = np.round(z[4] * 2) / 2
+    z[5] = -np.sort(-z[5])
+    z[6] = np.sort(z[6])
+    z[7] = np.where(rng.random(V) < 0.5, 0.0, -0.0)
+    z[8] = np.float32(2.0) ** rng.integers(-140, 120, size=V).astype(np.float32)
+    z[9] = np.inf
+    z[9, ::2] = -np.inf
+    z[10] = 1.0 + np.float32(2.0 ** -23) * rng.integers(0, 3, size=V).astype(np.float32)
+    z[11, ::5] = z[11].max()
+    check_pick(torch.from_numpy(z), z, uniform=rng.random(12).astype(np.float32), max_top_k=k,
+               temperature=np.full(12, 2.0, np.float32))
+    u = rng.random(12).astype(np.float32)
+    check_pick(torch.from_numpy(z).half(), torch.from_numpy(z).half().float().numpy(), uniform=u,
+               max_top_k=k)
+
+
 def test_rows_more_than_2_to_31_elements_apart():
     rng = np.random.default_rng(16)
     stride, V = 2 ** 31 + 40, 33000
