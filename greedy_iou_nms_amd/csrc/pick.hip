@@ -123,6 +123,19 @@ struct Ranks {
     }
 };
 
+// One more in hist[bin] for every lane that is in.  The lanes that agree with
+// the first one add once for all: equal values would else queue for a bin.
+// Called by whole waves.
+__device__ __forceinline__ void count_bin(uint32_t *hist, bool in, uint32_t bin) {
+    const uint64_t all = __ballot(in);
+    if (all == 0ull) return;
+    const int leader = __builtin_ctzll(all);
+    const uint32_t its = (uint32_t)__builtin_amdgcn_readlane((int)bin, leader);
+    const uint64_t same = __ballot(in && bin == its);
+    if ((int)(threadIdx.x & 63) == leader) atomicAdd(&hist[its], (uint32_t)__popcll(same));
+    else if (in && bin != its) atomicAdd(&hist[bin], 1u);
+}
+
 // One digit of a k-th largest word: chosen[0] is the digit of the word that
 // is `left`-th largest among those counted in hist[0..256), chosen[1] its rank
 // among those with this digit.  One wave.
@@ -192,15 +205,8 @@ __device__ __forceinline__ uint32_t narrowed(SliceSpace<THREADS, VALUES> &x, uin
         for (int i = tid; i < BINS; i += THREADS) x.hist[i] = 0;
         __syncthreads();
         each([&](int, uint32_t key) {
-            const uint32_t d = key - low, b = d >> shift;
-            // the lanes that agree with the first one add once for all
-            const uint64_t in = __ballot(d <= range);
-            if (in == 0ull) return;
-            const int leader = __builtin_ctzll(in);
-            const uint32_t its = (uint32_t)__builtin_amdgcn_readlane((int)b, leader);
-            const uint64_t same = __ballot(d <= range && b == its);
-            if (lane == leader) atomicAdd(&x.hist[its], (uint32_t)__popcll(same));
-            else if (d <= range && b != its) atomicAdd(&x.hist[b], 1u);
+            const uint32_t d = key - low;
+            count_bin(x.hist, d <= range, d >> shift);
         });
         __syncthreads();
         if (wave == 0) {
@@ -406,7 +412,8 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     // are candidates
     const float first = x.bound[0];
     float edge = fminf(fmaxf(first, -3.402823466e38f), 3.402823466e38f);
-    if (edge == 0.0f) edge = -1.0e-38f;  // so that -0 is not below it
+    constexpr float ZERO_EDGE = -1.0e-38f;
+    if (edge == 0.0f) edge = ZERO_EDGE;  // so that -0 is not below it
     // bit j: z[j] >= edge, the sign of a difference that is no NaN
     uint32_t hits = 0;
 #pragma unroll
@@ -418,11 +425,13 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     const uint32_t wave_hits = last_lane(through);
     uint32_t to = 0;
     if ((tid & 63) == 0) to = atomicAdd(&x.taken, wave_hits);
-    to = __builtin_amdgcn_readfirstlane(to) + through - mine;
+    to = __builtin_amdgcn_readfirstlane(to);
+    if (to >= (uint32_t)cap) hits = 0;  // too many: they are found anew below
+    to += through - mine;
     while (hits != 0u) {
         const int j = __builtin_ctz(hits), at = token_at<THREADS>(j);
         hits &= hits - 1u;
-        // (what is too much goes to the last place: it is found anew below)
+        // (what the last wave has too many goes to the last place)
         found[min(to++, (uint32_t)cap - 1u)] =
             candidate_of(__uint_as_float(word[slot((unsigned)at)]), lo + at);
     }
@@ -439,7 +448,8 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     if (first == NEG_INF) edge = unordered(x.lowest);
     uint32_t count = x.taken;
     if (count > (uint32_t)cap) {
-        count = narrowed<THREADS, VALUES>(x, order_key(edge), order_key(top), k, cap, lo, found);
+        count = narrowed<THREADS, VALUES>(x, order_key(edge == ZERO_EDGE ? 0.0f : edge),
+                                          order_key(top), k, cap, lo, found);
         edge = key_value(x.chosen[0]);
     }
     if (wave == 0) finish(count, first, x.bound[1], x.bound[2], x.bound[3], edge);
@@ -710,7 +720,7 @@ __device__ __forceinline__ void join(const PickArgs &a, int64_t row, int slices,
                 if (tid < 256) hist[tid] = 0;
                 __syncthreads();
                 each([&](uint64_t w) {
-                    if (w != 0 && (w & mask) == prefix) atomicAdd(&hist[(w >> shift) & 255], 1u);
+                    count_bin(hist, w != 0 && (w & mask) == prefix, (uint32_t)(w >> shift) & 255u);
                 });
                 __syncthreads();
                 if (wave == 0) digit_of_rank(hist, left, x.chosen);
