@@ -109,26 +109,33 @@ def _vector(t, name: str, n: int, dtype, device) -> Optional[int]:
     raise ValueError("%s must be contiguous" % name)
 
 
-def _int32(v, name: str) -> None:
-    """ctypes would cut what does not fit a C int."""
-    if not -2 ** 31 <= operator.index(v) < 2 ** 31:
+def _whole(v, name: str, bits: int = 32) -> int:
+    """A plain integer; ctypes would cut what its C type does not hold."""
+    v = operator.index(v)
+    if not -1 << (bits - 1) <= v < 1 << (bits - 1):
         raise ValueError("%s is out of range (got %d)" % (name, v))
+    return v
 
 
 # ------------------------------------------------------------------- routing
 
-@functools.lru_cache(maxsize=256)
 def _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_top):
+    """The options' address.  They are remembered by plain numbers: a tensor
+    would be remembered by its identity, whatever it holds by the next call,
+    and 4.0 be taken for a 4 of an earlier one."""
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
-    _int32(top_k, "top_k")
-    _int32(groups, "groups")
-    _int32(group_top, "group_top")
-    if kept_groups is not None:
-        _int32(kept_groups, "kept_groups")
-    return ctypes.byref(_RouteOptions(
-        _SCORES[score], int(top_k), int(bool(renormalise)), float(scale), int(groups),
-        int(groups if kept_groups is None else kept_groups), int(group_top)))
+    groups = _whole(groups, "groups")
+    return _plain_options(
+        _SCORES[score], _whole(top_k, "top_k"), bool(renormalise), float(scale), groups,
+        groups if kept_groups is None else _whole(kept_groups, "kept_groups"),
+        _whole(group_top, "group_top"))
+
+
+@functools.lru_cache(maxsize=256)
+def _plain_options(score, top_k, renormalise, scale, groups, kept_groups, group_top):
+    return ctypes.byref(_RouteOptions(score, top_k, int(renormalise), scale, groups, kept_groups,
+                                      group_top))
 
 
 def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
@@ -147,6 +154,7 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     is left for holds id -1 and weight 0."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
+    top_k = _whole(top_k, "top_k")  # of the options and of the outputs
     if device.index != _current_device():
         with torch.cuda.device(device):
             return route_experts(logits, top_k, score, bias, groups, kept_groups, group_top,
@@ -323,10 +331,15 @@ def adjust_logits(logits: torch.Tensor, rules: LogitRules,
     return out
 
 
-@functools.lru_cache(maxsize=256)
 def pick_workspace_size(rows: int, vocab: int, max_top_k: int) -> int:
     """The bytes of workspace that ``pick_tokens`` takes."""
-    _int32(max_top_k, "max_top_k")
+    return _pick_workspace_size(_whole(rows, "rows", 64), _whole(vocab, "vocab", 64),
+                                _whole(max_top_k, "max_top_k"))
+
+
+@functools.lru_cache(maxsize=256)
+def _pick_workspace_size(rows: int, vocab: int, max_top_k: int) -> int:
+    # a function of the sizes alone, so it can be remembered
     out = ctypes.c_size_t(0)
     _check(_lib.nms_pick_workspace_size(rows, vocab, max_top_k, ctypes.byref(out)))
     return int(out.value)
@@ -359,7 +372,8 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
         with torch.cuda.device(device):
             return pick_tokens(logits, uniform, max_top_k, temperature, top_k, top_p, min_p,
                                rules)
-    nbytes = pick_workspace_size(rows, vocab, max_top_k)
+    max_top_k = _whole(max_top_k, "max_top_k")
+    nbytes = _pick_workspace_size(rows, vocab, max_top_k)
     # kept per thread and stream; a captured call takes one of its own from
     # the graph's memory, so that no two graphs share it
     stream = _raw_stream(device)

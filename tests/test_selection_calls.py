@@ -1,0 +1,117 @@
+"""What the binding of the selection operators hands to the library, without a
+GPU: the library's entry points are replaced by ones that note their arguments,
+and the tensors only claim to be on a GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import greedy_iou_nms_amd as g
+from greedy_iou_nms_amd import selection as sel
+
+
+class Claimed(torch.Tensor):
+    is_cuda = True
+
+
+def on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(Claimed)
+
+
+class Library:
+    """Notes the arguments of each call; the options as they are at the call."""
+
+    def __init__(self):
+        self.calls = []
+
+    def _note(self, name, args):
+        self.calls.append((name, args))
+        return 0
+
+    def nms_route_experts(self, *args):
+        o = ctypes.cast(args[7], ctypes.POINTER(sel._RouteOptions)).contents
+        return self._note("route", dict(top_k=o.top_k, scale=o.scale, groups=o.groups,
+                                        kept_groups=o.kept_groups, renormalise=o.renormalise))
+
+    def nms_route_experts_backward(self, *args):
+        o = ctypes.cast(args[7], ctypes.POINTER(sel._RouteOptions)).contents
+        return self._note("back", dict(top_k=o.top_k, scale=o.scale, renormalise=o.renormalise))
+
+    def nms_pick_workspace_size(self, rows, vocab, k, out):
+        ctypes.cast(out, ctypes.POINTER(ctypes.c_size_t)).contents.value = 8 * rows * k
+        return self._note("size", (rows, vocab, k))
+
+    def nms_pick_tokens(self, *args):
+        return self._note("pick", args)
+
+    def nms_adjust_logits(self, *args):
+        return self._note("adjust", args)
+
+    def last(self):
+        return self.calls[-1][1]
+
+
+@pytest.fixture
+def library(monkeypatch):
+    fake = Library()
+    monkeypatch.setattr(sel, "_lib", fake)
+    monkeypatch.setattr(sel, "_current_device", lambda: None)  # a CPU device's index
+    monkeypatch.setattr(sel, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(sel, "_capturing", lambda: False)
+    sel._pick_workspace_size.cache_clear()
+    yield fake
+    sel._pick_workspace_size.cache_clear()  # the sizes here are made up
+
+
+# ------------------------------------------------- numbers, not their holders
+
+def test_options_are_read_at_every_call(library):
+    """A tensor's value may change between two calls with the same tensor."""
+    z = on_gpu(4, 8)
+    scale, k = torch.tensor(2.5), torch.tensor(3)
+    for value, count in ((2.5, 3), (4.0, 5), (1.0, 2)):
+        scale.fill_(value)
+        k.fill_(count)
+        ids, w = g.route_experts(z, k, scale=scale)
+        assert library.last()["scale"] == value and library.last()["top_k"] == count
+        assert ids.shape == (4, count) and w.shape == (4, count)
+        g.route_experts_backward(z, on_gpu(4, 2, dtype=torch.int32), on_gpu(4, 2), scale=scale)
+        assert library.last()["scale"] == value and library.last()["top_k"] == 2
+    keep = torch.tensor(True)
+    for value in (True, False):
+        keep.fill_(value)
+        g.route_experts(z, 2, renormalise=keep)
+        assert library.last()["renormalise"] == int(value)
+
+
+def test_whole_numbers_of_other_types(library):
+    z = on_gpu(4, 8)
+    g.route_experts(z, np.int64(3), groups=np.int32(2), kept_groups=np.int8(1))
+    assert [library.last()[n] for n in ("top_k", "groups", "kept_groups")] == [3, 2, 1]
+
+
+@pytest.mark.parametrize("name", ["top_k", "groups", "kept_groups", "group_top"])
+def test_a_wrong_type_is_refused_after_a_right_one(library, name):
+    """4.0 is no whole number, whatever was called before."""
+    z = on_gpu(4, 8)
+    kw = dict(top_k=2, groups=2, kept_groups=2, group_top=2)
+    g.route_experts(z, **kw)
+    with pytest.raises(TypeError):
+        g.route_experts(z, **{**kw, name: 2.0})
+
+
+def test_pick_sizes_are_read_at_every_call(library):
+    k = torch.tensor(5)
+    z, u = on_gpu(3, 100), on_gpu(3)
+    for count in (5, 9):
+        k.fill_(count)
+        assert g.pick_workspace_size(3, 100, k) == 8 * 3 * count
+        g.pick_tokens(z, u, max_top_k=k)
+        assert library.last()[11] == count and library.last()[15] >= 8 * 3 * count
+    for bad in ((3.0, 100, 5), (3, 100.0, 5), (3, 100, 5.0)):
+        with pytest.raises(TypeError):
+            g.pick_workspace_size(*bad)
+    for bad in ((2 ** 64 + 3, 100, 5), (3, 2 ** 64 + 100, 5), (3, 100, 2 ** 32 + 5)):
+        with pytest.raises(ValueError):
+            g.pick_workspace_size(*bad)
