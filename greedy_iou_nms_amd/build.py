@@ -35,6 +35,9 @@ FLAGS = [
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function", "-I" + INCLUDE,
+    # a constant index past the end of an array is an error, in the last array
+    # of a struct too (which C lets stand for one of any length)
+    "-fstrict-flex-arrays=3", "-Werror=array-bounds",
 ]
 
 # Kernels whose resource report is checked, by a substring of their mangled

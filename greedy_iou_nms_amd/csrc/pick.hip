@@ -172,7 +172,7 @@ struct SliceSpace {  // in LDS
     float bound[EDGES];
     unsigned long long greatest;
     int highest, lowest;  // as ordered()
-    uint32_t taken, chosen[2];
+    uint32_t taken, chosen[3];
 };
 
 // The candidates of a slice whose bound lets too many through (equal values,
