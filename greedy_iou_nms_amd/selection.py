@@ -223,8 +223,11 @@ class LogitRules:
     for tokens of the history, biases and masks of allowed tokens.
 
     A serving loop makes one and keeps it while the contents of its tensors
-    change from step to step; it holds on to the tensors.  All tensors are on
-    one device, with one row (or entry) per row of logits:
+    change from step to step; it holds on to the tensors and their memory.  A
+    matrix that has another shape by the next call, or a tensor with other
+    memory (``resize_``, ``set_``, ``.data``), is checked anew and read where it
+    is then; a captured graph goes on reading what it was captured with.  All
+    tensors are on one device, with one row (or entry) per row of logits:
 
     ``history`` (rows, capacity) int32, the prompt and then what was
     generated; ``history_len`` and ``prompt_len`` (rows,) int32;
@@ -238,21 +241,31 @@ class LogitRules:
                  repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None,
                  allowed=None, allowed_rows=None):
         self.vocab = int(vocab)
+        self._given = (history, history_len, prompt_len, repetition, presence, frequency,
+                       bias_ids, bias_values, allowed, allowed_rows)
+        self._lay_out()
+
+    def _lay_out(self) -> None:
+        """Checks the tensors and takes down where they are."""
+        (history, history_len, prompt_len, repetition, presence, frequency, bias_ids, bias_values,
+         allowed, allowed_rows) = self._given
         per_row = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids,
                    bias_values, allowed_rows)
         if allowed is not None and allowed_rows is None:
             per_row += (allowed,)
-        given = [t for t in per_row + (allowed,) if t is not None]
+        given = [t for t in self._given if t is not None]
         if not all(isinstance(t, torch.Tensor) and t.dim() > 0 for t in given):
             raise TypeError("the rules must be torch tensors with a dimension")
-        self.device = given[0].device if given else None
+        # before anything is read of them
+        matrices = [t for t in (history, bias_ids, bias_values, allowed) if t is not None]
+        at = self._places(given, matrices)
+        device = given[0].device if given else None
         if given and not given[0].is_cuda:
             raise ValueError("the rules must be on a GPU device")
         rows = {t.shape[0] for t in per_row if t is not None}
         if len(rows) > 1:
             raise ValueError("the rules have different numbers of rows: %s" % sorted(rows))
-        self.rows = rows.pop() if rows else None
-        n, device = self.rows, self.device
+        n = rows.pop() if rows else None
         if (history is None) != (history_len is None):
             raise ValueError("history and history_len go together")
         if prompt_len is not None and history is None:
@@ -288,12 +301,25 @@ class LogitRules:
             # numbers of its masks count
             c.allowed, c.allowed_count = allowed.data_ptr() or 8, allowed.shape[0]
             c.allowed_rows = _vector(allowed_rows, "allowed_rows", n, torch.int32, device)
-        self._tensors = given
+        self.device, self.rows = device, n
         self._struct = c
         self._ref = ctypes.byref(c)
+        # aliases hold the memory that the addresses are of
+        self._memory = [t.detach() for t in given]
+        self._tensors, self._matrices, self._at = given, matrices, at
+
+    @staticmethod
+    def _places(tensors, matrices) -> list:
+        """What tells whether the tensors are still where they were.  (A vector
+        whose memory is the same needs no more: it is read for as many rows as
+        it had.)"""
+        return (list(map(torch.Tensor.data_ptr, tensors)) +
+                [(t.shape, t.stride()) for t in matrices])
 
     def _for(self, rows: int, vocab: int, device) -> object:
         """The struct's address, for logits of this shape."""
+        if self._places(self._tensors, self._matrices) != self._at:
+            self._lay_out()
         if self.vocab != vocab:
             raise ValueError("the rules are for %d tokens, the logits have %d" % (self.vocab, vocab))
         if self.rows is not None and self.rows != rows:

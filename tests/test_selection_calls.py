@@ -115,3 +115,88 @@ def test_pick_sizes_are_read_at_every_call(library):
     for bad in ((2 ** 64 + 3, 100, 5), (3, 2 ** 64 + 100, 5), (3, 100, 2 ** 32 + 5)):
         with pytest.raises(ValueError):
             g.pick_workspace_size(*bad)
+
+
+# --------------------------------------------------------- where the rules are
+
+def rules_of(library):
+    """The struct that the last adjust call was given."""
+    return library.last()[5]._obj
+
+
+def test_rules_follow_a_history_that_grows(library):
+    z = on_gpu(2, 100)
+    history = on_gpu(2, 8, dtype=torch.int32)
+    rules = g.LogitRules(100, history=history, history_len=on_gpu(2, dtype=torch.int32))
+    g.adjust_logits(z, rules)
+    before = history.data_ptr()
+    assert rules_of(library).history == before and rules_of(library).history_capacity == 8
+    history.resize_(2, 5000)
+    assert history.data_ptr() != before
+    g.adjust_logits(z, rules)
+    assert rules_of(library).history == history.data_ptr()
+    assert rules_of(library).history_capacity == rules_of(library).history_stride == 5000
+    g.pick_tokens(z, on_gpu(2), rules=rules)
+    assert library.last()[5]._obj.history == history.data_ptr()
+
+
+def test_rules_follow_other_memory_and_other_shapes(library):
+    z = on_gpu(2, 100)
+    wide = on_gpu(2, 40, dtype=torch.int32)
+    history, length = on_gpu(2, 8, dtype=torch.int32), on_gpu(2, dtype=torch.int32)
+    values, allowed = on_gpu(2), on_gpu(2, 2, dtype=torch.int64)
+    rules = g.LogitRules(100, history=history, history_len=length, repetition=values,
+                         allowed=allowed)
+    history.data = wide[:, 4:20]
+    length.set_(on_gpu(2, dtype=torch.int32))
+    values.data = on_gpu(2) + 1
+    allowed.set_(on_gpu(2, 7, dtype=torch.int64))
+    g.adjust_logits(z, rules)
+    u = rules_of(library)
+    assert (u.history, u.history_stride, u.history_capacity) == (wide.data_ptr() + 16, 40, 16)
+    assert u.history_len == length.data_ptr() and u.repetition == values.data_ptr()
+    assert u.allowed == allowed.data_ptr() and u.allowed_stride == 7
+    # the same address, another shape
+    at = history.data_ptr()
+    history.set_(wide.untyped_storage(), 4, (2, 10), (20, 1))
+    assert history.data_ptr() == at
+    g.adjust_logits(z, rules)
+    u = rules_of(library)
+    assert (u.history, u.history_stride, u.history_capacity) == (at, 20, 10)
+
+
+def test_rules_hold_the_memory_that_they_read(library):
+    """Nothing else may be put where the struct points to."""
+    values = on_gpu(3)
+    rules = g.LogitRules(100, repetition=values)
+    held = rules._memory[0].untyped_storage()._cdata
+    assert held == values.untyped_storage()._cdata
+    values.data = on_gpu(3)
+    assert rules._memory[0].untyped_storage()._cdata == held
+    assert rules._memory[0].data_ptr() == rules._struct.repetition != values.data_ptr()
+
+
+def test_rules_that_no_longer_fit_are_refused(library):
+    z = on_gpu(2, 100)
+
+    def make():
+        t = dict(history=on_gpu(2, 8, dtype=torch.int32),
+                 history_len=on_gpu(2, dtype=torch.int32), repetition=on_gpu(2),
+                 allowed=on_gpu(2, 2, dtype=torch.int64))
+        return t, g.LogitRules(100, **t)
+
+    for name, other, error in (("history", on_gpu(3, 8, dtype=torch.int32), ValueError),
+                               ("repetition", on_gpu(3), ValueError),
+                               ("allowed", on_gpu(2, 1, dtype=torch.int64), ValueError),
+                               ("history", on_gpu(2, 16, dtype=torch.int32)[:, ::2],
+                                ValueError)):
+        t, rules = make()
+        g.adjust_logits(z, rules)
+        calls = len(library.calls)
+        t[name].set_(other)
+        for call in (lambda: g.adjust_logits(z, rules),
+                     lambda: g.pick_tokens(z, on_gpu(2), rules=rules)):
+            for _ in range(2):
+                with pytest.raises(error):
+                    call()
+        assert len(library.calls) == calls
