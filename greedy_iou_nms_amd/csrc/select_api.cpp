@@ -36,7 +36,7 @@ nms_status check_route(nms_dtype dtype, int64_t tokens, int64_t experts,
     return NMS_OK;
 }
 
-nms_status check_rules(const nms_logit_rules &u, int64_t vocab) {
+nms_status check_rules(const nms_logit_rules &u, int64_t rows, int64_t vocab) {
     if (u.history != nullptr) {
         if (u.history_len == nullptr || u.history_capacity < 0 ||
             u.history_stride < u.history_capacity)
@@ -45,8 +45,9 @@ nms_status check_rules(const nms_logit_rules &u, int64_t vocab) {
     } else if (u.history_len != nullptr || u.prompt_len != nullptr) {
         return NMS_INVALID_ARG;
     }
-    if (u.bias_count < 0 || (u.bias_count > 0 && (!u.bias_ids || !u.bias_values ||
-                                                  u.bias_stride < u.bias_count)))
+    // (the entries of an empty batch have no address)
+    if (u.bias_count < 0 || (u.bias_count > 0 && u.bias_stride < u.bias_count) ||
+        (u.bias_count > 0 && rows > 0 && (!u.bias_ids || !u.bias_values)))
         return NMS_INVALID_ARG;
     if (u.bias_count > NMS_MAX_BIASES) return NMS_TOO_LARGE;
     if (u.allowed != nullptr) {
@@ -120,7 +121,7 @@ nms_status nms_adjust_logits(const void *logits, nms_dtype dtype, int64_t rows, 
     nms_status st = check_logits(dtype, rows, vocab);
     if (st != NMS_OK) return st;
     if (rules == nullptr) return NMS_INVALID_ARG;
-    st = check_rules(*rules, vocab);
+    st = check_rules(*rules, rows, vocab);
     if (st != NMS_OK) return st;
     if (rows == 0) return NMS_OK;
     st = check_matrix(logits, dtype, rows, vocab, row_stride);
@@ -150,7 +151,7 @@ nms_status nms_pick_tokens(const void *logits, nms_dtype dtype, int64_t rows, in
     if (st != NMS_OK) return st;
     if (max_top_k < 1 || max_top_k > NMS_MAX_TOP_K) return NMS_INVALID_ARG;
     if (rules != nullptr) {
-        st = check_rules(*rules, vocab);
+        st = check_rules(*rules, rows, vocab);
         if (st != NMS_OK) return st;
     }
     if (rows == 0) return NMS_OK;

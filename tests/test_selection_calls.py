@@ -200,3 +200,26 @@ def test_rules_that_no_longer_fit_are_refused(library):
                 with pytest.raises(error):
                     call()
         assert len(library.calls) == calls
+
+
+# ------------------------------------------------------------- an empty batch
+
+def test_an_empty_batch_with_full_rules():
+    """Tensors without rows have no address; the library itself is called."""
+    lib = g._lib
+    t = dict(history=on_gpu(0, 5, dtype=torch.int32), history_len=on_gpu(0, dtype=torch.int32),
+             prompt_len=on_gpu(0, dtype=torch.int32), repetition=on_gpu(0), presence=on_gpu(0),
+             frequency=on_gpu(0), bias_ids=on_gpu(0, 3, dtype=torch.int32),
+             bias_values=on_gpu(0, 3), allowed=on_gpu(0, 2, dtype=torch.int64),
+             allowed_rows=on_gpu(0, dtype=torch.int32))
+    for leave_out in ((), ("allowed_rows",), ("history", "history_len", "prompt_len"),
+                      ("bias_ids", "bias_values")):
+        ref = g.LogitRules(100, **{k: v for k, v in t.items() if k not in leave_out})._ref
+        assert lib.nms_adjust_logits(None, 0, 0, 100, 100, ref, None, 100, None) == 0
+        assert lib.nms_pick_tokens(None, 0, 0, 100, 100, ref, None, None, None, None, None, 5,
+                                   None, None, None, 0, None) == 0
+    # what is wrong whatever the rows are is refused all the same
+    many = g.LogitRules(100, bias_ids=on_gpu(0, 2048, dtype=torch.int32),
+                        bias_values=on_gpu(0, 2048))
+    assert g._STATUS[lib.nms_adjust_logits(None, 0, 0, 100, 100, many._ref, None, 100,
+                                           None)] == "NMS_TOO_LARGE"
