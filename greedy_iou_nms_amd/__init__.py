@@ -179,11 +179,14 @@ class Workspace:
 _tls = threading.local()
 
 
-def _default_workspace(device: torch.device, stream: int) -> Workspace:
+def _default_workspace(device: torch.device, stream: int, use: str = "nms") -> Workspace:
+    """The kept workspace of this thread, per stream and use.  NMS has its own:
+    it tells its words from an earlier call's by 32-bit tags, and words of
+    another use, left there call after call, would pass for them now and then."""
     cache = getattr(_tls, "ws", None)
     if cache is None:
         cache = _tls.ws = {}
-    key = (device.index, stream)
+    key = (device.index, stream, use)
     if key not in cache:
         cache[key] = Workspace(device)
     return cache[key]

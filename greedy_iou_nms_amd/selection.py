@@ -403,7 +403,7 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     # kept per thread and stream; a captured call takes one of its own from
     # the graph's memory, so that no two graphs share it
     stream = _raw_stream(device)
-    kept = Workspace(device) if _capturing() else _default_workspace(device, stream)
+    kept = Workspace(device) if _capturing() else _default_workspace(device, stream, "pick")
     buf = kept.get(nbytes, device)
     ids = torch.empty(rows, dtype=torch.int32, device=device)
     logprobs = torch.empty(rows, dtype=f32, device=device)

@@ -223,3 +223,17 @@ def test_an_empty_batch_with_full_rules():
                         bias_values=on_gpu(0, 2048))
     assert g._STATUS[lib.nms_adjust_logits(None, 0, 0, 100, 100, many._ref, None, 100,
                                            None)] == "NMS_TOO_LARGE"
+
+
+# ------------------------------------------------------------------ workspaces
+
+def test_workspace_of_its_own(library):
+    """NMS tells its own words in its workspace from older ones by a tag of 32
+    bits; what picking leaves behind would be mistaken for them now and then."""
+    nms_buf = g._default_workspace(torch.device("cpu"), 0).get(1 << 16, torch.device("cpu"))
+    g.pick_tokens(on_gpu(3, 100), on_gpu(3))
+    first = library.last()[14]
+    assert not nms_buf.data_ptr() <= first < nms_buf.data_ptr() + nms_buf.numel()
+    g.pick_tokens(on_gpu(2, 100), on_gpu(2))
+    assert library.last()[14] == first                      # kept
+    assert g._default_workspace(torch.device("cpu"), 0).buf is nms_buf
