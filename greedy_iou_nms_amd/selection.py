@@ -24,6 +24,7 @@ _capturing = torch.cuda.is_current_stream_capturing
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # nms_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}  # NMS_ROUTE_SOFTMAX, NMS_ROUTE_SIGMOID
+_MAX_EXPERTS_PER_TOKEN = 64  # NMS_ROUTE_MAX_TOP_K
 
 
 class _RouteOptions(ctypes.Structure):  # nms_route_options
@@ -164,8 +165,8 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     alive = None if live is None else _vector(
         live, "live", tokens, torch.bool if getattr(live, "dtype", None) is torch.bool
         else torch.uint8, device)
-    # a call that will be refused allocates no negative shape
-    shape = (tokens, max(top_k, 0))
+    # a top_k that the library will refuse gets no outputs
+    shape = (tokens, top_k if 0 < top_k <= _MAX_EXPERTS_PER_TOKEN else 0)
     ids = torch.empty(shape, dtype=torch.int32, device=device)
     weights = torch.empty(shape, dtype=torch.float32, device=device)
     count = torch.empty(experts, dtype=torch.int32, device=device) if counts else None

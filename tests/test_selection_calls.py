@@ -237,3 +237,23 @@ def test_workspace_of_its_own(library):
     g.pick_tokens(on_gpu(2, 100), on_gpu(2))
     assert library.last()[14] == first                      # kept
     assert g._default_workspace(torch.device("cpu"), 0).buf is nms_buf
+
+
+def test_a_call_to_be_refused_allocates_nothing(monkeypatch):
+    """top_k above the limit, as far as an int goes: the library refuses it
+    before any output of that width is made."""
+    monkeypatch.setattr(sel, "_current_device", lambda: None)
+    monkeypatch.setattr(sel, "_raw_stream", lambda device: 0)
+    made = []
+    empty = torch.empty
+
+    def noted(*shape, **kw):
+        made.append(shape)
+        assert np.prod(shape[0] if isinstance(shape[0], tuple) else shape) < 1 << 20
+        return empty(*shape, **kw)
+
+    monkeypatch.setattr(sel.torch, "empty", noted)
+    for k in (0, -1, -2 ** 31, 65, 1 << 20, 2 ** 31 - 1):
+        with pytest.raises(g.NMSError) as e:
+            g.route_experts(on_gpu(1 << 14, 128), k)
+        assert e.value.status == "NMS_INVALID_ARG"
