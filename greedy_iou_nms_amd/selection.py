@@ -21,6 +21,7 @@ from . import Workspace, _check, _default_workspace, _lib, _raw_stream
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _capturing = torch.cuda.is_current_stream_capturing
+_data_ptr, _size, _stride = torch.Tensor.data_ptr, torch.Tensor.size, torch.Tensor.stride
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # nms_dtype
 _SCORES = {"softmax": 0, "sigmoid": 1}  # NMS_ROUTE_SOFTMAX, NMS_ROUTE_SIGMOID
@@ -124,19 +125,22 @@ def _route_options(score, top_k, renormalise, scale, groups, kept_groups, group_
     """The options' address.  They are remembered by plain numbers: a tensor
     would be remembered by its identity, whatever it holds by the next call,
     and 4.0 be taken for a 4 of an earlier one."""
-    if score not in _SCORES:
-        raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
-    groups = _whole(groups, "groups")
-    return _plain_options(
-        _SCORES[score], _whole(top_k, "top_k"), bool(renormalise), float(scale), groups,
-        groups if kept_groups is None else _whole(kept_groups, "kept_groups"),
-        _whole(group_top, "group_top"))
+    if not (type(top_k) is type(groups) is type(group_top) is int and type(scale) is float and
+            (kept_groups is None or type(kept_groups) is int)):
+        top_k, groups, group_top = map(operator.index, (top_k, groups, group_top))
+        kept_groups = None if kept_groups is None else operator.index(kept_groups)
+        scale = float(scale)
+    return _plain_options(score, top_k, bool(renormalise), scale, groups, kept_groups, group_top)
 
 
 @functools.lru_cache(maxsize=256)
 def _plain_options(score, top_k, renormalise, scale, groups, kept_groups, group_top):
-    return ctypes.byref(_RouteOptions(score, top_k, int(renormalise), scale, groups, kept_groups,
-                                      group_top))
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
+    kept_groups = groups if kept_groups is None else kept_groups
+    return ctypes.byref(_RouteOptions(
+        _SCORES[score], _whole(top_k, "top_k"), int(renormalise), scale, _whole(groups, "groups"),
+        _whole(kept_groups, "kept_groups"), _whole(group_top, "group_top")))
 
 
 def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
@@ -155,7 +159,8 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     is left for holds id -1 and weight 0."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
-    top_k = _whole(top_k, "top_k")  # of the options and of the outputs
+    if type(top_k) is not int:
+        top_k = operator.index(top_k)  # of the options and of the outputs
     if device.index != _current_device():
         with torch.cuda.device(device):
             return route_experts(logits, top_k, score, bias, groups, kept_groups, group_top,
@@ -259,7 +264,8 @@ class LogitRules:
             raise TypeError("the rules must be torch tensors with a dimension")
         # before anything is read of them
         matrices = [t for t in (history, bias_ids, bias_values, allowed) if t is not None]
-        at = self._places(given, matrices)
+        addresses, shapes = list(map(_data_ptr, given)), list(map(_size, matrices))
+        strides = list(map(_stride, matrices))
         device = given[0].device if given else None
         if given and not given[0].is_cuda:
             raise ValueError("the rules must be on a GPU device")
@@ -307,19 +313,15 @@ class LogitRules:
         self._ref = ctypes.byref(c)
         # aliases hold the memory that the addresses are of
         self._memory = [t.detach() for t in given]
-        self._tensors, self._matrices, self._at = given, matrices, at
-
-    @staticmethod
-    def _places(tensors, matrices) -> list:
-        """What tells whether the tensors are still where they were.  (A vector
-        whose memory is the same needs no more: it is read for as many rows as
-        it had.)"""
-        return (list(map(torch.Tensor.data_ptr, tensors)) +
-                [(t.shape, t.stride()) for t in matrices])
+        self._tensors, self._addresses = given, addresses
+        self._matrices, self._shapes, self._strides = matrices, shapes, strides
 
     def _for(self, rows: int, vocab: int, device) -> object:
         """The struct's address, for logits of this shape."""
-        if self._places(self._tensors, self._matrices) != self._at:
+        # (a vector whose memory is the same is read for as many rows as it had)
+        if (list(map(_data_ptr, self._tensors)) != self._addresses or
+                list(map(_size, self._matrices)) != self._shapes or
+                list(map(_stride, self._matrices)) != self._strides):
             self._lay_out()
         if self.vocab != vocab:
             raise ValueError("the rules are for %d tokens, the logits have %d" % (self.vocab, vocab))
