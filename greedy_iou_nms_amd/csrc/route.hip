@@ -356,11 +356,12 @@ __device__ __forceinline__ uint32_t short_key(T v) {
     return to_f32(v) > NEG_INF ? k : 0u;
 }
 
-// The binary64 score of one expert of a token, good to 2^-40.
+// The binary64 score of one expert of a token, good to 2^-40.  (A quotient:
+// a sigmoid is above 0 down to -709.78, where the inverse is out of range.)
 __device__ __forceinline__ double exact_score(bool softmax, float z, float top, double share,
                                               float bias) {
     const double s = softmax ? exp_below(z, top, [](double v) { return exp_of(v); }) * share
-                             : inverse_of(1.0 + exp_of(-(double)z));
+                             : 1.0 / (1.0 + exp_of(-(double)z));
     return s + (double)bias;
 }
 
