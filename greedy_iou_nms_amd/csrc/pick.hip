@@ -69,9 +69,11 @@ __device__ __forceinline__ float max4(float a, float b, float c, float d) {
 // use 1.
 __device__ __forceinline__ float warmth(float t) { return t > 0.0f ? t : 1.0f; }
 
-// z - top, with the limit 0 at z = top = +infinity.
+// z - top, with the limit 0 at z = top = +infinity, and finite, so that an
+// infinite temperature makes every quotient 0.  In binary64: two float32 values
+// may lie further apart than float32 reaches.
 __device__ __forceinline__ double below_top(float z, float top) {
-    return z == top ? 0.0 : (double)z - (double)top;
+    return z == top ? 0.0 : fmax((double)z - (double)top, -1.7976931348623157e308);
 }
 
 // The bin of v in [lo, hi], monotone in v: lo in bin 0, hi at most in the
@@ -350,7 +352,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
 #pragma unroll
             for (int j = 0; j < VALUES; ++j)
                 if (z[j] > NEG_INF)
-                    sum += z[j] == top ? 1.0f : __builtin_amdgcn_exp2f((z[j] - top) * c);
+                    sum += __builtin_amdgcn_exp2f((float)(below_top(z[j], top) * (double)c));
             sum = wave_sum(sum);
             break;
         }
@@ -383,7 +385,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
         double all = 0.0;
         if (wt > NEG_INF)
             all = (double)x.wave_sums[tid & (WAVES - 1)] *
-                  (wt == top ? 1.0 : (double)__builtin_amdgcn_exp2f((wt - top) * c));
+                  (double)__builtin_amdgcn_exp2f((float)(below_top(wt, top) * (double)c));
         all = wave_sum(all);
         if (tid == 0) parts[part] = Part{top, count, all, {e0, e1, e2, e3}, least_found, 0.0f};
     };

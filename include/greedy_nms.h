@@ -557,7 +557,7 @@ nms_status nms_pick_workspace_size(int64_t rows, int64_t vocab, int max_top_k, s
  *   uniform      device float[rows]: one number in [0, 1) per row (below: as
  *                0; above: the last token that stays).
  *   temperature  device float[rows] or NULL (1): t; 0 or below takes the first
- *                token.
+ *                token; at +infinity all allowed tokens weigh alike.
  *   top_k        device int32[rows] or NULL (max_top_k): clamped into
  *                1..max_top_k.
  *   top_p, min_p device float[rows] or NULL (1 and 0).  Where one of these
