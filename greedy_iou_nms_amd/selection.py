@@ -156,9 +156,15 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     expert) counts for the choice only; of ``groups`` groups of neighbouring
     experts ``kept_groups`` (default: all) may be chosen from; ``live`` (bool
     or uint8, one per token) marks padded rows with 0.  A place that no expert
-    is left for holds id -1 and weight 0."""
+    is left for holds id -1 and weight 0.
+
+    Where ``logits`` require a gradient, the weights carry it
+    (``route_experts_backward``)."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _Routed.apply(logits, top_k, score, bias, groups, kept_groups, group_top,
+                             bool(renormalise), float(scale), live, counts)
     if type(top_k) is not int:
         top_k = operator.index(top_k)  # of the options and of the outputs
     if device.index != _current_device():
@@ -181,6 +187,27 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     if status:
         _check(status)
     return (ids, weights, count) if counts else (ids, weights)
+
+
+class _Routed(torch.autograd.Function):
+    """``route_experts`` (called without gradients here) and its gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, top_k, score, bias, groups, kept_groups, group_top, renormalise,
+                scale, live, counts):
+        out = route_experts(logits, top_k, score, bias, groups, kept_groups, group_top,
+                            renormalise, scale, live, counts)
+        ctx.save_for_backward(logits, out[0])
+        ctx.options = score, renormalise, scale
+        ctx.mark_non_differentiable(out[0], *out[2:])
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_ids, grad_weights, *grad_counts):
+        logits, ids = ctx.saved_tensors
+        grad = route_experts_backward(logits, ids, grad_weights.contiguous(), *ctx.options)
+        return (grad,) + (None,) * 10
 
 
 def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights: torch.Tensor,
