@@ -268,7 +268,7 @@ class LogitRules:
     int32 and ``bias_values`` float32, (rows, entries), ids outside the
     vocabulary unused; ``allowed`` (masks, words) int64, bit v mod 64 of word
     v // 64 for token v; ``allowed_rows`` (rows,) int32, the mask of each row
-    (negative: every token is allowed)."""
+    (negative: every token is allowed).  None of them gets a gradient."""
 
     def __init__(self, vocab: int, history=None, history_len=None, prompt_len=None,
                  repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None,
@@ -359,6 +359,24 @@ class LogitRules:
         return self._ref
 
 
+class _Ungraded(torch.autograd.Function):
+    """The outputs of a call that has no gradient here, though its logits
+    require one: a backward pass that reaches them raises, where it would go on
+    without their part."""
+
+    @staticmethod
+    def forward(ctx, logits, name, call):
+        out = call(logits)
+        ctx.name = name
+        if isinstance(out, tuple):
+            ctx.mark_non_differentiable(*(t for t in out if not t.is_floating_point()))
+        return out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise NotImplementedError("%s has no gradient" % ctx.name)
+
+
 def _rules(rules, rows: int, vocab: int, device) -> object:
     if not isinstance(rules, LogitRules):
         raise TypeError("rules must be LogitRules")
@@ -368,9 +386,17 @@ def _rules(rules, rows: int, vocab: int, device) -> object:
 def adjust_logits(logits: torch.Tensor, rules: LogitRules,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The logits under the rules, a tensor like ``logits`` (or ``out``, which
-    may be ``logits`` itself and must not overlap it otherwise)."""
+    may be ``logits`` itself and must not overlap it otherwise).  It has no
+    gradient: a backward pass through it raises, and ``out`` is refused where
+    it or the logits require one."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
+    if torch.is_grad_enabled() and (logits.requires_grad or
+                                    getattr(out, "requires_grad", False)):
+        if out is not None:
+            raise RuntimeError("adjust_logits with out has no gradient, but logits or out "
+                               "require one")
+        return _Ungraded.apply(logits, "adjust_logits", lambda z: adjust_logits(z, rules))
     ref = _rules(rules, rows, vocab, device)
     if device.index != _current_device():
         with torch.cuda.device(device):
@@ -412,9 +438,13 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     ``temperature`` (0: the first token), ``top_p`` and ``min_p`` are float32
     and ``top_k`` int32, one per row (top_k up to ``max_top_k``, at most
     1024).  The logprob is that of the token under the softmax over all
-    allowed tokens.  A row without an allowed token gets -1 and -infinity."""
+    allowed tokens.  A row without an allowed token gets -1 and -infinity.
+    The logprobs have no gradient: a backward pass through them raises."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _Ungraded.apply(logits, "pick_tokens", lambda z: pick_tokens(
+            z, uniform, max_top_k, temperature, top_k, top_p, min_p, rules))
     if uniform is None:
         raise TypeError("uniform must be a torch tensor")
     f32 = torch.float32

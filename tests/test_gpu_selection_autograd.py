@@ -146,3 +146,48 @@ def test_another_stream_and_a_captured_step():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, explicit(x))
+
+
+# ------------------------------------------------- logits and tokens
+
+def rules_and_logits(rng, B=3, V=500):
+    g = lib()
+    z = normal(rng, B, V).requires_grad_()
+    history = torch.from_numpy(rng.integers(0, V, size=(B, 20)).astype(np.int32)).to(device())
+    rules = g.LogitRules(V, history=history,
+                         history_len=torch.full((B,), 20, dtype=torch.int32, device=device()),
+                         repetition=torch.full((B,), 1.5, device=device()))
+    return g, z, rules
+
+
+def test_adjusted_logits_do_not_lose_a_gradient_silently():
+    g, z, rules = rules_and_logits(np.random.default_rng(5))
+    with torch.no_grad():
+        want = g.adjust_logits(z, rules)
+    assert not want.requires_grad
+    out = g.adjust_logits(z, rules)
+    assert out.requires_grad and torch.equal(out, want)
+    with pytest.raises(NotImplementedError):
+        (out.sum() + z.sum()).backward()
+    assert not g.adjust_logits(z.detach(), rules).requires_grad
+    for kw in (dict(logits=z, out=torch.empty_like(want)), dict(logits=z, out=z),
+               dict(logits=want, out=torch.empty_like(want).requires_grad_())):
+        before = z.detach().clone()
+        with pytest.raises(RuntimeError):
+            g.adjust_logits(kw["logits"], rules, out=kw["out"])
+        assert torch.equal(z, before)
+        with torch.no_grad():
+            assert torch.equal(g.adjust_logits(kw["logits"].clone(), rules, out=kw["out"].clone()),
+                               want if kw["logits"] is z else g.adjust_logits(want, rules))
+
+
+def test_picked_tokens_do_not_lose_a_gradient_silently():
+    g, z, rules = rules_and_logits(np.random.default_rng(6))
+    u = torch.full((3,), 0.4, device=device())
+    with torch.no_grad():
+        want = g.pick_tokens(z, u, max_top_k=9, rules=rules)
+    ids, lp = g.pick_tokens(z, u, max_top_k=9, rules=rules)
+    assert torch.equal(ids, want[0]) and torch.equal(lp, want[1])
+    assert not ids.requires_grad and lp.requires_grad and not want[1].requires_grad
+    with pytest.raises(NotImplementedError):
+        lp.sum().backward()
