@@ -21,6 +21,8 @@ from . import Workspace, _check, _default_workspace, _lib, _raw_stream
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _capturing = torch.cuda.is_current_stream_capturing
+# tells autograd that a tensor's values change, which the library does unseen
+_overwritten = torch.autograd.graph.increment_version
 _data_ptr, _size, _stride = torch.Tensor.data_ptr, torch.Tensor.size, torch.Tensor.stride
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # nms_dtype
@@ -215,9 +217,9 @@ def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights
                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of ``route_experts``' weights in its logits, from the
     forward call's ``ids`` and the gradient of its weights; a tensor like
-    ``logits`` (or ``out``, which may be ``logits`` itself and must not overlap
-    it otherwise).  The choice of the experts, and so the bias, has
-    no gradient."""
+    ``logits`` (or ``out``, which may be ``logits`` itself, must not overlap it
+    otherwise and is refused where it requires a gradient).  The choice of the
+    experts, and so the bias, has no gradient, and this one has no further."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
@@ -241,6 +243,9 @@ def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights
         out_stride = experts
     else:
         out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
+        if out.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("route_experts_backward with an out that requires a gradient")
+        _overwritten(out)
     status = _lib.nms_route_experts_backward(
         logits.data_ptr(), code, tokens, experts, stride, ids.data_ptr(), grad_weights.data_ptr(),
         options, out.data_ptr(), out_stride, _raw_stream(device))
@@ -406,6 +411,7 @@ def adjust_logits(logits: torch.Tensor, rules: LogitRules,
         out_stride = vocab
     else:
         out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
+        _overwritten(out)
     status = _lib.nms_adjust_logits(logits.data_ptr(), code, rows, vocab, stride, ref,
                                     out.data_ptr(), out_stride, _raw_stream(device))
     if status:

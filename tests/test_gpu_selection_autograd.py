@@ -191,3 +191,31 @@ def test_picked_tokens_do_not_lose_a_gradient_silently():
     assert not ids.requires_grad and lp.requires_grad and not want[1].requires_grad
     with pytest.raises(NotImplementedError):
         lp.sum().backward()
+
+
+# ------------------------------------------------------- what out overwrites
+
+def test_writing_to_out_is_seen_by_autograd():
+    """A tensor that a backward pass needs, overwritten by a call in place: the
+    pass must not go on with the new values."""
+    g, z, rules = rules_and_logits(np.random.default_rng(7))
+    y = z.exp()                                     # its gradient needs y
+    with torch.no_grad():
+        assert g.adjust_logits(y, rules, out=y) is y
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+    other, x = torch.empty_like(z, requires_grad=False), normal(np.random.default_rng(8), 3, 500)
+    g.adjust_logits(x, rules, out=other)
+    version = other._version
+    g.adjust_logits(x, rules, out=other)
+    assert other._version > version
+    ids, w = g.route_experts(x, 4)
+    version = other._version
+    assert g.route_experts_backward(x, ids, w, out=other) is other
+    assert other._version > version
+    with pytest.raises(RuntimeError):
+        g.route_experts_backward(x, ids, w, out=torch.empty_like(x).requires_grad_())
+    with torch.inference_mode():                    # no versions there
+        x = torch.ones(3, 500, device=device())
+        assert g.adjust_logits(x, rules, out=x) is x
+        g.route_experts_backward(x, *g.route_experts(x, 4), out=x)
