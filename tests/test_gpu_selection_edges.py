@@ -7,7 +7,9 @@ import numpy as np
 import pytest
 
 from gpu_util import device, note
-from test_gpu_logits import SUM_ERROR, check_pick, lib, to_gpu
+from oracle import selection as plain
+from test_gpu_logits import (SUM_ERROR, check_pick, gpu_rules, lib, make_logits, make_rules,
+                             row_parameters, same, to_gpu)
 from test_gpu_route import check_route
 
 torch = pytest.importorskip("torch")
@@ -80,3 +82,132 @@ def test_infinite_temperature_and_infinite_logits(V, k):
         assert int(ids[b]) == order[int(float(u[b]) * len(order))]
         want = -math.log(len(there))
         assert abs(float(lp[b]) - want) <= SUM_ERROR + 2.0 ** -24 * abs(want)
+
+
+# --------------------------------------------- rows of more slices and forms
+
+def most_in_late_slices(rng, B, V, crowded=False):
+    """bfloat16 values, so that many are equal; the largest in the last slices."""
+    z = torch.from_numpy(rng.normal(size=(B, V)).astype(np.float32))
+    z[0, V - V // 16:] += 3.0
+    if crowded:
+        z[-1] = torch.round(z[-1])
+        z[-1, -9:] = z[-1].max()
+    return z.bfloat16()
+
+
+@pytest.mark.parametrize("V", [150001, 262147])
+@pytest.mark.parametrize("k", [1000, 1024])
+def test_more_candidates_than_a_join_holds(V, k):
+    """The join's waves hold 192 pieces of 64 candidates; these rows have 240
+    to 425, so that the rest is read again for every pass over them."""
+    rng = np.random.default_rng([V, k])
+    z = most_in_late_slices(rng, 5, V, crowded=True).float().numpy()
+    z[1] = 0.0
+    z[2] = np.sort(z[2])
+    z[3, rng.random(V) < 0.9] = np.finfo(np.float32).min
+    for _ in range(2):
+        check_pick(torch.from_numpy(z), z, **row_parameters(rng, 5, k))
+        check_pick(torch.from_numpy(z), z, uniform=rng.random(5).astype(np.float32), max_top_k=k,
+                   temperature=np.full(5, 3.0, np.float32))
+
+
+@pytest.mark.parametrize("V", [1048577, 1100003, 4194304])
+@pytest.mark.parametrize("k", [1, 40, 1024])
+def test_more_slices_than_a_wave_has_lanes(V, k):
+    rng = np.random.default_rng([V, k])
+    z = most_in_late_slices(rng, 3, V, crowded=True)
+    zf = z.float().numpy()
+    check_pick(z, zf, **row_parameters(rng, 3, k))
+    zf = np.full((2, V), -np.inf, np.float32)
+    zf[0, -1] = 1.0
+    zf[1, V - 30000:] = rng.normal(size=30000)
+    check_pick(torch.from_numpy(zf), zf, uniform=rng.random(2).astype(np.float32), max_top_k=k)
+    u = make_rules(rng, 3, V, L=500)
+    check_pick(z, plain.adjust(z.float().numpy(), **u), rules=gpu_rules(V, u),
+               **row_parameters(rng, 3, k))
+
+
+@pytest.mark.parametrize("V", [700, 8192, 8193])
+@pytest.mark.parametrize("k", [1, 40, 600])
+@pytest.mark.parametrize("B", [256, 257, 300])
+def test_many_short_rows(B, V, k):
+    """Both sides of the border between one launch and two, and of that between
+    slices of 8192 and of 16384."""
+    rng = np.random.default_rng([B, V, k])
+    z = most_in_late_slices(rng, B, V, crowded=True)
+    zf = z.float().numpy()
+    check_pick(z, zf, **row_parameters(rng, B, k))
+
+
+@pytest.mark.parametrize("V", [16384, 16385, 32767, 32768, 32769])
+@pytest.mark.parametrize("k", [1, 256, 257])
+def test_borders_of_a_row_in_one_launch(V, k):
+    rng = np.random.default_rng([V, k])
+    z = most_in_late_slices(rng, 4, V, crowded=True)
+    u = make_rules(rng, 4, V, L=500)
+    check_pick(z, plain.adjust(z.float().numpy(), **u), rules=gpu_rules(V, u),
+               **row_parameters(rng, 4, k))
+
+
+@pytest.mark.parametrize("B,V", [(256, 16384), (255, 16384), (64, 8192), (63, 8192), (2, 4194304),
+                                 (40, 40000)])
+@pytest.mark.parametrize("L", [4096, 4097])
+def test_borders_of_adjusting(B, V, L):
+    rng = np.random.default_rng([B, V, L])
+    u = make_rules(rng, B, V, L)
+    z, zf = make_logits(rng, B, V, "bf16")
+    note("adjust %d %d %d" % (B, V, L))
+    same(lib().adjust_logits(z.to(device()), gpu_rules(V, u)), plain.adjust(zf, **u))
+
+
+# ----------------------------------------------------- rules whose tensors move
+
+def test_rules_of_a_history_that_grows():
+    rng = np.random.default_rng(31)
+    B, V = 3, 900
+    z, zf = make_logits(rng, B, V, "f32")
+    z = z.to(device())
+    u = make_rules(rng, B, V, L=10)
+    on = {k: to_gpu(v) for k, v in u.items()}
+    rules = lib().LogitRules(V, **on)
+    same(lib().adjust_logits(z, rules), plain.adjust(zf, **u))
+    for L in (200, 7, 5000, 5001):
+        u.update({k: v for k, v in make_rules(rng, B, V, L=L).items() if "len" in k or
+                  k == "history"})
+        on["history"].resize_(B, L)
+        for name in ("history", "history_len", "prompt_len"):
+            on[name].copy_(to_gpu(u[name]))
+        same(lib().adjust_logits(z, rules), plain.adjust(zf, **u))
+        check_pick(z, plain.adjust(zf, **u), rules=rules, **row_parameters(rng, B, 20))
+    u["repetition"] = np.full(B, 1.75, np.float32)
+    on["repetition"].data = to_gpu(u["repetition"])
+    u["allowed"] = rng.integers(-2 ** 63, 2 ** 63 - 1, size=(4, 20), dtype=np.int64)
+    on["allowed"].set_(to_gpu(u["allowed"]))
+    same(lib().adjust_logits(z, rules), plain.adjust(zf, **u))
+
+
+def test_an_empty_batch_with_rules():
+    u = make_rules(np.random.default_rng(32), 3, 100)
+    on = {k: to_gpu(v)[:0] if k != "allowed" else to_gpu(v) for k, v in u.items()}
+    rules = lib().LogitRules(100, **on)
+    z = torch.zeros(0, 100, device=device())
+    assert lib().adjust_logits(z, rules).shape == (0, 100)
+    ids, lp = lib().pick_tokens(z, torch.zeros(0, device=device()), rules=rules)
+    assert ids.shape == (0,) and lp.shape == (0,)
+
+
+def test_picking_and_nms_in_turn():
+    """Both keep a workspace per thread and stream."""
+    g = lib()
+    rng = np.random.default_rng(33)
+    n = 3000
+    at = rng.random((n, 2)).astype(np.float32) * 300
+    boxes = torch.from_numpy(np.concatenate([at, at + 1 + rng.random((n, 2)).astype(np.float32)
+                                             * 30], axis=1)).to(device())
+    scores = torch.from_numpy(rng.random(n).astype(np.float32)).to(device())
+    z, zf = make_logits(rng, 4, 70000, "f32")
+    first = g.nms(boxes, scores, 0.5)
+    for _ in range(4):
+        check_pick(z, zf, **row_parameters(rng, 4, 900))
+        assert torch.equal(g.nms(boxes, scores, 0.5), first)
