@@ -252,9 +252,12 @@ __device__ __forceinline__ void write_token(const RouteArgs &a, int64_t t, bool 
         w = id >= 0 ? 1.0 / (1.0 + e(-(double)z)) : 0.0;
         sum = a.opt.renormalise ? all_sum<LANES>(w) : 1.0;
     }
-    // (a quotient where the inverse is out of range)
-    if (__builtin_expect(__ballot(!(sum > 1.0e-290)) == 0ull, 1)) w *= inverse_of(sum);
-    else w = sum > 0.0 ? w / sum : 0.0;
+    // a quotient where the inverse is out of range, and only there: the other
+    // tokens of the wave must not round differently for it
+    const bool in_range = sum > 1.0e-290;
+    double share = in_range ? w * inverse_of(sum) : 0.0;
+    if (__builtin_expect(!in_range && sum > 0.0, 0)) share = w / sum;
+    w = share;
     if (write && place < a.opt.top_k) {
         a.ids[t * a.opt.top_k + place] = id;
         a.weights[t * a.opt.top_k + place] = (float)(w * (double)a.opt.scale);

@@ -211,3 +211,44 @@ def test_picking_and_nms_in_turn():
     for _ in range(4):
         check_pick(z, zf, **row_parameters(rng, 4, 900))
         assert torch.equal(g.nms(boxes, scores, 0.5), first)
+
+
+# ------------------------------------------ neighbours that must not matter
+
+# Logits of a token's chosen experts one of whose weights rounds to another
+# float32 by a quotient than by the product with an inverse.
+CHOSEN = [
+    ("sigmoid", ["0x1.9407aap+1", "0x1.61eeaap+1", "0x1.12773ep+1", "0x1.7f0f08p+0",
+                 "0x1.6d8c74p+0", "0x1.6a6820p+0", "0x1.43f9d8p+0", "0x1.3fc452p+0"]),
+    ("sigmoid", ["0x1.14e26ap+1", "0x1.ac24a0p+0", "0x1.906c46p+0", "0x1.7461ccp+0",
+                 "0x1.5e7af0p+0", "0x1.4ec740p+0", "0x1.4a7b12p+0", "0x1.309752p+0"]),
+    ("sigmoid", ["0x1.0f36bap+1", "0x1.0027c8p+1", "0x1.da1202p+0", "0x1.c05c2ap+0",
+                 "0x1.9ea182p+0", "0x1.83a776p+0", "0x1.82e9f0p+0", "0x1.5de654p+0"]),
+    ("sigmoid", ["0x1.c8b170p+0", "0x1.c357f6p+0", "0x1.9d2024p+0", "0x1.5896cep+0",
+                 "0x1.1cea1ap+0", "0x1.be1084p-1", "0x1.a3ec4ap-1", "0x1.9ed144p-1"]),
+    ("sigmoid", ["0x1.3102c0p+1", "0x1.eeb8bap+0", "0x1.ee3de8p+0", "0x1.c11f76p+0",
+                 "0x1.bc5598p+0", "0x1.b2df18p+0", "0x1.4794cap+0", "0x1.2843c2p+0"]),
+    ("softmax", ["0x1.46891cp+1", "0x1.fd7e7ap+0", "0x1.f5639ep+0", "0x1.e9c392p+0",
+                 "0x1.e5dc32p+0", "0x1.7e87cep+0", "0x1.66a43ap+0", "0x1.38acb8p+0"]),
+]
+
+
+@pytest.mark.parametrize("score,chosen", CHOSEN)
+@pytest.mark.parametrize("E", [8, 64, 200, 500])
+def test_weights_do_not_depend_on_padded_neighbours(E, score, chosen):
+    rng = np.random.default_rng(E)
+    dev = device()
+    z = np.full((9, E), -40.0, np.float32)
+    z[:, rng.permutation(E)[:8]] = [float.fromhex(x) for x in chosen]
+    z = torch.from_numpy(z).to(dev)
+    ids, w = lib().route_experts(z, 8, score=score)
+    live = torch.ones(9, dtype=torch.bool, device=dev)
+    for dead in ([1], [0, 3, 4], [8], list(range(1, 9))):
+        live.fill_(True)
+        live[dead] = False
+        ids1, w1 = lib().route_experts(z, 8, score=score, live=live)
+        assert torch.equal(ids1[live], ids[live]) and torch.equal(w1[live], w[live])
+    empty = z.clone()
+    empty[2] = -math.inf
+    _, w1 = lib().route_experts(empty, 8, score=score)
+    assert torch.equal(w1[[0, 1, 3]], w[[0, 1, 3]])
