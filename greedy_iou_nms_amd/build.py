@@ -44,9 +44,12 @@ FLAGS = [
 # name.  The plain sweep kernel of a build that held 2048 list entries per
 # register set compiled to exactly 256 VGPRs and returned wrong kept sets.
 # The team sort's workgroups wait on one another, so all of them must be
-# resident at once; scratch memory could limit that.
+# resident at once; scratch memory could limit that.  The selection kernels
+# keep a row's values in registers (slices that spilled took 72 us for 55).
 GUARDED_KERNELS = ("12sweep_kernel", "17mask_sweep_kernel", "18group_sweep_kernel",
-                   "16small_nms_kernel", "16team_sort_kernel", "18team_sample_kernel")
+                   "16small_nms_kernel", "16team_sort_kernel", "18team_sample_kernel",
+                   "12quick_kernel", "12exact_kernel", "11back_kernel", "13adjust_kernel",
+                   "12slice_kernel", "12whole_kernel", "11join_kernel")
 MAX_VGPRS = 255
 
 

@@ -45,12 +45,7 @@ struct Part {
 // they are above is below the max_top_k-th value (or equal to it).
 __host__ __device__ constexpr int slice_cap(int k) { return k + k / 2 + 16; }
 
-__device__ __forceinline__ uint64_t candidate(float z, int token) {
-    const uint32_t k = order_key(z);
-    return k == 0u ? 0ull : ((uint64_t)k << 32) | (uint32_t)~token;
-}
-
-// The same of a value known to be above -infinity.
+// The word of a value above -infinity.
 __device__ __forceinline__ uint64_t candidate_of(float z, int token) {
     const int u = __float_as_int(z + 0.0f);
     return (uint64_t)(uint32_t)(u ^ ((u >> 31) | (int)0x80000000)) << 32 | (uint32_t)~token;

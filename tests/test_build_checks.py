@@ -17,3 +17,12 @@ def test_no_constant_index_past_an_array(source):
                         "-fstrict-flex-arrays=3", "-Werror=array-bounds",
                         os.path.join(build.CSRC, source)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_kernels_that_must_not_spill_are_watched():
+    fine = {"VGPRs": 75, "ScratchSize [bytes/lane]": 0, "VGPRs Spill": 0}
+    for kernel in ("quick", "exact", "back", "adjust", "slice", "whole", "join"):
+        name = "_ZN4gnms12_GLOBAL__N_1%d%s_kernelEv" % (len(kernel) + 7, kernel)
+        assert build.check_resources({name: fine}) == []
+        for field, value in (("VGPRs", 256), ("ScratchSize [bytes/lane]", 16), ("VGPRs Spill", 1)):
+            assert len(build.check_resources({name: {**fine, field: value}})) == 1
