@@ -136,11 +136,13 @@ def _workspace_size_lists(n: int) -> int:
 _WORKSPACE_TOO_SMALL = 2  # NMS_WORKSPACE_TOO_SMALL
 
 
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device: torch.device) -> int:
     """The current stream of ``device`` as a raw hipStream_t value."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if get is not None:
-        return int(get(device.index))
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -67,6 +67,14 @@ def _matrix(t, name: str) -> Tuple[int, int, int, int]:
     return code, rows, columns, stride
 
 
+def _like(logits, rows: int, columns: int, stride: int) -> torch.Tensor:
+    """A contiguous matrix of the logits' shape and type (1 us less of the
+    caller's time where they are contiguous themselves)."""
+    if stride == columns:
+        return torch.empty_like(logits)
+    return torch.empty((rows, columns), dtype=logits.dtype, device=logits.device)
+
+
 def _rows(t, name: str, device=None, shape=None, dtype=None) -> int:
     """The row stride of a matrix whose rows hold neighbouring elements and
     do not overlap; other layouts are refused."""
@@ -239,7 +247,7 @@ def route_experts_backward(logits: torch.Tensor, ids: torch.Tensor, grad_weights
                                           out)
     options = _route_options(score, top_k, renormalise, scale, 1, 1, 1)
     if out is None:
-        out = torch.empty((tokens, experts), dtype=logits.dtype, device=device)
+        out = _like(logits, tokens, experts, stride)
         out_stride = experts
     else:
         out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
@@ -407,7 +415,7 @@ def adjust_logits(logits: torch.Tensor, rules: LogitRules,
         with torch.cuda.device(device):
             return adjust_logits(logits, rules, out)
     if out is None:
-        out = torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        out = _like(logits, rows, vocab, stride)
         out_stride = vocab
     else:
         out_stride = _rows(out, "out", device, logits.shape, logits.dtype)
@@ -472,7 +480,7 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     kept = Workspace(device) if _capturing() else _default_workspace(device, stream, "pick")
     buf = kept.get(nbytes, device)
     ids = torch.empty(rows, dtype=torch.int32, device=device)
-    logprobs = torch.empty(rows, dtype=f32, device=device)
+    logprobs = torch.empty_like(uniform)
     status = _lib.nms_pick_tokens(logits.data_ptr(), code, rows, vocab, stride, ref, u, t, k, p, m,
                                   max_top_k, ids.data_ptr(), logprobs.data_ptr(),
                                   buf.data_ptr(), nbytes, stream)
