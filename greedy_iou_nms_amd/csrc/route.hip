@@ -359,18 +359,21 @@ __device__ __forceinline__ uint32_t short_key(T v) {
     return to_f32(v) > NEG_INF ? k : 0u;
 }
 
-// The binary64 score of one expert of a token, good to 2^-40.  (A quotient:
-// a sigmoid is above 0 down to -709.78, where the inverse is out of range.)
+// The score of one expert of a token as binary64 has it: to the last places,
+// or groups whose sums are equal, as 1 / (1 + exp(-z)) + 1 / (1 + exp(z)) is for
+// every z, would come in the order of the errors.  (16384 tokens of 256 experts
+// take the same 9.6 us with exp_of, and 34 if all their scores are equal; a
+// sigmoid is above 0 down to -709.78, where inverse_of is out of range.)
 __device__ __forceinline__ double exact_score(bool softmax, float z, float top, double share,
                                               float bias) {
-    const double s = softmax ? exp_below(z, top, [](double v) { return exp_of(v); }) * share
-                             : 1.0 / (1.0 + exp_of(-(double)z));
+    const double s = softmax ? exp_below(z, top, [](double v) { return exp(v); }) * share
+                             : 1.0 / (1.0 + exp(-(double)z));
     return s + (double)bias;
 }
 
-// The choice of quick_kernel for a wave's tokens, from binary64 scores (good
-// to 2^-40): lane i of a token gets its i-th expert, or -1.  z: the lane's
-// logits, -infinity where there is none; bias: the lane's, or 0.
+// The choice of quick_kernel for a wave's tokens, from binary64 scores: lane i
+// of a token gets its i-th expert, or -1.  z: the lane's logits, -infinity where
+// there is none; bias: the lane's, or 0.
 template <int LANES, int VALUES>
 __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z,
                                               const float *bias, float top, double sum,

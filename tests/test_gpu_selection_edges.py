@@ -37,6 +37,22 @@ def test_sigmoid_scores_near_the_end_of_binary64(E, G, kept):
                     group_top=1, bias=bias)
 
 
+@pytest.mark.parametrize("E,G,kept,k", [(4, 2, 1, 2), (32, 16, 7, 6), (48, 16, 10, 5),
+                                        (128, 64, 32, 8), (120, 30, 24, 9), (64, 8, 3, 6),
+                                        (256, 8, 4, 8), (512, 128, 60, 8)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_whose_sums_are_equal(E, G, kept, k, biased):
+    """Sigmoid scores of z and of -z sum to 1 for every z: groups of such pairs
+    are equal, and the lower ones stay."""
+    rng = np.random.default_rng([E, G])
+    z = np.round(rng.normal(size=(60, E)) * 2) / 2
+    z[:, 1::2] = np.where(rng.random((60, E // 2)) < 0.6, -z[:, ::2], z[:, 1::2])
+    z[0, 1::2] = -z[0, ::2]
+    for dtype in (torch.float32, torch.bfloat16):
+        check_route(torch.from_numpy(z).to(dtype), z, score="sigmoid", top_k=k, groups=G,
+                    kept_groups=kept, bias=np.zeros(E, np.float32) if biased else None)
+
+
 # ------------------------------------------------------ temperatures at the end
 
 @pytest.mark.parametrize("V,k", [(40, 1), (40, 30), (9000, 40), (33000, 400), (70000, 900),
