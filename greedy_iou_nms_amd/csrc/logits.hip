@@ -1,9 +1,10 @@
 // Penalties for repeated tokens, biases and grammar masks on logits: one
 // workgroup per slice of a row, which adjusts the tokens that the rules touch
-// in LDS and streams the slice once (adjust_core.h).  Memory bounds it where
-// there is much to do: 256 rows of 131072 bfloat16 logits with 2048 history
-// entries take 30.5 us for 138 MB (4.5 TB/s; a copy of that size reaches 5.3);
-// 4 rows of 32000 take 4.5 us, which is latency.
+// in LDS and streams the slice once (adjust_core.h).  256 rows of 131072
+// bfloat16 logits with 2048 history entries take 30 us for 138 MB, 4.6 TB/s: a
+// copy from HBM reaches 5.1 to 5.4, one of this size that stays in the last
+// cache 8.2, so that gathering the rules before the stream shows too; 4 rows of
+// 32000 take 4.4 us, which is latency.
 #include "adjust_core.h"
 
 #pragma clang fp contract(off)

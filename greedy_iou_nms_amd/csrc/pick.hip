@@ -271,9 +271,10 @@ __device__ __forceinline__ uint32_t narrowed(SliceSpace<THREADS, VALUES> &x, uin
 // Instructions bound it: a wave (1024 tokens) issues 230 for the values, the
 // maximum and the softmax sum, 115 more to find 50 candidates, 210 to find
 // 1000, 150 for a history of 4096, 20 for biases and 25 for a mask.  256 rows
-// of 131072 bfloat16 logits with all of these take 47.5 us, 35 of them issuing,
-// where reading the 72 MB takes 14; 64 rows of 100003 float32 logits with 50
-// candidates 12.6 us (reading: 5).
+// of 131072 bfloat16 logits with all of these take 47.7 us, 35 of them issuing,
+// where reading the 72 MB takes 10 to 14 (a copy's 7.5 TB/s from cache, 5.1 from
+// HBM); 64 rows of 100003 float32 logits with 50 candidates 12.4 us (reading:
+// 3.5 to 5).
 template <typename T, int THREADS, int VALUES, int GROUP, bool FIRST>
 __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *found,
                                       SliceSpace<THREADS, VALUES> &x) {
@@ -880,16 +881,26 @@ __global__ __launch_bounds__(1024, 4) void whole_kernel(PickArgs a, uint32_t inv
 }
 
 // How a row is split.  Not at all, in one launch, while no more than one
-// workgroup of 1024 threads is wanted per CU: at 32000 tokens one row with one
-// candidate takes 9.2 us a call so and 11.8 in two launches, which are bound by
-// launching (8.7 and 6.7 replayed in a graph); 256 rows with 1000 candidates
-// 20.2 and 23.6; but 600 rows of 16000 tokens 30.1 and 22.0.
+// workgroup of 1024 threads is wanted per CU.  Bfloat16 rows, us a call, eager /
+// in a graph, in one launch and in two:
+//   rows x tokens, candidates            one launch      two
+//   1 x 32000, 1                         9.5 / 6.7       11.7 / 7.1
+//   1 x 32000, 1, a history of 200       9.8 / 8.4       12.4 / 8.0
+//   1 x 32000, 50, a history of 200      13.8 / 13.8     12.8 / 12.4
+//   64 x 32000, 50, a history of 200     14.7 / 14.7     13.8 / 13.2
+//   256 x 8000, 50, a history of 200     12.5 / 12.4     13.4 / 12.8
+//   256 x 32000, 1000, a history of 200  18.1 / 18.1     21.9 / 21.7
+//   300 x 32000, 50, a history of 200    28.4 / 28.4     21.1 / 20.4
+//   600 x 8000, 50, a history of 200     30.3 / 30.4     19.4 / 19.2
+// (What the first form loses by with 50 candidates in few rows is less than
+// what it gains with one or with many.)
 // Else in slices of 16384 tokens, or of 8192 where the vocabulary has no more
-// (300 rows of 8000 with 50 candidates: 15.9 us, and 17.0 in one of 16384).
+// (300 rows of 8000 with 50 candidates: 13.5 us, and 15.1 in one of 16384).
 // Slices of 8192 have twice the candidates to join and every slice reads the
-// whole history: 17 rows of 131072 with 1000 candidates take 33 us in them and
-// 23 in slices of 16384, 256 rows 93 and 59 (55 now); one row with 50 candidates 15.0
-// and 14.6.  512 threads with 32 tokens each made 65 us of the 59.
+// whole history: 17 rows of 131072 with 1000 candidates take 31 us in them and
+// 20.7 in slices of 16384, 256 rows 73 and 46 (86 and 55 with a history of
+// 4096); one row with 50 candidates 14.2 and 13.2.  512 threads with 32 tokens
+// each made 65 us where 16384 by 1024 threads made 59.
 constexpr int WHOLE_MOST = 32768;
 
 bool whole(int64_t rows, int vocab) { return vocab <= WHOLE_MOST && rows <= 256; }

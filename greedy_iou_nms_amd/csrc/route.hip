@@ -446,11 +446,13 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, const float *z
 //
 // A token's row is read once, in one load per lane, and everything after it
 // stays in registers: what bounds a large call is the instructions (Batcher's
-// sort per lane, then top_k maxima over the lanes), not memory.  16384 tokens
-// of 256 float32 experts in 8 groups, top 8: 11.2 us, where reading them takes
-// 3.3 us; 5003 of 60 float16 experts, top 4: 4.3 us; a decode step of 8 tokens
-// 3.5 us, all of it latency.  16 lanes rather than a wave per token leave four
-// tokens' steps to share each instruction.
+// sort per lane, then top_k maxima over the lanes, each of which moves all
+// VALUES keys up), and that its 4096 waves are one fill of the GPU, so that
+// reading and computing hardly overlap.  16384 tokens of 256 float32 experts in
+// 8 groups, top 8: 11 us, 9.6 in a graph, where reading them takes 2.4 at a
+// copy's 7.4 TB/s from cache; 5003 of 60 float16 experts, top 4: 4.3 us; a
+// decode step of 8 tokens 3.6 us, all of it latency.  16 lanes rather than a
+// wave per token leave four tokens' steps to share each instruction.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(RT, 4) void quick_kernel(RouteArgs a, int group_lanes) {
     constexpr int TOKENS = 64 / LANES;  // per wave
@@ -766,10 +768,12 @@ static_assert(CT == NMS_ROUTE_MAX_EXPERTS, "a thread per expert");
 // Only the first needs the whole row.  LANES lanes share a token, VALUES
 // experts each; the chosen experts' terms go to their places through LDS, all
 // at once, or one after another where an index comes twice, so that it adds up
-// in a fixed order.  32768 tokens of 128 bfloat16 experts, plain softmax: 7.1
-// us, of which 3.8 are instructions (283 per wave of four tokens) and 3.6 would
-// be the reading and writing alone (19 MB); one term after another took 8.9,
-// the library's exponential 8.7.
+// in a fixed order.  32768 tokens of 128 bfloat16 experts, plain softmax: 7.2
+// us (renormalised 5.6, in a graph), of which 3.8 are instructions (283 per wave
+// of four tokens; every lane has places for 64 / LANES chosen experts, whatever
+// top_k is) and 2.6 would be the reading and writing alone (19 MB at a copy's
+// 7.4 TB/s from cache); one term after another took 8.9, the library's
+// exponential 8.7.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(RT) void back_kernel(RouteBackArgs a) {
     constexpr int TOKENS = 64 / LANES;            // per wave
@@ -975,6 +979,11 @@ bool holds(const RouteArgs &a, int lanes, int values, int *group_lanes) {
     return a.opt.groups * n <= lanes;
 }
 
+// The fewest lanes and places that hold the shape; binary64 throughout where
+// groups are more than lanes.  8192 tokens of float32 with top 8, in a graph: 256
+// experts 7.0 us, 384 19.5, 512 18.4 and 1024 17.9 (the last three a wave per
+// token, 384 with 40 of 64 lanes empty); 512 in 64 groups 35 us; in 512 groups,
+// which only exact_kernel holds, 1363 us, and 539 for 128 tokens.
 template <typename T>
 bool run_route(const RouteArgs &a, hipStream_t stream) {
     int g = 1;
@@ -993,6 +1002,8 @@ void run_back(const RouteBackArgs &a, hipStream_t stream) {
     back_kernel<T, LANES, VALUES><<<(unsigned)((a.tokens + per - 1) / per), RT, 0, stream>>>(a);
 }
 
+// 8192 float32 tokens, top 8, softmax over all: 256 experts 7.1 us, 384 10.8, 512
+// 13.2, 1024 20.1.
 template <typename T>
 void run_back(const RouteBackArgs &a, hipStream_t stream) {
     if (a.experts <= 64) run_back<T, 16, 4>(a, stream);

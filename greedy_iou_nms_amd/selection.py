@@ -450,8 +450,10 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
 
     ``uniform`` (rows,) float32 holds one number in [0, 1) per row;
     ``temperature`` (0: the first token), ``top_p`` and ``min_p`` are float32
-    and ``top_k`` int32, one per row (top_k up to ``max_top_k``, at most
-    1024).  The logprob is that of the token under the softmax over all
+    and ``top_k`` int32, one per row.  The draw is always from the first
+    ``max_top_k`` tokens (64 unless given, at most 1024) or a row's first
+    ``top_k`` of them; a ``top_k`` of 0 or below takes the first token and does
+    not lift the limit.  The logprob is that of the token under the softmax over all
     allowed tokens.  A row without an allowed token gets -1 and -infinity.
     The logprobs have no gradient: a backward pass through them raises."""
     code, rows, vocab, stride = _matrix(logits, "logits")

@@ -559,7 +559,8 @@ nms_status nms_pick_workspace_size(int64_t rows, int64_t vocab, int max_top_k, s
  *   temperature  device float[rows] or NULL (1): t; 0 or below takes the first
  *                token; at +infinity all allowed tokens weigh alike.
  *   top_k        device int32[rows] or NULL (max_top_k): clamped into
- *                1..max_top_k.
+ *                1..max_top_k (0 and below take the first token; there is no
+ *                value for a draw from more than max_top_k tokens).
  *   top_p, min_p device float[rows] or NULL (1 and 0).  Where one of these
  *                four is not a number, the first token is taken.
  *   max_top_k    1 .. NMS_MAX_TOP_K.
