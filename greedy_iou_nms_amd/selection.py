@@ -404,8 +404,8 @@ def adjust_logits(logits: torch.Tensor, rules: LogitRules,
     it or the logits require one."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
-    if torch.is_grad_enabled() and (logits.requires_grad or
-                                    getattr(out, "requires_grad", False)):
+    if ((logits.requires_grad or (out is not None and getattr(out, "requires_grad", False))) and
+            torch.is_grad_enabled()):
         if out is not None:
             raise RuntimeError("adjust_logits with out has no gradient, but logits or out "
                                "require one")
