@@ -169,7 +169,9 @@ def route_experts(logits: torch.Tensor, top_k: int, score: str = "softmax",
     is left for holds id -1 and weight 0.
 
     Where ``logits`` require a gradient, the weights carry it
-    (``route_experts_backward``)."""
+    (``route_experts_backward``).  While a step is captured with its backward
+    pass, no eager graph of the same leaves may be alive, as with torch's own
+    operators."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
     if logits.requires_grad and torch.is_grad_enabled():
