@@ -293,6 +293,11 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     const RowRules r = row_rules(a.rules, row, a.uniform);
     const float warm = warmth(parameter(a.temperature, row, 1.0f, a.uniform));
     const float c = fminf(1.4426950408889634f / warm, 3.0e38f);
+    // exp((z - top) / t) where c, or a product with it, may be out of range
+    auto share = [&](float v, float most) {
+        return __builtin_amdgcn_exp2f(
+            (float)(below_top(v, most) * (1.4426950408889634 / (double)warm)));
+    };
     const T *in = static_cast<const T *>(a.logits) + row * a.row_stride + lo;
     const Raw<T, THREADS, VALUES> raw(r, lo, size, in);
     for (int i = tid; i < BINS; i += THREADS) hist[i] = 0;
@@ -310,8 +315,9 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
     // to that: exp2(z c - top c), one multiply-add and one exponential a value,
     // where the rounding of top c is a factor of all terms and is taken out of
     // the sum.  A NaN, an infinite top, a c of 0 or a product of 2^24 and more
-    // show in the sum or in what is taken out; then the values are gone over
-    // again, with a NaN made -infinity and each difference taken by itself.
+    // show in the sum or in what is taken out; then, and where c does not reach
+    // (temperatures below 4.8e-39), the values are gone over again, with a NaN
+    // made -infinity and each difference taken by itself.
     float m[VALUES / GROUP], top, sum;
     for (bool again = false;; again = true) {
         if (again) {
@@ -343,12 +349,13 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
             for (int j = 0; j < VALUES; ++j)
                 sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[j], c, -hi));
             sum = wave_sum(sum) * __builtin_amdgcn_exp2f(-rest);
-            if (__builtin_amdgcn_readfirstlane(sum < 3.0e38f && fabsf(rest) <= 1.0f)) break;
+            if (__builtin_amdgcn_readfirstlane(sum < 3.0e38f && fabsf(rest) <= 1.0f &&
+                                               c < 3.0e38f))
+                break;
         } else {
 #pragma unroll
             for (int j = 0; j < VALUES; ++j)
-                if (z[j] > NEG_INF)
-                    sum += __builtin_amdgcn_exp2f((float)(below_top(z[j], top) * (double)c));
+                if (z[j] > NEG_INF) sum += share(z[j], top);
             sum = wave_sum(sum);
             break;
         }
@@ -380,8 +387,7 @@ __device__ __forceinline__ void slice(const PickArgs &a, Part *parts, uint64_t *
         const float wt = tid < WAVES ? x.wave_top[tid & (WAVES - 1)] : NEG_INF;
         double all = 0.0;
         if (wt > NEG_INF)
-            all = (double)x.wave_sums[tid & (WAVES - 1)] *
-                  (double)__builtin_amdgcn_exp2f((float)(below_top(wt, top) * (double)c));
+            all = (double)x.wave_sums[tid & (WAVES - 1)] * (double)share(wt, top);
         all = wave_sum(all);
         if (tid == 0) parts[part] = Part{top, count, all, {e0, e1, e2, e3}, least_found, 0.0f};
     };

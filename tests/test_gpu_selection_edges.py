@@ -78,6 +78,19 @@ def test_temperatures_that_make_the_largest_distances_small(V, k):
                    max_top_k=k, temperature=np.full(6, t, np.float32))
 
 
+@pytest.mark.parametrize("V,k", [(40, 1), (40, 30), (9000, 40), (33000, 400), (70000, 900),
+                                 (70000, 1)])
+@pytest.mark.parametrize("size", [1e-44, 1e-41, 1e-38])
+def test_temperatures_below_the_normal_numbers(V, k, size):
+    """Logits of the same size as the temperature, down to its smallest step."""
+    rng = np.random.default_rng([V, k])
+    z = (rng.normal(size=(4, V)) * size).astype(np.float32)
+    z[3, ::3] = -np.inf
+    for t in (1e-45, 1e-41, 1e-38):
+        check_pick(torch.from_numpy(z), z, "t=%g" % t, uniform=rng.random(4).astype(np.float32),
+                   max_top_k=k, temperature=np.full(4, t, np.float32))
+
+
 @pytest.mark.parametrize("V,k", [(40, 1), (40, 30), (9000, 40), (33000, 400), (70000, 900)])
 def test_infinite_temperature_and_infinite_logits(V, k):
     """All tokens that are allowed weigh alike."""
