@@ -22,7 +22,9 @@ __all__ = [
     "debug_order", "debug_mask", "debug_decide", "debug_plan", "library_path",
     "MATRIX_STAGES", "matrix_nms", "matrix_nms_profiled", "matrix_workspace_size",
     "route_experts", "route_experts_backward", "LogitRules", "adjust_logits", "pick_tokens",
-    "pick_workspace_size",
+    "pick_workspace_size", "token_logprobs", "token_logprobs_backward", "policy_loss",
+    "policy_loss_with_grad", "preference_loss", "preference_loss_with_grad", "balance_loss",
+    "balance_loss_with_grad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -103,6 +105,20 @@ def _load():
     lib.nms_pick_tokens.argtypes = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp,
                                     c_vp, c_vp, c_int, c_vp, c_vp, c_vp, c_sz, c_vp]
     lib.nms_pick_tokens.restype = c_int
+    p_sz = ctypes.POINTER(c_sz)
+    rows = [c_vp, c_int, c_i64, c_i64, c_i64, c_vp]  # logits and what comes with each row
+    space = [c_vp, c_sz, c_vp]
+    for name, args in (
+            ("nms_loss_workspace_size", [c_i64, c_i64, c_i64, p_sz]),
+            ("nms_token_logprobs", rows + [c_vp] * 3 + space),
+            ("nms_token_logprobs_backward", rows + [c_vp] * 4 + [c_i64] + space),
+            ("nms_policy_loss", rows + [c_vp] * 11 + [c_i64] + space),
+            ("nms_preference_loss", rows + [c_vp, c_i64] + [c_vp] * 8 + [c_i64] + space),
+            ("nms_preference_loss_backward", rows + [c_vp, c_i64] + [c_vp] * 5 + [c_i64] + space),
+            ("nms_balance_loss", rows + [c_vp] * 2 + [c_i64] + [c_vp] * 5 + [c_i64] + space),
+            ("nms_balance_workspace_size", [c_i64, c_i64, c_i64, c_int, p_sz])):
+        entry = getattr(lib, name)
+        entry.argtypes, entry.restype = args, c_int
     return lib
 
 
@@ -491,3 +507,9 @@ def matrix_nms_profiled(boxes, scores, score_threshold, sigma=0.5, workspace=Non
 
 from .selection import (LogitRules, adjust_logits, pick_tokens, pick_workspace_size,  # noqa: E402
                         route_experts, route_experts_backward)
+
+# ----------------------------------------------------- losses of language models
+
+from .losses import (balance_loss, balance_loss_with_grad, policy_loss,  # noqa: E402
+                     policy_loss_with_grad, preference_loss, preference_loss_with_grad,
+                     token_logprobs, token_logprobs_backward)

@@ -28,7 +28,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["radix.hip", "team_sort.hip", "mask.hip", "sweep.hip", "matrix.hip", "nms_api.cpp",
-           "route.hip", "logits.hip", "pick.hip", "select_api.cpp"]
+           "route.hip", "logits.hip", "pick.hip", "select_api.cpp",
+           "loss.hip", "balance.hip", "loss_api.cpp"]
 
 FLAGS = [
     "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-x", "hip",

@@ -26,56 +26,6 @@ constexpr double LOWEST = -__builtin_inf();
 
 // ---------------------------------------- reductions over 4 .. 64 lanes
 
-// A DPP move that reaches every lane (permutations and mirrors within 16
-// lanes), which the compiler can make part of the instruction that uses it.
-template <int CTRL>
-__device__ __forceinline__ uint32_t moved(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
-}
-template <int CTRL>
-__device__ __forceinline__ int moved(int v) {
-    return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
-}
-template <int CTRL>
-__device__ __forceinline__ float moved(float v) {
-    return __int_as_float(moved<CTRL>(__float_as_int(v)));
-}
-template <int CTRL>
-__device__ __forceinline__ double moved(double v) {
-    const uint64_t x = (uint64_t)__double_as_longlong(v);
-    return __longlong_as_double((long long)((uint64_t)moved<CTRL>((uint32_t)(x >> 32)) << 32 |
-                                            moved<CTRL>((uint32_t)x)));
-}
-
-constexpr int XOR1 = 0xB1, XOR2 = 0x4E;            // quads permuted
-constexpr int MIRROR8 = 0x141, MIRROR16 = 0x140;   // lanes in reverse order
-constexpr int ROTATE = 0x120;                      // + n: by n lanes within 16
-
-// Combines with every lane of the aligned N lanes; the result is in all of
-// them.  Mirrors serve as butterfly steps once the halves agree.
-template <int N, typename V, typename F>
-__device__ __forceinline__ V all_lanes(V v, F f) {
-    if (N >= 2) v = f(v, moved<XOR1>(v));
-    if (N >= 4) v = f(v, moved<XOR2>(v));
-    if (N >= 8) v = f(v, moved<MIRROR8>(v));
-    if (N >= 16) v = f(v, moved<MIRROR16>(v));
-    if (N >= 32) v = f(v, __shfl_xor(v, 16));
-    if (N >= 64) v = f(v, __shfl_xor(v, 32));
-    return v;
-}
-template <int N, typename V>
-__device__ __forceinline__ V all_max(V v) {
-    return all_lanes<N>(v, [](V a, V b) { return a > b ? a : b; });
-}
-template <int N, typename V>
-__device__ __forceinline__ V all_min(V v) {
-    return all_lanes<N>(v, [](V a, V b) { return a < b ? a : b; });
-}
-template <int N, typename V>
-__device__ __forceinline__ V all_sum(V v) {
-    return all_lanes<N>(v, [](V a, V b) { return a + b; });
-}
-
 // ------------------------------------------------------------ exact scores
 
 // exp(x) to 2^-40 of its value: 2^n from the exponent, a Taylor polynomial of

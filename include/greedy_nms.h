@@ -586,6 +586,221 @@ nms_status nms_pick_tokens(const void *logits, nms_dtype dtype, int64_t rows, in
                            const float *min_p, int max_top_k, int32_t *ids, float *logprobs,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Losses of language models: what trains the models whose tokens and experts
+ * the operators above select.  Log probabilities of given tokens, the clipped
+ * policy loss and the preference loss that are made of them, and the balance
+ * loss of routing, each with its gradient in the logits.
+ *
+ * As for the operators above: asynchronous, capturable, nothing is allocated,
+ * read back or kept, device data cannot make a call fail, and two calls that
+ * may run at the same time need workspaces of their own.  Results do not
+ * depend on how the GPU schedules a call: the same input gives the same bits.
+ *
+ * Rows of logits: `rows` rows of `vocab` elements of dtype, row_stride
+ * elements apart, with one token each.  A row counts where its token is in
+ * 0..vocab-1 (and, for the policy loss, its weight is not 0); one that does
+ * not has log probability, entropy and gradient 0 and is not read.  With t
+ * the row's temperature, p = softmax(z / t) and a the token,
+ *     log probability  log p_a;    entropy  H = -sum p log p.
+ * A logit of -infinity has probability 0.  NaN or +infinity in a row that
+ * counts makes its results NaN (nms_pick_tokens passes over a NaN; a loss does
+ * not hide it); where all logits are -infinity, the log probability is
+ * -infinity and entropy and gradient are 0.  A temperature of 0 or below, or
+ * NaN, counts as 1 (the log probability that nms_pick_tokens gives for it); at
+ * +infinity all tokens but those at -infinity weigh alike.
+ * Terms are computed in float32, sums over rows in binary64.
+ *
+ * grad_logits: device, rows of elements of dtype, grad_stride elements apart,
+ * every element is written (0 in rows that do not count); may be logits, with
+ * the same stride, and must not overlap it otherwise.  Rounded once to dtype.
+ * grad_loss: device float, the gradient of the loss, or NULL: 1.  (With
+ * float16 logits a scaled loss keeps small gradients in range.)
+ * ------------------------------------------------------------------------ */
+
+#define NMS_MAX_PAIRS 32768
+#define NMS_MAX_SEQUENCES 65536
+
+/*
+ * nms_loss_workspace_size -- device workspace needed by the calls on rows of
+ * logits below.
+ *   pairs  of nms_preference_loss and its gradient; 0 for the others.
+ * Returns NMS_OK, NMS_INVALID_ARG or NMS_TOO_LARGE.
+ */
+nms_status nms_loss_workspace_size(int64_t rows, int64_t vocab, int64_t pairs, size_t *bytes);
+
+/*
+ * nms_token_logprobs -- log probabilities of given tokens.
+ *   tokens       device int32[rows].
+ *   temperature  device float[rows] or NULL: 1.
+ *   logprobs     device float[rows].
+ *   entropies    device float[rows] or NULL: not wanted.
+ *   workspace    device, 256-byte aligned, nms_loss_workspace_size() bytes.
+ * Returns NMS_OK, NMS_INVALID_ARG, NMS_WORKSPACE_TOO_SMALL, NMS_TOO_LARGE (as
+ * for nms_pick_tokens) or NMS_HIP_ERROR.
+ */
+nms_status nms_token_logprobs(const void *logits, nms_dtype dtype, int64_t rows, int64_t vocab,
+                              int64_t row_stride, const int32_t *tokens, const float *temperature,
+                              float *logprobs, float *entropies, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * nms_token_logprobs_backward -- the gradient of these in the logits,
+ *     dz_j = (g ([j = a] - p_j) - h p_j (log p_j + H)) / t
+ *   grad_logprobs   device float[rows]: g.
+ *   grad_entropies  device float[rows] or NULL: h, 0.
+ * A row whose g and h are 0 has gradient 0, whatever it holds.
+ * Returns as nms_token_logprobs.
+ */
+nms_status nms_token_logprobs_backward(const void *logits, nms_dtype dtype, int64_t rows,
+                                       int64_t vocab, int64_t row_stride, const int32_t *tokens,
+                                       const float *temperature, const float *grad_logprobs,
+                                       const float *grad_entropies, void *grad_logits,
+                                       int64_t grad_stride, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+typedef struct nms_policy_options {
+    float clip_low, clip_high; /* the ratio is held in 1 - clip_low .. 1 + clip_high;
+                                  0 <= clip_low <= 1, 0 <= clip_high (finite) */
+    float kl;                  /* weight of the divergence from the reference, >= 0 */
+    float entropy;             /* weight of the entropy bonus, finite */
+} nms_policy_options;
+
+/*
+ * nms_policy_loss -- the clipped policy loss over rows of logits, its gradient
+ * or both at once (which reads the logits once where a row fits the registers
+ * of a compute unit).  With l a row's log probability, r = exp(l - old),
+ *     each = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A)
+ *            + kl (exp(ref - l) - (ref - l) - 1) - entropy H
+ *     loss = sum over the rows that count of weight * each.
+ * Where A is 0 the first term is 0.  The gradient is that of r A where it is
+ * the smaller one or equal, and 0 where the ratio is held.
+ *   old_logprobs   device float[rows]: of the policy that picked the tokens.
+ *   advantages     device float[rows]: A.
+ *   weights        device float[rows] or NULL: 1 / rows.  0 marks a row that
+ *                  does not count.  Means over tokens, sequences, micro-batches
+ *                  and ranks are made by these weights.
+ *   ref_logprobs   device float[rows] or NULL: no divergence.
+ *   options        kl without ref_logprobs must be 0.
+ *   grad_loss      as above.
+ *   loss           device float or NULL; logprobs, entropies: device
+ *                  float[rows] or NULL; grad_logits: as above or NULL.  At
+ *                  least one of the four.
+ * Returns as nms_token_logprobs.
+ */
+nms_status nms_policy_loss(const void *logits, nms_dtype dtype, int64_t rows, int64_t vocab,
+                           int64_t row_stride, const int32_t *tokens, const float *old_logprobs,
+                           const float *advantages, const float *weights,
+                           const float *ref_logprobs, const float *temperature,
+                           const nms_policy_options *options, const float *grad_loss, float *loss,
+                           float *logprobs, float *entropies, void *grad_logits,
+                           int64_t grad_stride, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+#define NMS_PREFERENCE_SIGMOID 0
+#define NMS_PREFERENCE_HINGE 1
+#define NMS_PREFERENCE_SQUARED 2
+
+typedef struct nms_preference_options {
+    int kind;        /* NMS_PREFERENCE_* */
+    int average;     /* nonzero: a sequence's log probability is the mean over
+                        its rows that count, not the sum */
+    float beta;      /* finite, > 0 */
+    float smoothing; /* of the sigmoid kind, 0 .. 0.5 */
+    float margin;    /* finite */
+} nms_preference_options;
+
+/*
+ * nms_preference_loss -- the loss of paired log ratios, and its gradient where
+ * grad_logits is given.  Sequence i < pairs is the preferred one of pair i,
+ * sequence pairs + i the other.  With l_q the sum (or mean) of the log
+ * probabilities of sequence q's rows that count,
+ *     h = beta ((l_i - ref_i) - (l_pairs+i - ref_pairs+i)) - margin
+ *     sigmoid  (1 - smoothing) log(1 + exp(-h)) + smoothing log(1 + exp(h))
+ *     hinge    max(0, 1 - h)
+ *     squared  ((h - 1/2) / beta)^2
+ *     loss = sum over pairs of weight * each.
+ *   offsets       device int64[2 * pairs + 1]: sequence q is the rows from
+ *                 offsets[q] to offsets[q + 1], from the largest offset so far
+ *                 where they decrease, within the rows.  Rows of no sequence
+ *                 have gradient 0.
+ *   ref_logprobs  device float[2 * pairs] or NULL: 0.
+ *   weights       device float[pairs] or NULL: 1 / pairs.  A pair of weight 0
+ *                 has no part in the loss, whatever it holds.
+ *   loss          device float; logprobs: device float[2 * pairs], l;
+ *                 margins: device float[pairs], h.
+ *   grad_logits   as above, or NULL: not wanted.
+ *   workspace     nms_loss_workspace_size(rows, vocab, pairs) bytes.
+ * Returns as nms_token_logprobs (NMS_TOO_LARGE: pairs above NMS_MAX_PAIRS).
+ */
+nms_status nms_preference_loss(const void *logits, nms_dtype dtype, int64_t rows, int64_t vocab,
+                               int64_t row_stride, const int32_t *tokens, const int64_t *offsets,
+                               int64_t pairs, const float *ref_logprobs, const float *weights,
+                               const nms_preference_options *options, const float *grad_loss,
+                               float *loss, float *logprobs, float *margins, void *grad_logits,
+                               int64_t grad_stride, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * nms_preference_loss_backward -- the gradient alone, from the margins of the
+ * forward call.
+ */
+nms_status nms_preference_loss_backward(const void *logits, nms_dtype dtype, int64_t rows,
+                                        int64_t vocab, int64_t row_stride, const int32_t *tokens,
+                                        const int64_t *offsets, int64_t pairs,
+                                        const float *weights,
+                                        const nms_preference_options *options,
+                                        const float *margins, const float *grad_loss,
+                                        void *grad_logits, int64_t grad_stride, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+typedef struct nms_balance_options {
+    int score;     /* NMS_ROUTE_SOFTMAX or NMS_ROUTE_SIGMOID, as in the routing */
+    int top_k;     /* places per token in ids, 0 .. NMS_ROUTE_MAX_TOP_K */
+    float balance; /* finite */
+    float z;       /* finite */
+} nms_balance_options;
+
+/*
+ * nms_balance_loss -- the balance loss of routing, the loss on the size of the
+ * logits and the counts they go by, and the gradient where grad_logits is
+ * given.  Over the tokens of sequence q that count (live, in a sequence), n_q
+ * many, with c_qe those that chose expert e, s the softmax of their logits or
+ * their sigmoids divided by the sum of these,
+ *     f_qe = experts c_qe / sum_e c_qe,    P_qe = sum of s_e / n_q
+ *     loss = balance / sequences * sum_q sum_e f_qe P_qe
+ *            + z * the mean over all tokens that count of log(sum exp z)^2.
+ * The counts have no gradient.  A logit of -infinity has score 0; a token with
+ * no other logits has no part in the loss but counts as a token.  NaN in a
+ * token that counts makes the loss NaN, and so does +infinity (of sigmoid
+ * scores with z = 0 it does not).
+ *   logits, dtype, tokens, experts, row_stride  as for nms_route_experts.
+ *   ids        device int32[tokens * top_k], as nms_route_experts gives them
+ *              (one outside 0..experts-1 is an empty place), or NULL: counts
+ *              are given, of all ranks for instance.
+ *   live       device byte[tokens] or NULL: 0 marks a padded row.
+ *   offsets    device int64[sequences + 1]: as for nms_preference_loss; NULL:
+ *              one sequence.
+ *   loss       device float or NULL.
+ *   counts     device int32[sequences * experts]: written (NULL: not wanted),
+ *              or read where ids is NULL (below 0: as 0).
+ *   workspace  device, 256-byte aligned, nms_balance_workspace_size() bytes.
+ * Returns as nms_route_experts, or NMS_WORKSPACE_TOO_SMALL.
+ */
+nms_status nms_balance_loss(const void *logits, nms_dtype dtype, int64_t tokens, int64_t experts,
+                            int64_t row_stride, const int32_t *ids, const uint8_t *live,
+                            const int64_t *offsets, int64_t sequences,
+                            const nms_balance_options *options, const float *grad_loss,
+                            float *loss, int32_t *counts, void *grad_logits, int64_t grad_stride,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * nms_balance_workspace_size -- device workspace needed by nms_balance_loss.
+ * Returns NMS_OK, NMS_INVALID_ARG or NMS_TOO_LARGE.
+ */
+nms_status nms_balance_workspace_size(int64_t tokens, int64_t experts, int64_t sequences,
+                                      int top_k, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
