@@ -19,10 +19,10 @@ namespace {
 
 constexpr float LOG2E = 1.44269504f;
 constexpr int CT = 1024;  // threads that count
-constexpr int MAX_PARTS = 64, PART_IDS = 32768;
+constexpr int MAX_PARTS = 64, PART_IDS = 8192;
 
-// The counts of each part of a sequence and of the whole (as they go into the
-// factors), its tokens, the factors a, the sequence of each token, the terms.
+// The counts of each part of a sequence, the tokens of the parts and of the
+// whole, the sequence of each token, the factors a, the terms.
 struct BalanceSpace {
     int32_t *parts, *part_tokens, *tokens, *owner;
     float *factors;
@@ -46,8 +46,13 @@ int lanes_of(int experts) {
     return experts <= 64 ? 8 : experts <= 128 ? 16 : experts <= 256 ? 32 : 64;
 }
 
+// Tokens that a group of lanes takes in turn, their logits loaded together.
+int turns_of(int64_t tokens, int experts) {
+    return tokens * lanes_of(experts) >= (int64_t)4096 * MT ? 4 : 1;
+}
+
 int64_t blocks_of(int64_t tokens, int experts) {
-    const int64_t per = MT / lanes_of(experts);
+    const int64_t per = (int64_t)MT / lanes_of(experts) * turns_of(tokens, experts);
     return (tokens + per - 1) / per;
 }
 
@@ -75,162 +80,152 @@ size_t lay_out(int64_t tokens, int experts, int64_t sequences, int top_k, void *
     return n;
 }
 
-__device__ __forceinline__ int block_total(int v, int *shared) {
-    v = wave_sum(v);
+// -------------------------------------------------------- counts and factors
+
+// Two sums over the workgroup, the same in every thread.  (Counts that are
+// given may add up to more than 31 bits.)
+struct Totals {
+    int tokens;
+    double counts;
+};
+__device__ __forceinline__ Totals totals_of(int tokens, int count, Totals *shared) {
+    Totals t = {wave_sum(tokens), wave_sum((double)count)};
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = t;
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int sum = 0;
-    for (int q = 0; q < (int)blockDim.x / 64; ++q) sum += shared[q];
-    return sum;
+    t = {0, 0.0};
+    for (int q = 0; q < CT / 64; ++q) {
+        t.tokens += shared[q].tokens;
+        t.counts += shared[q].counts;
+    }
+    return t;
 }
 
-// Where a sequence starts: the largest offset up to its own, within the
-// tokens, so that the sequences never overlap.
-__device__ __forceinline__ int start_of(const BalanceArgs &a, int64_t q, int *shared) {
-    if (a.offsets == nullptr) return q == 0 ? 0 : (int)a.tokens;
+// Where sequence q starts and ends: the largest offset up to its own, within
+// the tokens, so that the sequences never overlap.
+__device__ __forceinline__ void bounds_of(const BalanceArgs &a, int64_t q, int *shared, int &begin,
+                                          int &end) {
+    begin = 0;
+    end = (int)a.tokens;
+    if (a.offsets == nullptr) return;
+    const int64_t next = a.offsets[q + 1];
     int64_t top = 0;
-    for (int64_t i = threadIdx.x; i <= q; i += blockDim.x) top = max(top, a.offsets[i]);
-    int v = wave_max((int)min(top, a.tokens));
-    __syncthreads();
+    for (int64_t i = threadIdx.x; i <= q; i += CT) top = max(top, a.offsets[i]);
+    const int v = wave_max((int)min(top, a.tokens));
     if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
     __syncthreads();
-    for (int w = 0; w < (int)blockDim.x / 64; ++w) v = max(v, shared[w]);
-    return v;
+    for (int w = 0; w < CT / 64; ++w) begin = max(begin, shared[w]);
+    end = max(begin, (int)min(max(next, (int64_t)0), a.tokens));
 }
 
-// a_qe of the thread's expert from its count, whose sum over the experts all
-// threads know.
-__device__ __forceinline__ void write_factor(const BalanceArgs &a, const BalanceSpace &s, int64_t q,
-                                             int count, int64_t all, int tokens) {
+// Adds the experts of the tokens from `from` to `to` to the counts in LDS, a
+// thread per token; returns how many of these count.
+__device__ __forceinline__ int count_tokens(const BalanceArgs &a, int from, int to, int q,
+                                            int32_t *owner, int *hist) {
+    int used = 0;
+    for (int t = from + (int)threadIdx.x; t < to; t += CT) {
+        const bool live = a.live == nullptr || a.live[t] != 0;
+        used += live;
+        if (owner) owner[t] = live ? q : -1;
+        if (!live || a.ids == nullptr) continue;
+        const int32_t *ids = a.ids + (int64_t)t * a.top_k;
+        for (int i = 0; i < a.top_k; i += 4) {
+            int id[4] = {-1, -1, -1, -1};
+            if (i + 4 <= a.top_k) {
+                __builtin_memcpy(id, ids + i, sizeof(id));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (i + j < a.top_k) id[j] = ids[i + j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if ((unsigned)id[j] < (unsigned)a.experts) atomicAdd(&hist[id[j]], 1);
+        }
+    }
+    return used;
+}
+
+// a_qe from an expert's count.
+__device__ __forceinline__ float factor_of(const BalanceArgs &a, int count, const Totals &t) {
+    const double per = (double)a.sequences * (double)t.tokens * t.counts;
+    return per > 0.0 ? (float)((double)a.balance * a.experts * (double)count / per) : 0.0f;
+}
+
+__device__ __forceinline__ void write_sequence(const BalanceArgs &a, const BalanceSpace &s,
+                                               int64_t q, int count, const Totals &t) {
     const int e = threadIdx.x;
-    if (e >= a.experts) return;
-    const double per = (double)a.sequences * (double)tokens * (double)all;
-    s.factors[q * a.experts + e] =
-        all > 0 && tokens > 0 ? (float)((double)a.balance * a.experts * (double)count / per) : 0.0f;
-}
-
-// The sum of counts that are given may pass 31 bits.
-__device__ __forceinline__ int64_t block_total64(int64_t v, double *shared) {
-    double d = wave_sum((double)v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = d;
-    __syncthreads();
-    d = 0.0;
-    for (int q = 0; q < (int)blockDim.x / 64; ++q) d += shared[q];
-    return (int64_t)d;
+    if (e == 0) s.tokens[q] = t.tokens;
+    if (e < a.experts) s.factors[q * a.experts + e] = factor_of(a, count, t);
 }
 
 // A workgroup per (sequence, part): the part's counts and tokens, and which
 // sequence its tokens are of.  Alone, it writes the sequence's factors too.
 __global__ __launch_bounds__(CT) void count_kernel(BalanceArgs a, BalanceSpace s, int parts) {
     __shared__ int hist[NMS_ROUTE_MAX_EXPERTS];
-    __shared__ int shared[CT / 64];
-    __shared__ double wide[CT / 64];
+    __shared__ int places[CT / 64];
+    __shared__ Totals sums[CT / 64];
     const int64_t q = blockIdx.x;
     const int part = blockIdx.y, tid = threadIdx.x;
     hist[tid] = 0;
-    const int begin = start_of(a, q, shared), end = start_of(a, q + 1, shared);
+    int begin, end;
+    bounds_of(a, q, places, begin, end);
     __syncthreads();
     const int size = (end - begin + parts - 1) / parts;
     const int from = min(begin + part * size, end), to = min(from + size, end);
-    int used = 0;
-    for (int t = from + tid; t < to; t += CT) {
-        const bool live = a.live == nullptr || a.live[t] != 0;
-        used += live;
-        s.owner[t] = live ? (int)q : -1;
-    }
+    const int used = count_tokens(a, from, to, (int)q, s.owner, hist);
     // the tokens of no sequence
     if (q == 0 && part == 0)
         for (int t = tid; t < begin; t += CT) s.owner[t] = -1;
     if (q == a.sequences - 1 && part == 0)
         for (int64_t t = end + tid; t < a.tokens; t += CT) s.owner[t] = -1;
-    if (a.ids) {
-        const int64_t last = (int64_t)to * a.top_k;
-        for (int64_t i = (int64_t)from * a.top_k + tid; i < last; i += CT) {
-            const int id = a.ids[i];
-            if ((unsigned)id < (unsigned)a.experts &&
-                (a.live == nullptr || a.live[i / a.top_k] != 0))
-                atomicAdd(&hist[id], 1);
-        }
-    }
-    const int tokens = block_total(used, shared);
     __syncthreads();
-    if (parts > 1) {
-        if (tid < a.experts && a.ids)
-            s.parts[((int64_t)q * parts + part) * a.experts + tid] = hist[tid];
-        if (tid == 0) s.part_tokens[q * parts + part] = tokens;
-        return;
-    }
     int count = 0;
     if (tid < a.experts) {
-        count = a.ids ? hist[tid] : max(a.counts[q * a.experts + tid], 0);
-        if (a.ids && a.counts) a.counts[q * a.experts + tid] = count;
+        if (a.ids) count = hist[tid];
+        else if (parts == 1) count = max(a.counts[q * a.experts + tid], 0);
     }
-    write_factor(a, s, q, count, block_total64(count, wide), tokens);
-    if (tid == 0) s.tokens[q] = tokens;
+    const Totals t = totals_of(used, count, sums);
+    if (parts > 1) {
+        if (tid < a.experts && a.ids) s.parts[(q * parts + part) * a.experts + tid] = count;
+        if (tid == 0) s.part_tokens[q * parts + part] = t.tokens;
+        return;
+    }
+    if (tid < a.experts && a.ids && a.counts) a.counts[q * a.experts + tid] = count;
+    write_sequence(a, s, q, count, t);
 }
 
 // A workgroup per sequence: its counts and factors from those of its parts.
 __global__ __launch_bounds__(CT) void join_kernel(BalanceArgs a, BalanceSpace s, int parts) {
-    __shared__ double wide[CT / 64];
+    __shared__ Totals sums[CT / 64];
     const int64_t q = blockIdx.x;
     const int tid = threadIdx.x;
-    int tokens = 0, count = 0;
-    for (int p = 0; p < parts; ++p) tokens += s.part_tokens[q * parts + p];
+    int count = 0;
     if (tid < a.experts) {
         if (a.ids) {
+#pragma unroll 8
             for (int p = 0; p < parts; ++p) count += s.parts[(q * parts + p) * a.experts + tid];
             if (a.counts) a.counts[q * a.experts + tid] = count;
         } else {
             count = max(a.counts[q * a.experts + tid], 0);
         }
     }
-    write_factor(a, s, q, count, block_total64(count, wide), tokens);
-    if (tid == 0) s.tokens[q] = tokens;
+    write_sequence(a, s, q, count,
+                   totals_of(tid < parts ? s.part_tokens[q * parts + tid] : 0, count, sums));
 }
 
-// LANES lanes per token, VALUES experts each.
-template <typename T, int LANES, int VALUES>
-__global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace s) {
-    __shared__ double shared[MT / 64];
-    constexpr int TOKENS = MT / LANES;
-    const int sub = threadIdx.x % LANES, E = a.experts, e0 = sub * VALUES;
-    const int64_t t = (int64_t)blockIdx.x * TOKENS + threadIdx.x / LANES;
-    const bool inside = t < a.tokens;
-    const int owner = inside ? s.owner[t] : -1;
-    const bool softmax = a.score == NMS_ROUTE_SOFTMAX;
-    float per = 0.0f;  // z / N
-    if (a.z != 0.0f) {
-        int64_t all = 0;
-        for (int64_t q = threadIdx.x & 63; q < a.sequences; q += 64) all += s.tokens[q];
-        const double n = wave_sum((double)all);
-        per = n > 0.0 ? (float)((double)a.z / n) : 0.0f;
-    }
-    float z[VALUES], f[VALUES];
-#pragma unroll
-    for (int j = 0; j < VALUES; ++j) {
-        z[j] = NEG_INF;
-        f[j] = 0.0f;
-    }
-    if (owner >= 0) {
-        const T *row = static_cast<const T *>(a.logits) + t * a.row_stride + e0;
-        const float *from = s.factors + (int64_t)owner * E + e0;
-        if (e0 + VALUES <= E) {
-            T raw[VALUES];
-            __builtin_memcpy(raw, row, sizeof(raw));
-            __builtin_memcpy(f, from, sizeof(f));
-#pragma unroll
-            for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < VALUES; ++j)
-                if (e0 + j < E) {
-                    z[j] = to_f32(row[j]);
-                    f[j] = from[j];
-                }
-        }
-    }
+// ------------------------------------------------------- loss and gradient
+
+// z / N, for the number N of tokens that count.
+__device__ __forceinline__ float share_of(float z, double n) {
+    return n > 0.0 ? (float)((double)z / n) : 0.0f;
+}
+
+// A token's part of the loss and its gradient (in place of its logits) on LANES
+// lanes, VALUES experts each: z its logits (-infinity past the last), f its
+// sequence's factors, per: z / N.
+template <int LANES, int VALUES>
+__device__ __forceinline__ float token_loss(float (&z)[VALUES], const float (&f)[VALUES],
+                                            bool softmax, float per) {
     float top = NEG_INF;
 #pragma unroll
     for (int j = 0; j < VALUES; ++j) top = fmaxf(top, z[j]);
@@ -246,13 +241,13 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
         sum = all_sum<LANES>(sum);
     }
     const float inverse = sum != 0.0f ? 1.0f / sum : 0.0f;
-    float d[VALUES], inner = 0.0f;
+    float inner = 0.0f;
     if (softmax) {
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) inner += f[j] * x[j];
         inner = all_sum<LANES>(inner) * inverse;
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) d[j] = x[j] * inverse * (f[j] - inner);
+        for (int j = 0; j < VALUES; ++j) z[j] = x[j] * inverse * (f[j] - inner);
     } else {
         // shares of the scores' sum, each score divided by exp(m) first,
         // m = min(largest logit, 0): below -88 a score itself is under
@@ -261,49 +256,118 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
         float total = 0.0f, rest[VALUES];  // rest: 1 - score
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) {
-            // one exponential of what is not above 0
             const float low = __builtin_amdgcn_exp2f(-fabsf(z[j]) * LOG2E);
             const float part = 1.0f / (1.0f + low);
             const bool up = z[j] > 0.0f;
             rest[j] = up ? low * part : part;
-            const float score =
-                up ? part : __builtin_amdgcn_exp2f((z[j] - m) * LOG2E) * part;
-            d[j] = z[j] == z[j] ? score : z[j];
-            total += d[j];
+            const float score = up ? part : __builtin_amdgcn_exp2f((z[j] - m) * LOG2E) * part;
+            z[j] = z[j] == z[j] ? score : z[j];
+            total += z[j];
         }
         total = all_sum<LANES>(total);
         const float under = total != 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) inner += f[j] * d[j];
+        for (int j = 0; j < VALUES; ++j) inner += f[j] * z[j];
         inner = all_sum<LANES>(inner) * under;
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) d[j] = d[j] * under * rest[j] * (f[j] - inner);
+        for (int j = 0; j < VALUES; ++j) z[j] = z[j] * under * rest[j] * (f[j] - inner);
     }
-    float term = inner;
     if (per != 0.0f && sum != 0.0f) {
         const float lse = base + logf(sum);
-        term += per * lse * lse;
         const float more = 2.0f * per * lse * inverse;
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) d[j] += more * x[j];
+        for (int j = 0; j < VALUES; ++j) z[j] += more * x[j];
+        inner += per * lse * lse;
     }
-    if (a.grad_logits && inside) {
-        const float up = a.grad_loss ? a.grad_loss[0] : 1.0f;
-        T out[VALUES];
+    return inner;
+}
+
+template <typename T, int VALUES>
+struct Raw {
+    T v[VALUES];
+};
+
+template <typename T, int VALUES>
+__device__ __forceinline__ Raw<T, VALUES> load_raw(const T *row, int left, bool there) {
+    Raw<T, VALUES> r;
+    if (there && left >= VALUES) {
+        __builtin_memcpy(&r, row, sizeof(r));
+    } else {
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) out[j] = from_f32<T>(owner >= 0 ? d[j] * up : 0.0f);
-        T *to = static_cast<T *>(a.grad_logits) + t * a.grad_stride + e0;
-        if (e0 + VALUES <= E) {
-            __builtin_memcpy(to, out, sizeof(out));
-        } else {
+        for (int j = 0; j < VALUES; ++j) r.v[j] = there && j < left ? row[j] : from_f32<T>(NEG_INF);
+    }
+    return r;
+}
+
+template <typename T, int VALUES>
+__device__ __forceinline__ void store_gradient(T *to, int left, const float (&d)[VALUES], float up) {
+    T out[VALUES];
 #pragma unroll
-            for (int j = 0; j < VALUES; ++j)
-                if (e0 + j < E) to[j] = out[j];
+    for (int j = 0; j < VALUES; ++j) out[j] = from_f32<T>(d[j] * up);
+    if (left >= VALUES) {
+        __builtin_memcpy(to, out, sizeof(out));
+    } else {
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j)
+            if (j < left) to[j] = out[j];
+    }
+}
+
+// LANES lanes per token, VALUES experts each, TURNS tokens one after another.
+template <typename T, int LANES, int VALUES, int TURNS>
+__global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace s) {
+    __shared__ double shared[MT / 64];
+    constexpr int GROUPS = MT / LANES;
+    const int sub = threadIdx.x % LANES, E = a.experts, e0 = sub * VALUES, left = E - e0;
+    const int64_t first = (int64_t)blockIdx.x * (GROUPS * TURNS) + threadIdx.x / LANES;
+    const T *logits = static_cast<const T *>(a.logits) + e0;
+    T *out = static_cast<T *>(a.grad_logits) + e0;
+    int owner[TURNS];
+    Raw<T, VALUES> raw[TURNS];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int64_t t = first + i * GROUPS;
+        owner[i] = t < a.tokens ? s.owner[t] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int64_t t = first + i * GROUPS;
+        raw[i] = load_raw<T, VALUES>(logits + t * a.row_stride, left, owner[i] >= 0);
+    }
+    float per = 0.0f;
+    if (a.z != 0.0f) {
+        int64_t all = 0;
+        for (int64_t q = threadIdx.x & 63; q < a.sequences; q += 64) all += s.tokens[q];
+        per = share_of(a.z, wave_sum((double)all));
+    }
+    const float up = a.grad_loss ? a.grad_loss[0] : 1.0f;
+    double term = 0.0;
+    float f[VALUES];
+    int held = -1;
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int64_t t = first + i * GROUPS;
+        if (i == 0 || owner[i] != held) {
+            const float *from = s.factors + (int64_t)max(owner[i], 0) * E + e0;
+            if (left >= VALUES) {
+                __builtin_memcpy(f, from, sizeof(f));
+            } else {
+#pragma unroll
+                for (int j = 0; j < VALUES; ++j) f[j] = j < left ? from[j] : 0.0f;
+            }
+            held = owner[i];
         }
+        float z[VALUES];
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw[i].v[j]);
+        const float mine = token_loss<LANES, VALUES>(z, f, a.score == NMS_ROUTE_SOFTMAX, per);
+        if (sub == 0) term += (double)mine;
+        if (a.grad_logits && t < a.tokens)
+            store_gradient<T, VALUES>(out + t * a.grad_stride, left, z, owner[i] >= 0 ? up : 0.0f);
     }
     if (a.loss == nullptr) return;
-    const double mine = wave_sum(sub == 0 && owner >= 0 ? (double)term : 0.0);
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = mine;
+    term = wave_sum(term);
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = term;
     __syncthreads();
     if (threadIdx.x == 0) {
         double all = 0.0;
@@ -313,15 +377,83 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
     }
 }
 
-template <typename T>
-void run(const BalanceArgs &a, const BalanceSpace &s, hipStream_t stream) {
+// All of a small call in one workgroup.
+template <typename T, int LANES, int VALUES>
+__global__ __launch_bounds__(CT) void small_kernel(BalanceArgs a) {
+    __shared__ int hist[NMS_ROUTE_MAX_EXPERTS];
+    __shared__ int places[CT / 64];
+    __shared__ Totals sums[CT / 64];
+    __shared__ float factors[NMS_ROUTE_MAX_EXPERTS];
+    __shared__ double shared[CT / 64];
+    constexpr int GROUPS = CT / LANES;
+    const int tid = threadIdx.x, sub = tid % LANES, E = a.experts, e0 = sub * VALUES, left = E - e0;
+    hist[tid] = 0;
+    int begin, end;
+    bounds_of(a, 0, places, begin, end);
+    __syncthreads();
+    const int used = count_tokens(a, begin, end, 0, nullptr, hist);
+    __syncthreads();
+    const int count = tid >= E ? 0 : a.ids ? hist[tid] : max(a.counts[tid], 0);
+    const Totals sum = totals_of(used, count, sums);
+    if (tid < E && a.ids && a.counts) a.counts[tid] = count;
+    factors[tid] = tid < E ? factor_of(a, count, sum) : 0.0f;
+    __syncthreads();
+    const float per = a.z != 0.0f ? share_of(a.z, (double)sum.tokens) : 0.0f;
+    const float up = a.grad_loss ? a.grad_loss[0] : 1.0f;
+    float f[VALUES];
+#pragma unroll
+    for (int j = 0; j < VALUES; ++j) f[j] = j < left ? factors[e0 + j] : 0.0f;
+    double term = 0.0;
+    for (int from = 0; from < (int)a.tokens; from += GROUPS) {
+        const int t = from + tid / LANES;
+        const bool counts = t >= begin && t < end && (a.live == nullptr || a.live[t] != 0);
+        const Raw<T, VALUES> raw = load_raw<T, VALUES>(
+            static_cast<const T *>(a.logits) + t * a.row_stride + e0, left, counts);
+        float z[VALUES];
+#pragma unroll
+        for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw.v[j]);
+        const float mine = token_loss<LANES, VALUES>(z, f, a.score == NMS_ROUTE_SOFTMAX, per);
+        if (sub == 0) term += (double)mine;
+        if (a.grad_logits && t < a.tokens)
+            store_gradient<T, VALUES>(static_cast<T *>(a.grad_logits) + t * a.grad_stride + e0,
+                                      left, z, counts ? up : 0.0f);
+    }
+    term = wave_sum(term);
+    if ((tid & 63) == 0) shared[tid >> 6] = term;
+    __syncthreads();
+    if (tid == 0 && a.loss) {
+        double all = 0.0;
+        for (int q = 0; q < CT / 64; ++q) all += shared[q];
+        a.loss[0] = (float)all;
+    }
+}
+
+// ----------------------------------------------------------------- launches
+
+template <typename T, int LANES, int VALUES>
+void launch(const BalanceArgs &a, const BalanceSpace &s, bool small, hipStream_t stream) {
     const unsigned n = (unsigned)s.blocks;
+    if (small) small_kernel<T, LANES, VALUES><<<1, CT, 0, stream>>>(a);
+    else if (turns_of(a.tokens, a.experts) == 1)
+        balance_kernel<T, LANES, VALUES, 1><<<n, MT, 0, stream>>>(a, s);
+    else
+        balance_kernel<T, LANES, VALUES, 4><<<n, MT, 0, stream>>>(a, s);
+}
+
+template <typename T>
+void run(const BalanceArgs &a, const BalanceSpace &s, bool small, hipStream_t stream) {
     const int E = a.experts;
-    if (E <= 64) balance_kernel<T, 8, 8><<<n, MT, 0, stream>>>(a, s);
-    else if (E <= 128) balance_kernel<T, 16, 8><<<n, MT, 0, stream>>>(a, s);
-    else if (E <= 256) balance_kernel<T, 32, 8><<<n, MT, 0, stream>>>(a, s);
-    else if (E <= 512) balance_kernel<T, 64, 8><<<n, MT, 0, stream>>>(a, s);
-    else balance_kernel<T, 64, 16><<<n, MT, 0, stream>>>(a, s);
+    if (E <= 64) launch<T, 8, 8>(a, s, small, stream);
+    else if (E <= 128) launch<T, 16, 8>(a, s, small, stream);
+    else if (E <= 256) launch<T, 32, 8>(a, s, small, stream);
+    else if (E <= 512) launch<T, 64, 8>(a, s, small, stream);
+    else launch<T, 64, 16>(a, s, small, stream);
+}
+
+void run(const BalanceArgs &a, const BalanceSpace &s, bool small, hipStream_t stream) {
+    if (a.dtype == NMS_F32) run<float>(a, s, small, stream);
+    else if (a.dtype == NMS_F16) run<half_t>(a, s, small, stream);
+    else run<bf16_t>(a, s, small, stream);
 }
 
 }  // namespace
@@ -333,14 +465,14 @@ size_t balance_workspace_bytes(int64_t tokens, int experts, int64_t sequences, i
 hipError_t launch_balance(const BalanceArgs &a, hipStream_t stream) {
     BalanceSpace s;
     lay_out(a.tokens, a.experts, a.sequences, a.top_k, a.workspace, &s);
+    if (a.sequences == 1 && a.tokens * lanes_of(a.experts) <= 4 * CT) {
+        run(a, s, true, stream);
+        return hipGetLastError();
+    }
     const int parts = parts_of(a.tokens, a.sequences, a.top_k);
     count_kernel<<<dim3((unsigned)a.sequences, (unsigned)parts), CT, 0, stream>>>(a, s, parts);
     if (parts > 1) join_kernel<<<(unsigned)a.sequences, CT, 0, stream>>>(a, s, parts);
-    if (a.tokens > 0 && (a.loss || a.grad_logits)) {
-        if (a.dtype == NMS_F32) run<float>(a, s, stream);
-        else if (a.dtype == NMS_F16) run<half_t>(a, s, stream);
-        else run<bf16_t>(a, s, stream);
-    }
+    if (a.tokens > 0 && (a.loss || a.grad_logits)) run(a, s, false, stream);
     if (a.loss) launch_total(s.terms, a.tokens > 0 ? s.blocks : 0, a.loss, stream);
     return hipGetLastError();
 }

@@ -17,116 +17,325 @@
 namespace gnms {
 namespace {
 
-constexpr float LOG2E = 1.44269504f;
 constexpr double LN2 = 0.693147180559945309;
 
 // -------------------------------------------------------------------- rows
 
-// A slice's largest logit, sum of exponentials and weighted sum.  m may be
-// -infinity (no logit above it); then s and w are 0, or NaN where one was NaN.
+// The largest logit m of a part of a row, the sum s of the exponentials and the
+// weighted sum w.  m may be -infinity (no logit above it); then s and w are 0,
+// or NaN where one was NaN.  The sums of 32 exponentials at a time are added up
+// in binary64: in float32 the thread with the row's largest logit, 1 of the
+// sum, lost 2^-24 of the log probability with each of its other sums.
 // at: the logit of the row's token, which a gradient in place of the logits
 // overwrites.
 struct Part {
-    float m, s, w, at;
+    double s, w;
+    float m, at;
 };
 
-// Sixteen bytes of neighbouring elements.
+// Sixteen bytes of neighbouring elements, as words: as elements of 16 bits they
+// would take a register each.
 template <typename T>
 struct Pack {
     static constexpr int N = 16 / sizeof(T);
-    T v[N];
+    uint32_t w[4];
 };
 
-template <typename T>
-__device__ __forceinline__ Pack<T> load_pack(const T *p, int left) {
-    Pack<T> e;
-    if (left >= Pack<T>::N) {
-        __builtin_memcpy(&e, p, sizeof(e));
-    } else {
+__device__ __forceinline__ float element(const Pack<float> &e, int j) {
+    return __uint_as_float(e.w[j]);
+}
+__device__ __forceinline__ float element(const Pack<bf16_t> &e, int j) {
+    const uint32_t w = e.w[j / 2];
+    return __uint_as_float(j % 2 ? w & 0xffff0000u : w << 16);
+}
+__device__ __forceinline__ float element(const Pack<half_t> &e, int j) {
+    const uint32_t w = e.w[j / 2];
+    return (float)__builtin_bit_cast(half_t, (uint16_t)(j % 2 ? w >> 16 : w));
+}
+
+__device__ __forceinline__ void set_elements(Pack<float> &e, const float *v) {
 #pragma unroll
-        for (int j = 0; j < Pack<T>::N; ++j) e.v[j] = j < left ? p[j] : from_f32<T>(NEG_INF);
-    }
-    return e;
+    for (int j = 0; j < 4; ++j) e.w[j] = __float_as_uint(v[j]);
+}
+template <typename T>
+__device__ __forceinline__ void set_elements(Pack<T> &e, const float *v) {
+    typedef T Two __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        e.w[j] = __builtin_bit_cast(uint32_t, (Two){(T)v[2 * j], (T)v[2 * j + 1]});
 }
 
-// What a row's logits are multiplied by, and 1 / t.  A temperature of 0 or
-// below (or NaN) stands for 1; one beyond what its inverse holds takes the
-// largest or smallest that float32 has, so that the largest logit keeps 2^0
-// and -infinity stays out.
-__device__ __forceinline__ void temperature_of(const LossRows &r, int64_t row, float &k,
-                                               float &inverse) {
+typedef uint32_t Words __attribute__((ext_vector_type(4), may_alias));
+typedef uint32_t LooseWords __attribute__((ext_vector_type(4), aligned(2), may_alias));
+
+// The pack at an aligned address, or one of -infinity.
+template <typename T>
+__device__ __forceinline__ Pack<T> load_pack(const T *p, bool there) {
+    const uint32_t none = sizeof(T) == 4 ? 0xff800000u
+                          : __is_same(T, half_t) ? 0xfc00fc00u : 0xff80ff80u;
+    Words w = {none, none, none, none};
+    if (there) w = *reinterpret_cast<const Words *>(p);
+    return {{w.x, w.y, w.z, w.w}};
+}
+
+// To any element's address.  stream: the pack is not kept in the caches, where
+// it would take the place of logits that are still to be read.
+template <typename T>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T> &e, bool stream) {
+    const LooseWords w = {e.w[0], e.w[1], e.w[2], e.w[3]};
+    if (stream) __builtin_nontemporal_store(w, reinterpret_cast<LooseWords *>(p));
+    else *reinterpret_cast<LooseWords *>(p) = w;
+}
+
+// log2(e) / t as a sum, whose second term keeps sums over many rows unbiased
+// (the first alone is off by up to 2^-25 of u, in one direction for all rows),
+// and 1 / t.  The second term is above 0, so that -infinity times it is
+// -infinity.
+struct Scale {
+    float hi, lo, inverse;
+};
+
+// A temperature of 0 or below (or NaN) stands for 1; one beyond what its
+// inverse holds takes the largest or smallest that float32 has, so that the
+// largest logit keeps 2^0 and -infinity stays out.
+__device__ __forceinline__ Scale scale_of(const LossRows &r, int64_t row) {
+    constexpr double LOG2E = 1.4426950408889634;
+    constexpr float ONE = 1.44269502f, REST = (float)(LOG2E - (double)ONE);
+    static_assert((double)ONE < LOG2E, "the rest is above 0");
     float t = r.temperature ? r.temperature[row] : 1.0f;
-    if (!(t > 0.0f)) t = 1.0f;
-    k = fminf(fmaxf(LOG2E / t, 1.4012985e-45f), 3.4028235e38f);
-    inverse = fminf(1.0f / t, 3.4028235e38f);
+    if (!(t > 0.0f) || t == 1.0f) return {ONE, REST, 1.0f};
+    constexpr float LEAST = 1.4012985e-45f, MOST = 3.4028235e38f;
+    const double k = LOG2E / (double)t;
+    float hi = fminf(fmaxf((float)k, LEAST), MOST);
+    // the next float below where it was rounded up
+    if ((double)hi > k && hi > LEAST) hi = __uint_as_float(__float_as_uint(hi) - 1u);
+    float lo = fmaxf((float)(k - (double)hi), LEAST);
+    if (hi == MOST) lo = LEAST;
+    return {hi, lo, fminf(1.0f / t, MOST)};
 }
 
-__device__ __forceinline__ bool counts_for(const LossRows &r, int64_t row, int &token) {
-    token = r.tokens[row];
-    return (unsigned)token < (unsigned)r.vocab && (!r.weights || r.weights[row] != 0.0f);
-}
+// A row's logits: a body of whole packs at aligned addresses, and the elements
+// before and behind it, fewer than two packs, which threads take one each.  (Packs
+// at odd elements of 16 bits took 20 % longer: 4096 x 131073 float16 255 us for
+// 211 read, 541 for 440 read and written; and branches for a pack that is not
+// whole, at each pack that a thread holds, made code of 45 KB and 10 us a call.)
+template <typename T>
+struct Row {
+    const T *z;       // the body
+    int size;         // of the body
+    int head, edges;  // elements before it; before and behind it
+    int token;        // its place from the body on
+    __device__ __forceinline__ Row(const LossRows &r, int64_t row, int of) {
+        constexpr int N = Pack<T>::N;
+        z = static_cast<const T *>(r.logits) + row * r.row_stride;
+        const int past = (int)(reinterpret_cast<uintptr_t>(z) & 15) / (int)sizeof(T);
+        head = min((N - past) & (N - 1), r.vocab);
+        z += head;
+        size = (r.vocab - head) & ~(N - 1);
+        edges = r.vocab - size;
+        token = of - head;
+    }
+    __device__ __forceinline__ float at_token() const { return to_f32(z[token]); }
+    __device__ __forceinline__ int edge(int j) const { return j < head ? j - head : size + j - head; }
+    // the part of the thread's element at the edges, or an empty one
+    __device__ __forceinline__ Part first(bool mine) const {
+        Part p = {0.0, 0.0, NEG_INF, 0.0f};
+        if (mine && (int)threadIdx.x < edges) {
+            const float v = to_f32(z[edge(threadIdx.x)]);
+            if (v != NEG_INF) p.s = 1.0 + (double)(v - v);  // NaN of NaN and infinity
+            if (v == v) p.m = v;
+        }
+        return p;
+    }
+};
 
 // The difference to a largest logit that may be -infinity.
 __device__ __forceinline__ float base_of(float m) { return m == NEG_INF ? 0.0f : m; }
 
 __device__ __forceinline__ float exp2_of(float u) { return __builtin_amdgcn_exp2f(u); }
 
+// The maximum of three in one instruction, without quietening them first.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
+
+// The natural logarithm of a sum that is 0, NaN or from 2^-100 to 2^100: with
+// s = 2^n v, v from sqrt(1/2) to sqrt(2) and f = (v - 1) / (v + 1), n ln 2 +
+// 2 (f + f^3 / 3 + ... + f^15 / 15); the remainder is below 2 f^17 / 17 =
+// 1.2e-14.  The library's takes three times the instructions for the last bits,
+// which show where rows are short.
+__device__ __forceinline__ double inverse_of(double v) {
+    const double y = __builtin_amdgcn_rcp(v);
+    const double z = y * __builtin_fma(-v, y, 2.0);
+    return z * __builtin_fma(-v, z, 2.0);
+}
+__device__ __forceinline__ double log_of(double s) {
+    const int n = __builtin_amdgcn_frexp_exp(s);
+    const double half = __builtin_amdgcn_frexp_mant(s);  // 1/2 .. 1
+    const bool low = half < 0.70710678118654752;
+    const double v = low ? half + half : half;
+    const double f = (v - 1.0) * inverse_of(v + 1.0), g = f * f;
+    double p = 2.0 / 15;
+    p = __builtin_fma(p, g, 2.0 / 13);
+    p = __builtin_fma(p, g, 2.0 / 11);
+    p = __builtin_fma(p, g, 2.0 / 9);
+    p = __builtin_fma(p, g, 2.0 / 7);
+    p = __builtin_fma(p, g, 2.0 / 5);
+    p = __builtin_fma(p, g, 2.0 / 3);
+    p = __builtin_fma(p, g, 2.0);
+    const double y = __builtin_fma((double)(low ? n - 1 : n), LN2, f * p);
+    return s > 0.0 ? y : s == 0.0 ? (double)NEG_INF : s;
+}
+
 // u as a factor of an exponential that is 0 from -150 down
 __device__ __forceinline__ float factor(float u) { return fmaxf(u, -200.0f); }
 
-// p becomes that of the logits of p and q.
-template <bool ENTROPY>
-__device__ __forceinline__ void join(Part &p, float m, float s, float w, float k) {
-    const float top = fmaxf(p.m, m);
-    const float a = p.m == NEG_INF ? 0.0f : (p.m - top) * k, b = m == NEG_INF ? 0.0f : (m - top) * k;
-    const float fa = exp2_of(a), fb = exp2_of(b);
-    if (ENTROPY) p.w = (p.w + factor(a) * p.s) * fa + (w + factor(b) * s) * fb;
-    p.s = p.s * fa + s * fb;
+// What a part's sums are multiplied by, and w's are shifted by, when its
+// largest logit becomes top.
+struct Shift {
+    double by;
+    float u;
+};
+__device__ __forceinline__ Shift shift_to(float m, float top, float k) {
+    const float u = m == NEG_INF ? 0.0f : (m - top) * k;
+    return {(double)exp2_of(u), factor(u)};
+}
+
+// The sum of K values by halves.
+template <int K>
+__device__ __forceinline__ float sum_of(const float *v) {
+    float x[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) x[j] = v[j];
+#pragma unroll
+    for (int h = K / 2; h > 0; h /= 2)
+#pragma unroll
+        for (int j = 0; j < h; ++j) x[j] += x[j + h];
+    return x[0];
+}
+
+// A thread's next K packs.
+template <typename T, bool ENTROPY, int K>
+__device__ __forceinline__ void add_packs(Part &p, const Pack<T> *e, const Scale &k) {
+    constexpr int N = Pack<T>::N;
+    float top = p.m;
+#pragma unroll
+    for (int q = 0; q < K; ++q)
+#pragma unroll
+        for (int j = 0; j < N; j += 2) top = max3(top, element(e[q], j), element(e[q], j + 1));
+    const float base = base_of(top);
+    const Shift f = shift_to(p.m, base, k.hi);
+    float s[K], w[K];
+#pragma unroll
+    for (int q = 0; q < K; ++q) {
+        float x[N], y[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float d = element(e[q], j) - base;
+            const float u = fmaf(d, k.hi, d * k.lo);
+            x[j] = exp2_of(u);
+            if (ENTROPY) y[j] = factor(u) * x[j];
+        }
+        s[q] = sum_of<N>(x);
+        if (ENTROPY) w[q] = sum_of<N>(y);
+    }
+    if (ENTROPY) p.w = (p.w + (double)f.u * p.s) * f.by + (double)sum_of<K>(w);
+    p.s = p.s * f.by + (double)sum_of<K>(s);
     p.m = top;
 }
 
 // The join over the wave's lanes, the same in all of them.
 template <bool ENTROPY>
-__device__ __forceinline__ Part join_wave(Part p, float k) {
+__device__ __forceinline__ Part join_wave(Part p, const Scale &k) {
     const float top = wave_max(p.m);
-    const float d = p.m == NEG_INF ? 0.0f : (p.m - top) * k;
-    const float f = exp2_of(d);
-    if (ENTROPY) p.w = wave_sum((p.w + factor(d) * p.s) * f);
-    p.s = wave_sum(p.s * f);
+    const Shift f = shift_to(p.m, top, k.hi);
+    if (ENTROPY) p.w = wave_sum((p.w + (double)f.u * p.s) * f.by);
+    p.s = wave_sum(p.s * f.by);
     p.m = top;
     return p;
 }
 
+// The join over a workgroup of WAVES waves, the same in every lane.
+template <bool ENTROPY, int WAVES>
+__device__ __forceinline__ Part join_group(Part p, const Scale &k, Part *shared) {
+    p = join_wave<ENTROPY>(p, k);
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = p;
+    __syncthreads();
+    const int lane = threadIdx.x & 63;
+    p = {0.0, 0.0, NEG_INF, 0.0f};
+    if (lane < WAVES) p = shared[lane];
+    return join_wave<ENTROPY>(p, k);
+}
+
 // ---------------------------------------------------------------- results
+
+// What comes with a row besides its logits, read before them, and whether it
+// counts.
+struct RowGiven {
+    int token;
+    bool counts;
+    float weight, old, advantage, ref, up;  // LOSS_POLICY
+    float alpha, eta;                       // LOSS_GIVEN
+};
+
+// array[row], or what stands for an array that is not given.  The load is made
+// either way, from `any` if need be, so that all of them are in flight
+// together: behind a branch each, or behind the token, they cost a round trip
+// each.
+__device__ __forceinline__ float parameter(const float *array, int64_t row, float otherwise,
+                                           const void *any) {
+    const float v = *(array ? array + row : static_cast<const float *>(any));
+    return array ? v : otherwise;
+}
+
+template <bool ENTROPY>
+__device__ __forceinline__ RowGiven given_of(const LossArgs &a, int64_t row) {
+    RowGiven r = {};
+    const uintptr_t z = reinterpret_cast<uintptr_t>(a.in.logits) +
+                        row * a.in.row_stride * (a.in.dtype == NMS_F32 ? 4 : 2);
+    const void *any = reinterpret_cast<const void *>(z & ~(uintptr_t)3);
+    r.token = a.in.tokens[row];
+    r.weight = parameter(a.in.weights, row, a.weight, any);
+    r.old = parameter(a.old_logprobs, row, 0.0f, any);
+    r.advantage = parameter(a.advantages, row, 0.0f, any);
+    r.ref = parameter(a.ref_logprobs, row, 0.0f, any);
+    r.up = parameter(a.grad_loss, 0, 1.0f, any);
+    r.alpha = parameter(a.grad_logprobs, row, 0.0f, any);
+    r.eta = ENTROPY ? parameter(a.grad_entropies, row, 0.0f, any) : 0.0f;
+    r.counts = (unsigned)r.token < (unsigned)a.in.vocab;
+    if (a.in.weights) r.counts &= r.weight != 0.0f;
+    // (a row without a gradient in its results has none, whatever it holds)
+    if (a.kind == LOSS_GIVEN) r.counts &= r.alpha != 0.0f || r.eta != 0.0f;
+    return r;
+}
 
 // One row's results; alpha and eta: the gradients in its log probability and
 // entropy, times that of the loss; term: its part of the loss.
 struct RowResult {
     float logprob, entropy, alpha, eta;
-    double exact, term;
+    double exact, term, log_s;
 };
 
 template <bool ENTROPY>
-__device__ __forceinline__ RowResult result_of(const LossArgs &a, int64_t row, bool counts,
-                                               const Part &p, float inverse, double &log_s) {
+__device__ __forceinline__ RowResult result_of(const LossArgs &a, const RowGiven &given,
+                                               const Part &p, const Scale &k) {
     RowResult r = {};
-    log_s = 0.0;
-    if (!counts) return r;
+    if (!given.counts) return r;
     // in binary64: sums over rows are made of these
-    log_s = log((double)p.s);
-    r.exact = p.s == 0.0f    ? (double)NEG_INF
-              : p.at == NEG_INF ? (double)NEG_INF - log_s
-                                : ((double)p.at - (double)p.m) * (double)inverse - log_s;
+    r.log_s = log_of(p.s);
+    r.exact = p.s == 0.0        ? (double)NEG_INF
+              : p.at == NEG_INF ? (double)NEG_INF - r.log_s
+                                : ((double)p.at - (double)p.m) * (double)k.inverse - r.log_s;
     r.logprob = (float)r.exact;
-    if (ENTROPY) r.entropy = p.s == 0.0f ? 0.0f : (float)(log_s - LN2 * (double)p.w / (double)p.s);
-    if (a.kind == LOSS_GIVEN) {
-        r.alpha = a.grad_logprobs[row];
-        if (ENTROPY) r.eta = a.grad_entropies[row];
-    } else if (a.kind == LOSS_POLICY) {
-        const float weight = a.in.weights ? a.in.weights[row] : a.weight;
-        const float up = a.grad_loss ? a.grad_loss[0] : 1.0f;
-        const float advantage = a.advantages[row];
-        const float ratio = expf((float)(r.exact - (double)a.old_logprobs[row]));
+    if (ENTROPY)
+        r.entropy = p.s == 0.0 ? 0.0f : (float)(r.log_s - LN2 * p.w * inverse_of(p.s));
+    r.alpha = given.alpha;
+    r.eta = given.eta;
+    if (a.kind == LOSS_POLICY) {
+        const float advantage = given.advantage;
+        const float ratio = expf((float)(r.exact - (double)given.old));
         float each = 0.0f, slope = 0.0f;
         if (advantage != 0.0f) {
             const float free = ratio * advantage;
@@ -136,16 +345,15 @@ __device__ __forceinline__ RowResult result_of(const LossArgs &a, int64_t row, b
             if (ratio != ratio || advantage != advantage) each = slope = ratio * advantage;
         }
         if (a.ref_logprobs) {
-            // exp(q) - q - 1, in binary64: it is small where q is
-            const double q = (double)a.ref_logprobs[row] - r.exact;
-            const double more = expm1(q);
-            each += a.kl * (float)(more - q);
-            slope -= a.kl * (float)more;
+            const float q = (float)((double)given.ref - r.exact);
+            const float more = expm1f(q);
+            each += a.kl * (more - q);
+            slope -= a.kl * more;
         }
         if (ENTROPY) each -= a.bonus * r.entropy;
-        r.term = (double)weight * (double)each;
-        r.alpha = up * weight * slope;
-        r.eta = -up * weight * a.bonus;
+        r.term = (double)given.weight * (double)each;
+        r.alpha = given.up * given.weight * slope;
+        r.eta = -given.up * given.weight * a.bonus;
     }
     return r;
 }
@@ -168,6 +376,7 @@ struct LossSpace {
     Part *parts;
     double *terms, *exact;
     float *alpha;
+    bool stream;  // gradients do not stay in the caches
 };
 
 constexpr size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -175,16 +384,17 @@ constexpr size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int THREADS = 256, WAVES = THREADS / 64;
 constexpr int MAX_SLICES = 64;
 
-// Slices of a row: enough workgroups for the GPU where rows are few.
-__host__ __device__ inline int slices_of(int64_t rows, int vocab) {
-    int64_t n = (2048 + rows - 1) / (rows < 1 ? 1 : rows);
+// Slices of a row: two workgroups for each compute unit where rows are few (64 x
+// 131072 bfloat16: log probabilities 8.8 us, 11.1 with eight).
+inline int slices_of(int64_t rows, int vocab) {
+    int64_t n = 512 / (rows < 1 ? 1 : rows);
     const int64_t most = (vocab + 4095) / 4096;
     if (n > most) n = most;
     if (n > MAX_SLICES) n = MAX_SLICES;
     return n < 1 ? 1 : (int)n;
 }
 
-__host__ __device__ inline int slice_size(int vocab, int slices) {
+__device__ inline int slice_size(int vocab, int slices) {
     return ((vocab + slices - 1) / slices + 7) & ~7;
 }
 
@@ -203,6 +413,79 @@ size_t lay_out(int64_t rows, int vocab, int64_t pairs, void *at, LossSpace *s) {
     return parts + terms + exact + alpha;
 }
 
+// ---------------------------------------------------------------- gradient
+
+// What makes a row's gradient: dz_j = e_j (P + Q u_j), and `more` at the token;
+// any: it is not 0.  (A whole word: bytes behind it were copied through LDS at
+// the thread's number, for which every workgroup read the launch's packet in
+// host memory: 256 x 32000 25 us for 17.)
+struct Slope {
+    float base, k, P, Q, more;
+    int any;
+};
+
+template <bool ENTROPY>
+__device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, const Scale &k,
+                                          bool counts) {
+    Slope g;
+    g.any = counts && p.s != 0.0 && (r.alpha != 0.0f || r.eta != 0.0f);
+    g.base = base_of(p.m);
+    g.k = k.hi;
+    const double per = (double)k.inverse * inverse_of(p.s);
+    const double eta = ENTROPY ? (double)r.eta : 0.0;
+    g.P = (float)(-((double)r.alpha + eta * ((double)r.entropy - r.log_s)) * per);
+    g.Q = ENTROPY ? (float)(-eta * LN2 * per) : 0.0f;
+    g.more = r.alpha * k.inverse;
+    return g;
+}
+
+// The gradient of one logit that is not the token's.
+template <bool ENTROPY>
+__device__ __forceinline__ float gradient_of(float z, const Slope &g) {
+    const float u = (z - g.base) * g.k;
+    const float x = exp2_of(u);
+    return ENTROPY ? x * fmaf(g.Q, factor(u), g.P) : x * g.P;
+}
+
+// A pack of logits becomes its gradient, but for what the token's has more.
+template <typename T, bool ENTROPY>
+__device__ __forceinline__ void to_gradient(Pack<T> &e, const Slope &g) {
+    constexpr int N = Pack<T>::N;
+    float d[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) d[j] = gradient_of<ENTROPY>(element(e, j), g);
+    set_elements(e, d);
+}
+
+// As one store of its own, by bytes: it may follow one of a pack to the same place.
+template <typename T>
+__device__ __forceinline__ void store_one(T *p, float v) {
+    const T t = from_f32<T>(v);
+    __builtin_memcpy(p, &t, sizeof(t));
+}
+
+// The gradients of the elements at the edges, one by each thread.
+template <typename T, bool ENTROPY>
+__device__ __forceinline__ void write_edges(const Row<T> &r, T *dz, const Slope &g) {
+    if ((int)threadIdx.x >= r.edges) return;
+    const int i = r.edge(threadIdx.x);
+    float d = 0.0f;
+    if (g.any) {
+        d = gradient_of<ENTROPY>(to_f32(r.z[i]), g);
+        if (i == r.token) d += g.more;
+    }
+    store_one(dz + i, d);
+}
+
+// The token's gradient, over what its pack's thread has written there.
+template <typename T, bool ENTROPY>
+__device__ __forceinline__ void write_token(const Row<T> &r, T *dz, const Slope &g, float z, int lo,
+                                            int end, int group) {
+    if (r.token >= lo && r.token < end &&
+        (int)threadIdx.x == (r.token - lo) / Pack<T>::N % group)
+        store_one(dz + r.token, gradient_of<ENTROPY>(z, g) + g.more);
+}
+
 // ----------------------------------------------------------------- kernels
 
 // A workgroup per (row, slice): the slice's part, and where it is the row's
@@ -210,72 +493,48 @@ size_t lay_out(int64_t rows, int vocab, int64_t pairs, void *at, LossSpace *s) {
 template <typename T, bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void part_kernel(LossArgs a, LossSpace space, int slices,
                                                        bool finish) {
-    constexpr int N = Pack<T>::N, UNROLL = 4, STEP = THREADS * N * UNROLL;
+    constexpr int N = Pack<T>::N, UNROLL = 32 / N, STEP = THREADS * 32;
     __shared__ Part shared[WAVES];
     const int64_t row = blockIdx.x;
-    int token;
-    const bool counts = counts_for(a.in, row, token);
-    const T *z = static_cast<const T *>(a.in.logits) + row * a.in.row_stride;
-    float k, inverse;
-    temperature_of(a.in, row, k, inverse);
-    Part p = {NEG_INF, 0.0f, 0.0f, 0.0f};
-    if (counts) {
-        const int size = slice_size(a.in.vocab, slices);
+    const RowGiven given = given_of<ENTROPY>(a, row);
+    const Scale k = scale_of(a.in, row);
+    Part p = {0.0, 0.0, NEG_INF, 0.0f};
+    if (given.counts) {
+        const Row<T> r(a.in, row, given.token);
+        const float at_token = r.at_token();
+        const int size = slice_size(r.size, slices);
         const int lo = (int)blockIdx.y * size;
-        const int end = min(lo + size, a.in.vocab);
+        const int end = min(lo + size, r.size);
+        p = r.first(blockIdx.y == 0);
         for (int at = lo; at < end; at += STEP) {
             Pack<T> e[UNROLL];
 #pragma unroll
             for (int q = 0; q < UNROLL; ++q) {
                 const int i = at + (q * THREADS + (int)threadIdx.x) * N;
-                e[q] = load_pack(z + i, end - i);
+                e[q] = load_pack(r.z + i, i < end);
             }
-            float top = p.m;
-#pragma unroll
-            for (int q = 0; q < UNROLL; ++q)
-#pragma unroll
-                for (int j = 0; j < N; ++j) top = fmaxf(top, to_f32(e[q].v[j]));
-            const float base = base_of(top);
-            const float d = p.m == NEG_INF ? 0.0f : (p.m - base) * k, f = exp2_of(d);
-            if (ENTROPY) p.w = (p.w + factor(d) * p.s) * f;
-            p.s *= f;
-            p.m = top;
-#pragma unroll
-            for (int q = 0; q < UNROLL; ++q)
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float u = (to_f32(e[q].v[j]) - base) * k;
-                    const float x = exp2_of(u);
-                    p.s += x;
-                    if (ENTROPY) p.w = fmaf(factor(u), x, p.w);
-                }
+            add_packs<T, ENTROPY, UNROLL>(p, e, k);
         }
-        p = join_wave<ENTROPY>(p, k);
+        p = join_group<ENTROPY, WAVES>(p, k, shared);
+        p.at = at_token;
     }
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = p;
-    __syncthreads();
     if (threadIdx.x != 0) return;
-#pragma unroll
-    for (int q = 1; q < WAVES; ++q)
-        join<ENTROPY>(p, shared[q].m, shared[q].s, shared[q].w, k);
-    p.at = counts ? to_f32(z[token]) : 0.0f;
     space.parts[row * slices + blockIdx.y] = p;
-    if (finish) {
-        double log_s;
-        const RowResult r = result_of<ENTROPY>(a, row, counts, p, inverse, log_s);
-        write_result<ENTROPY>(a, row, r, space.exact, space.terms);
-    }
+    if (finish)
+        write_result<ENTROPY>(a, row, result_of<ENTROPY>(a, given, p, k), space.exact,
+                              space.terms);
 }
 
 // A row's part from those of its slices, the same in every lane.
 template <bool ENTROPY>
-__device__ __forceinline__ Part row_part(const LossSpace &space, int64_t row, int slices, float k) {
+__device__ __forceinline__ Part row_part(const LossSpace &space, int64_t row, int slices,
+                                         const Scale &k) {
     const int lane = threadIdx.x & 63;
-    Part p = {NEG_INF, 0.0f, 0.0f, 0.0f};
+    if (slices == 1) return space.parts[row];
+    Part p = {0.0, 0.0, NEG_INF, 0.0f};
     if (lane < slices) p = space.parts[row * slices + lane];
     const float at = __shfl(p.at, 0);
-    p = slices > 1 ? join_wave<ENTROPY>(p, k)
-                   : Part{__shfl(p.m, 0), __shfl(p.s, 0), __shfl(p.w, 0), 0.0f};
+    p = join_wave<ENTROPY>(p, k);
     p.at = at;
     return p;
 }
@@ -285,13 +544,10 @@ template <bool ENTROPY>
 __global__ __launch_bounds__(THREADS) void finish_kernel(LossArgs a, LossSpace space, int slices) {
     const int64_t row = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6);
     if (row >= a.in.rows) return;
-    int token;
-    const bool counts = counts_for(a.in, row, token);
-    float k, inverse;
-    temperature_of(a.in, row, k, inverse);
+    const RowGiven given = given_of<ENTROPY>(a, row);
+    const Scale k = scale_of(a.in, row);
     const Part p = row_part<ENTROPY>(space, row, slices, k);
-    double log_s;
-    const RowResult r = result_of<ENTROPY>(a, row, counts, p, inverse, log_s);
+    const RowResult r = result_of<ENTROPY>(a, given, p, k);
     if ((threadIdx.x & 63) == 0) write_result<ENTROPY>(a, row, r, space.exact, space.terms);
 }
 
@@ -302,50 +558,115 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
                                                            int part_slices, int slices,
                                                            bool results) {
     constexpr int N = Pack<T>::N;
-    const int64_t row = blockIdx.x;
-    int token;
-    const bool counts = counts_for(a.in, row, token);
-    float k, inverse;
-    temperature_of(a.in, row, k, inverse);
-    const T *z = static_cast<const T *>(a.in.logits) + row * a.in.row_stride;
-    T *dz = static_cast<T *>(a.grad_logits) + row * a.grad_stride;
-    const int size = slice_size(a.in.vocab, slices);
+    // the rows that were read last are still in the last cache
+    const int64_t row = (int64_t)gridDim.x - 1 - blockIdx.x;
+    const RowGiven given = given_of<ENTROPY>(a, row);
+    const Scale k = scale_of(a.in, row);
+    const Row<T> r(a.in, row, given.token);
+    T *dz = static_cast<T *>(a.grad_logits) + row * a.grad_stride + r.head;
+    const int size = slice_size(r.size, slices);
     const int lo = (int)blockIdx.y * size;
-    const int end = min(lo + size, a.in.vocab);
-    const Part p = row_part<ENTROPY>(space, row, part_slices, k);
-    double log_s;
-    const RowResult r = result_of<ENTROPY>(a, row, counts, p, inverse, log_s);
-    if (results && blockIdx.y == 0 && threadIdx.x == 0)
-        write_result<ENTROPY>(a, row, r, nullptr, space.terms);
-    // (a row without a gradient in its results has none, whatever it holds)
-    const bool any = counts && p.s != 0.0f && (r.alpha != 0.0f || r.eta != 0.0f);
-    const float base = base_of(p.m);
-    const float per = any ? inverse / p.s : 0.0f;
-    const float P = ENTROPY ? -(r.alpha + r.eta * (float)((double)r.entropy - log_s)) * per
-                            : -r.alpha * per;
-    const float Q = ENTROPY ? -r.eta * (float)LN2 * per : 0.0f;
-    const float more = any ? r.alpha * inverse : 0.0f;
+    const int end = min(lo + size, r.size);
+    Slope g = {};
+    float at_token = 0.0f;
+    if (given.counts || results) {
+        const Part p = row_part<ENTROPY>(space, row, part_slices, k);
+        const RowResult result = result_of<ENTROPY>(a, given, p, k);
+        if (results && blockIdx.y == 0 && threadIdx.x == 0)
+            write_result<ENTROPY>(a, row, result, nullptr, space.terms);
+        g = slope_of<ENTROPY>(result, p, k, given.counts);
+        at_token = p.at;
+    }
+    if (blockIdx.y == 0) write_edges<T, ENTROPY>(r, dz, g);
     for (int i = lo + (int)threadIdx.x * N; i < end; i += THREADS * N) {
         Pack<T> e = {};
-        if (any) {
-            e = load_pack(z + i, end - i);
+        if (g.any) {
+            e = load_pack(r.z + i, true);
+            to_gradient<T, ENTROPY>(e, g);
+        }
+        store_pack(dz + i, e, space.stream);
+    }
+    if (g.any) write_token<T, ENTROPY>(r, dz, g, at_token, lo, end, THREADS);
+}
+
+// A workgroup per row: its results and, with GRADIENT, its gradient.  The first
+// HELD packs of each thread stay in registers between the two, the others are
+// read again.
+template <typename T, bool ENTROPY, bool GRADIENT, int GROUP, int HELD>
+__global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_kernel(LossArgs a, LossSpace space) {
+    constexpr int N = Pack<T>::N, UNROLL = 16 / N, SPAN = GROUP * N;
+    constexpr int CHUNK = HELD < UNROLL ? HELD : UNROLL;
+    static_assert(HELD % CHUNK == 0, "whole chunks");
+    __shared__ Part shared[GROUP / 64];
+    __shared__ Slope slope;
+    const int64_t row = blockIdx.x;
+    const int first = (int)threadIdx.x * N;
+    const RowGiven given = given_of<ENTROPY>(a, row);
+    const Row<T> r(a.in, row, given.token);
+    const int V = r.size;
+    T *dz = static_cast<T *>(a.grad_logits) + row * a.grad_stride + r.head;
+    Pack<T> held[HELD];
+    Slope g = {};
+    float at_token = 0.0f;
+    if (given.counts) {
+        at_token = r.at_token();
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float u = (to_f32(e.v[j]) - base) * k;
-                const float x = exp2_of(u);
-                float d = ENTROPY ? x * fmaf(Q, factor(u), P) : x * P;
-                if (i + j == token) d += more;
-                e.v[j] = from_f32<T>(d);
+        for (int c = 0; c < HELD; c += CHUNK)
+            if (c == 0 || c * SPAN < V) {
+#pragma unroll
+                for (int q = c; q < c + CHUNK; ++q)
+                    held[q] = load_pack(r.z + q * SPAN + first, q * SPAN + first < V);
+            }
+        const Scale k = scale_of(a.in, row);
+        Part p = r.first(true);
+#pragma unroll
+        for (int c = 0; c < HELD; c += CHUNK)
+            if (c == 0 || c * SPAN < V) add_packs<T, ENTROPY, CHUNK>(p, held + c, k);
+        for (int i = HELD * SPAN + first; i < V; i += UNROLL * SPAN) {
+            Pack<T> e[UNROLL];
+#pragma unroll
+            for (int q = 0; q < UNROLL; ++q) e[q] = load_pack(r.z + i + q * SPAN, i + q * SPAN < V);
+            add_packs<T, ENTROPY, UNROLL>(p, e, k);
+        }
+        p = GROUP == 64 ? join_wave<ENTROPY>(p, k) : join_group<ENTROPY, GROUP / 64>(p, k, shared);
+        p.at = at_token;
+        if (threadIdx.x < 64) {
+            const RowResult result = result_of<ENTROPY>(a, given, p, k);
+            g = slope_of<ENTROPY>(result, p, k, true);
+            if (threadIdx.x == 0) {
+                write_result<ENTROPY>(a, row, result, space.exact, space.terms);
+                if (!GRADIENT && space.parts) space.parts[row] = p;
+                if (GRADIENT && GROUP > 64) slope = g;
             }
         }
-        if (end - i >= N) {
-            __builtin_memcpy(dz + i, &e, sizeof(e));
-        } else {
+        if (GRADIENT && GROUP > 64) {
+            __syncthreads();
+            g = slope;
+        }
+    } else if (threadIdx.x == 0) {
+        write_result<ENTROPY>(a, row, RowResult{}, space.exact, space.terms);
+        if (!GRADIENT && space.parts) space.parts[row] = {0.0, 0.0, NEG_INF, 0.0f};
+    }
+    if (!GRADIENT) return;
+    write_edges<T, ENTROPY>(r, dz, g);
+    if (!g.any) {
+        for (int i = first; i < V; i += SPAN) store_pack(dz + i, Pack<T>{}, space.stream);
+        return;
+    }
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (j < end - i) dz[i + j] = e.v[j];
+    for (int q = 0; q < HELD; ++q) {
+        const int i = q * SPAN + first;
+        if (q == 0 || q * SPAN < V) {
+            to_gradient<T, ENTROPY>(held[q], g);
+            if (i < V) store_pack(dz + i, held[q], space.stream);
         }
     }
+    for (int i = HELD * SPAN + first; i < V; i += SPAN) {
+        Pack<T> e = load_pack(r.z + i, true);
+        to_gradient<T, ENTROPY>(e, g);
+        store_pack(dz + i, e, space.stream);
+    }
+    write_token<T, ENTROPY>(r, dz, g, at_token, 0, V, GROUP);
 }
 
 // ---------------------------------------------------------- sums of a loss
@@ -465,37 +786,97 @@ __global__ __launch_bounds__(TOTAL_THREADS) void pair_kernel(PreferenceArgs a, L
 
 // ----------------------------------------------------------------- launches
 
-// Parts of all rows; their results too where nothing else is to follow.
+int64_t row_bytes(const LossRows &in) {
+    return (int64_t)in.vocab * (in.dtype == NMS_F32 ? 4 : 2);
+}
+
+// Whether a workgroup takes a whole row and holds it, for results alone.  Rows
+// up to 64 KB: 64 x 32000 bfloat16 5.2 us, 6.3 by slices in two launches; 16384 x
+// 2000 14 us, 42 by a workgroup of 256 that reads on.  Up to 128 KB from 64 rows
+// on: 256 x 65536 10.0 us, 12.6 by slices (one row: 6.6 and 5.3).  Longer rows
+// take all registers of a compute unit, so that reading one row waits for the
+// one before: 4096 x 131072 218 us, 200 by workgroups of 256 that read on.
+bool held_for_results(const LossRows &in) {
+    return row_bytes(in) <= 65536 || (row_bytes(in) <= 131072 && in.rows >= 64);
+}
+
+// For the gradient, which slices read a second time: 256 x 131072 bfloat16 29.6
+// us, 38.9 by slices; 4096 x 131072 398 and 611.  Few long rows leave the GPU
+// empty: 16 x 131072 19.1 and 10.0, 64 x 131072 21.9 and 18.1, 96 even.
+bool held_for_gradient(const LossRows &in) {
+    return row_bytes(in) <= 65536 || in.rows >= (row_bytes(in) <= 131072 ? 64 : 96);
+}
+
+// Threads and packs by the row's size; what 1024 threads do not hold (of rows
+// above 256 KB) is read a second time.  Rows of 4000 bfloat16 took 48 us for
+// 16384 with 128 threads, 60 with 64 and 53 with 256; of 32000 101 us for 4096 with
+// 512, 109 with 256; of 65536 201 with 1024 of 8 packs, 219 with 1024 of 16.
+template <typename T, bool ENTROPY, bool GRADIENT>
+void run_rows(const LossArgs &a, const LossSpace &s, hipStream_t stream) {
+    const unsigned n = (unsigned)a.in.rows;
+    const int64_t bytes = row_bytes(a.in);
+    if (bytes <= 4096)
+        row_kernel<T, ENTROPY, GRADIENT, 64, 4><<<n, 64, 0, stream>>>(a, s);
+    else if (bytes <= 16384)
+        row_kernel<T, ENTROPY, GRADIENT, 128, 8><<<n, 128, 0, stream>>>(a, s);
+    else if (bytes <= 65536)
+        row_kernel<T, ENTROPY, GRADIENT, 512, 8><<<n, 512, 0, stream>>>(a, s);
+    else if (bytes <= 131072)
+        row_kernel<T, ENTROPY, GRADIENT, 1024, 8><<<n, 1024, 0, stream>>>(a, s);
+    else if constexpr (GRADIENT)
+        row_kernel<T, ENTROPY, GRADIENT, 1024, 16><<<n, 1024, 0, stream>>>(a, s);
+}
+
+// The parts of all rows, and with `results` their results.  Returns the number
+// of parts of a row.
 template <typename T, bool ENTROPY>
-void run_parts(const LossArgs &a, const LossSpace &s, int slices, bool results,
-               hipStream_t stream) {
+int run_parts(const LossArgs &a, const LossSpace &s, bool results, hipStream_t stream) {
+    if (held_for_results(a.in)) {
+        run_rows<T, ENTROPY, false>(a, s, stream);
+        return 1;
+    }
+    const int slices = slices_of(a.in.rows, a.in.vocab);
     const bool finish = results && slices == 1;
     part_kernel<T, ENTROPY><<<dim3((unsigned)a.in.rows, (unsigned)slices), THREADS, 0, stream>>>(
         a, s, slices, finish);
     if (results && !finish)
         finish_kernel<ENTROPY>
             <<<(unsigned)((a.in.rows + WAVES - 1) / WAVES), THREADS, 0, stream>>>(a, s, slices);
+    return slices;
 }
 
+// The gradient from the parts.
 template <typename T, bool ENTROPY>
-void run_gradient(const LossArgs &a, const LossSpace &s, int slices, bool results,
+void run_gradient(const LossArgs &a, const LossSpace &s, int parts, bool results,
                   hipStream_t stream) {
+    const int slices = slices_of(a.in.rows, a.in.vocab);
     gradient_kernel<T, ENTROPY>
-        <<<dim3((unsigned)a.in.rows, (unsigned)slices), THREADS, 0, stream>>>(a, s, slices, slices,
-                                                                               results);
+        <<<dim3((unsigned)a.in.rows, (unsigned)slices), THREADS, 0, stream>>>(a, s, parts, slices,
+                                                                              results);
 }
+
+// Gradients above this many bytes are written past the caches: what is there of
+// the logits stays for a kernel that reads them again (8192 x 32000 bfloat16,
+// preference loss 212 us, 264 without), and 4096 x 131072 take 421 us for 435.
+// Below it whatever comes next finds the gradient there.
+constexpr int64_t STREAMED = (int64_t)192 << 20;
+bool streamed(const LossRows &in) { return in.rows * row_bytes(in) > STREAMED; }
 
 template <typename T, bool ENTROPY>
 void run(const LossArgs &a, hipStream_t stream) {
     LossSpace s;
     lay_out(a.in.rows, a.in.vocab, 0, a.workspace, &s);
     s.exact = nullptr;
-    const int slices = slices_of(a.in.rows, a.in.vocab);
-    const bool gradient = a.grad_logits != nullptr;
+    s.stream = streamed(a.in);
     if (a.loss == nullptr) s.terms = nullptr;
-    run_parts<T, ENTROPY>(a, s, slices, !gradient, stream);
-    if (gradient)
-        run_gradient<T, ENTROPY>(a, s, slices, a.logprobs || a.entropies || a.loss, stream);
+    if (a.grad_logits == nullptr) {
+        run_parts<T, ENTROPY>(a, s, true, stream);
+    } else if (held_for_gradient(a.in)) {
+        run_rows<T, ENTROPY, true>(a, s, stream);
+    } else {
+        const int parts = run_parts<T, ENTROPY>(a, s, false, stream);
+        run_gradient<T, ENTROPY>(a, s, parts, a.logprobs || a.entropies || a.loss, stream);
+    }
 }
 
 template <typename T>
@@ -508,21 +889,32 @@ template <typename T>
 void run_preference(const PreferenceArgs &a, hipStream_t stream) {
     LossSpace s;
     lay_out(a.in.rows, a.in.vocab, a.pairs, a.workspace, &s);
-    const int slices = slices_of(a.in.rows, a.in.vocab);
+    s.stream = streamed(a.in);
     LossArgs rows = {};
     rows.in = a.in;
     rows.kind = LOSS_LOGPROBS;
-    LossSpace first = s;
-    first.terms = nullptr;
-    if (a.in.rows > 0) run_parts<T, false>(rows, first, slices, a.known_margins == nullptr, stream);
+    LossSpace of_rows = s;
+    of_rows.terms = nullptr;
+    const bool forward = a.known_margins == nullptr, some = a.in.rows > 0;
+    int parts = 1;
+    if (forward && some) parts = run_parts<T, false>(rows, of_rows, true, stream);
     pair_kernel<<<(unsigned)a.pairs, TOTAL_THREADS, 0, stream>>>(a, s);
-    if (a.loss) launch_total(s.terms, a.pairs, a.loss, stream);
-    if (a.grad_logits && a.in.rows > 0) {
-        rows.kind = LOSS_GIVEN;
-        rows.grad_logprobs = s.alpha;
-        rows.grad_logits = a.grad_logits;
-        rows.grad_stride = a.grad_stride;
-        run_gradient<T, false>(rows, first, slices, false, stream);
+    if (forward) launch_total(s.terms, a.pairs, a.loss, stream);
+    if (a.grad_logits == nullptr || !some) return;
+    rows.kind = LOSS_GIVEN;
+    rows.grad_logprobs = s.alpha;
+    rows.grad_logits = a.grad_logits;
+    rows.grad_stride = a.grad_stride;
+    if (forward) {
+        run_gradient<T, false>(rows, of_rows, parts, false, stream);
+    } else {
+        of_rows.exact = nullptr;
+        if (held_for_gradient(a.in)) {
+            run_rows<T, false, true>(rows, of_rows, stream);
+        } else {
+            parts = run_parts<T, false>(rows, of_rows, false, stream);
+            run_gradient<T, false>(rows, of_rows, parts, false, stream);
+        }
     }
 }
 
