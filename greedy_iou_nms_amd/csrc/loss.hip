@@ -68,23 +68,28 @@ __device__ __forceinline__ void set_elements(Pack<T> &e, const float *v) {
 typedef uint32_t Words __attribute__((ext_vector_type(4), may_alias));
 typedef uint32_t LooseWords __attribute__((ext_vector_type(4), aligned(2), may_alias));
 
-// The pack at an aligned address, or one of -infinity.
-template <typename T>
+// The pack at an aligned address, or one of -infinity.  STREAM: it is not read
+// again, and does not stay in the caches.
+template <bool STREAM, typename T>
 __device__ __forceinline__ Pack<T> load_pack(const T *p, bool there) {
     const uint32_t none = sizeof(T) == 4 ? 0xff800000u
                           : __is_same(T, half_t) ? 0xfc00fc00u : 0xff80ff80u;
     Words w = {none, none, none, none};
-    if (there) w = *reinterpret_cast<const Words *>(p);
+    if (there) {
+        const Words *from = reinterpret_cast<const Words *>(p);
+        w = STREAM ? __builtin_nontemporal_load(from) : *from;
+    }
     return {{w.x, w.y, w.z, w.w}};
 }
 
-// To any element's address.  stream: the pack is not kept in the caches, where
-// it would take the place of logits that are still to be read.
-template <typename T>
-__device__ __forceinline__ void store_pack(T *p, const Pack<T> &e, bool stream) {
+// To any element's address.  STREAM: it does not stay in the caches, where it
+// would take the place of logits that are still to be read.
+template <bool STREAM, typename T>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T> &e) {
     const LooseWords w = {e.w[0], e.w[1], e.w[2], e.w[3]};
-    if (stream) __builtin_nontemporal_store(w, reinterpret_cast<LooseWords *>(p));
-    else *reinterpret_cast<LooseWords *>(p) = w;
+    LooseWords *to = reinterpret_cast<LooseWords *>(p);
+    if (STREAM) __builtin_nontemporal_store(w, to);
+    else *to = w;
 }
 
 // log2(e) / t as a sum, whose second term keeps sums over many rows unbiased
@@ -376,7 +381,6 @@ struct LossSpace {
     Part *parts;
     double *terms, *exact;
     float *alpha;
-    bool stream;  // gradients do not stay in the caches
 };
 
 constexpr size_t round_up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -511,7 +515,7 @@ __global__ __launch_bounds__(THREADS) void part_kernel(LossArgs a, LossSpace spa
 #pragma unroll
             for (int q = 0; q < UNROLL; ++q) {
                 const int i = at + (q * THREADS + (int)threadIdx.x) * N;
-                e[q] = load_pack(r.z + i, i < end);
+                e[q] = load_pack<false>(r.z + i, i < end);
             }
             add_packs<T, ENTROPY, UNROLL>(p, e, k);
         }
@@ -553,7 +557,7 @@ __global__ __launch_bounds__(THREADS) void finish_kernel(LossArgs a, LossSpace s
 
 // A workgroup per (row, slice): the gradient in its logits; the first of a
 // row writes the row's results.
-template <typename T, bool ENTROPY>
+template <typename T, bool ENTROPY, bool STREAM>
 __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace space,
                                                            int part_slices, int slices,
                                                            bool results) {
@@ -581,10 +585,10 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
     for (int i = lo + (int)threadIdx.x * N; i < end; i += THREADS * N) {
         Pack<T> e = {};
         if (g.any) {
-            e = load_pack(r.z + i, true);
+            e = load_pack<STREAM>(r.z + i, true);
             to_gradient<T, ENTROPY>(e, g);
         }
-        store_pack(dz + i, e, space.stream);
+        store_pack<STREAM>(dz + i, e);
     }
     if (g.any) write_token<T, ENTROPY>(r, dz, g, at_token, lo, end, THREADS);
 }
@@ -592,14 +596,15 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
 // A workgroup per row: its results and, with GRADIENT, its gradient.  The first
 // HELD packs of each thread stay in registers between the two, the others are
 // read again.
-template <typename T, bool ENTROPY, bool GRADIENT, int GROUP, int HELD>
+template <typename T, bool ENTROPY, bool GRADIENT, bool STREAM, int GROUP, int HELD>
 __global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_kernel(LossArgs a, LossSpace space) {
     constexpr int N = Pack<T>::N, UNROLL = 16 / N, SPAN = GROUP * N;
     constexpr int CHUNK = HELD < UNROLL ? HELD : UNROLL;
     static_assert(HELD % CHUNK == 0, "whole chunks");
     __shared__ Part shared[GROUP / 64];
     __shared__ Slope slope;
-    const int64_t row = blockIdx.x;
+    // the rows that were read or written last are still in the last cache
+    const int64_t row = GRADIENT ? (int64_t)gridDim.x - 1 - blockIdx.x : blockIdx.x;
     const int first = (int)threadIdx.x * N;
     const RowGiven given = given_of<ENTROPY>(a, row);
     const Row<T> r(a.in, row, given.token);
@@ -615,7 +620,7 @@ __global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_
             if (c == 0 || c * SPAN < V) {
 #pragma unroll
                 for (int q = c; q < c + CHUNK; ++q)
-                    held[q] = load_pack(r.z + q * SPAN + first, q * SPAN + first < V);
+                    held[q] = load_pack<STREAM>(r.z + q * SPAN + first, q * SPAN + first < V);
             }
         const Scale k = scale_of(a.in, row);
         Part p = r.first(true);
@@ -625,7 +630,7 @@ __global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_
         for (int i = HELD * SPAN + first; i < V; i += UNROLL * SPAN) {
             Pack<T> e[UNROLL];
 #pragma unroll
-            for (int q = 0; q < UNROLL; ++q) e[q] = load_pack(r.z + i + q * SPAN, i + q * SPAN < V);
+            for (int q = 0; q < UNROLL; ++q) e[q] = load_pack<false>(r.z + i + q * SPAN, i + q * SPAN < V);
             add_packs<T, ENTROPY, UNROLL>(p, e, k);
         }
         p = GROUP == 64 ? join_wave<ENTROPY>(p, k) : join_group<ENTROPY, GROUP / 64>(p, k, shared);
@@ -650,7 +655,7 @@ __global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_
     if (!GRADIENT) return;
     write_edges<T, ENTROPY>(r, dz, g);
     if (!g.any) {
-        for (int i = first; i < V; i += SPAN) store_pack(dz + i, Pack<T>{}, space.stream);
+        for (int i = first; i < V; i += SPAN) store_pack<STREAM>(dz + i, Pack<T>{});
         return;
     }
 #pragma unroll
@@ -658,13 +663,13 @@ __global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_
         const int i = q * SPAN + first;
         if (q == 0 || q * SPAN < V) {
             to_gradient<T, ENTROPY>(held[q], g);
-            if (i < V) store_pack(dz + i, held[q], space.stream);
+            if (i < V) store_pack<STREAM>(dz + i, held[q]);
         }
     }
     for (int i = HELD * SPAN + first; i < V; i += SPAN) {
-        Pack<T> e = load_pack(r.z + i, true);
+        Pack<T> e = load_pack<STREAM>(r.z + i, true);
         to_gradient<T, ENTROPY>(e, g);
-        store_pack(dz + i, e, space.stream);
+        store_pack<STREAM>(dz + i, e);
     }
     write_token<T, ENTROPY>(r, dz, g, at_token, 0, V, GROUP);
 }
@@ -811,20 +816,37 @@ bool held_for_gradient(const LossRows &in) {
 // above 256 KB) is read a second time.  Rows of 4000 bfloat16 took 48 us for
 // 16384 with 128 threads, 60 with 64 and 53 with 256; of 32000 101 us for 4096 with
 // 512, 109 with 256; of 65536 201 with 1024 of 8 packs, 219 with 1024 of 16.
-template <typename T, bool ENTROPY, bool GRADIENT>
-void run_rows(const LossArgs &a, const LossSpace &s, hipStream_t stream) {
+template <typename T, bool ENTROPY, bool GRADIENT, bool STREAM>
+void launch_rows(const LossArgs &a, const LossSpace &s, hipStream_t stream) {
     const unsigned n = (unsigned)a.in.rows;
     const int64_t bytes = row_bytes(a.in);
     if (bytes <= 4096)
-        row_kernel<T, ENTROPY, GRADIENT, 64, 4><<<n, 64, 0, stream>>>(a, s);
+        row_kernel<T, ENTROPY, GRADIENT, STREAM, 64, 4><<<n, 64, 0, stream>>>(a, s);
     else if (bytes <= 16384)
-        row_kernel<T, ENTROPY, GRADIENT, 128, 8><<<n, 128, 0, stream>>>(a, s);
+        row_kernel<T, ENTROPY, GRADIENT, STREAM, 128, 8><<<n, 128, 0, stream>>>(a, s);
     else if (bytes <= 65536)
-        row_kernel<T, ENTROPY, GRADIENT, 512, 8><<<n, 512, 0, stream>>>(a, s);
+        row_kernel<T, ENTROPY, GRADIENT, STREAM, 512, 8><<<n, 512, 0, stream>>>(a, s);
     else if (bytes <= 131072)
-        row_kernel<T, ENTROPY, GRADIENT, 1024, 8><<<n, 1024, 0, stream>>>(a, s);
+        row_kernel<T, ENTROPY, GRADIENT, STREAM, 1024, 8><<<n, 1024, 0, stream>>>(a, s);
     else if constexpr (GRADIENT)
-        row_kernel<T, ENTROPY, GRADIENT, 1024, 16><<<n, 1024, 0, stream>>>(a, s);
+        row_kernel<T, ENTROPY, GRADIENT, STREAM, 1024, 16><<<n, 1024, 0, stream>>>(a, s);
+}
+
+// Logits of more bytes than this pass the caches when they are read for the last
+// time, and so does their gradient.  What was read of them before, or is yet
+// to be, stays there: preference loss of 8192 x 32000 bfloat16 189 us, 248
+// without, of 4001 x 131072 507 and 574; policy loss of 4096 x 131072 389 and 399,
+// of 3000 x 32000 (183 MB) 66 and 80, but of 1024 x 32000 31 and 28.  Below, whatever
+// comes next finds the gradient in the caches; where logits are read twice
+// (2048 x 32000, 125 MB: 63 and 73 us) they are streamed earlier.
+constexpr int64_t STREAMED_ONCE = (int64_t)160 << 20, STREAMED_TWICE = (int64_t)96 << 20;
+
+template <typename T, bool ENTROPY>
+void run_rows(const LossArgs &a, const LossSpace &s, hipStream_t stream) {
+    if (a.in.rows * row_bytes(a.in) > STREAMED_ONCE)
+        launch_rows<T, ENTROPY, true, true>(a, s, stream);
+    else
+        launch_rows<T, ENTROPY, true, false>(a, s, stream);
 }
 
 // The parts of all rows, and with `results` their results.  Returns the number
@@ -832,7 +854,7 @@ void run_rows(const LossArgs &a, const LossSpace &s, hipStream_t stream) {
 template <typename T, bool ENTROPY>
 int run_parts(const LossArgs &a, const LossSpace &s, bool results, hipStream_t stream) {
     if (held_for_results(a.in)) {
-        run_rows<T, ENTROPY, false>(a, s, stream);
+        launch_rows<T, ENTROPY, false, false>(a, s, stream);
         return 1;
     }
     const int slices = slices_of(a.in.rows, a.in.vocab);
@@ -850,29 +872,25 @@ template <typename T, bool ENTROPY>
 void run_gradient(const LossArgs &a, const LossSpace &s, int parts, bool results,
                   hipStream_t stream) {
     const int slices = slices_of(a.in.rows, a.in.vocab);
-    gradient_kernel<T, ENTROPY>
-        <<<dim3((unsigned)a.in.rows, (unsigned)slices), THREADS, 0, stream>>>(a, s, parts, slices,
-                                                                              results);
+    const dim3 grid((unsigned)a.in.rows, (unsigned)slices);
+    if (a.in.rows * row_bytes(a.in) > STREAMED_TWICE)
+        gradient_kernel<T, ENTROPY, true>
+            <<<grid, THREADS, 0, stream>>>(a, s, parts, slices, results);
+    else
+        gradient_kernel<T, ENTROPY, false>
+            <<<grid, THREADS, 0, stream>>>(a, s, parts, slices, results);
 }
-
-// Gradients above this many bytes are written past the caches: what is there of
-// the logits stays for a kernel that reads them again (8192 x 32000 bfloat16,
-// preference loss 212 us, 264 without), and 4096 x 131072 take 421 us for 435.
-// Below it whatever comes next finds the gradient there.
-constexpr int64_t STREAMED = (int64_t)192 << 20;
-bool streamed(const LossRows &in) { return in.rows * row_bytes(in) > STREAMED; }
 
 template <typename T, bool ENTROPY>
 void run(const LossArgs &a, hipStream_t stream) {
     LossSpace s;
     lay_out(a.in.rows, a.in.vocab, 0, a.workspace, &s);
     s.exact = nullptr;
-    s.stream = streamed(a.in);
     if (a.loss == nullptr) s.terms = nullptr;
     if (a.grad_logits == nullptr) {
         run_parts<T, ENTROPY>(a, s, true, stream);
     } else if (held_for_gradient(a.in)) {
-        run_rows<T, ENTROPY, true>(a, s, stream);
+        run_rows<T, ENTROPY>(a, s, stream);
     } else {
         const int parts = run_parts<T, ENTROPY>(a, s, false, stream);
         run_gradient<T, ENTROPY>(a, s, parts, a.logprobs || a.entropies || a.loss, stream);
@@ -889,7 +907,6 @@ template <typename T>
 void run_preference(const PreferenceArgs &a, hipStream_t stream) {
     LossSpace s;
     lay_out(a.in.rows, a.in.vocab, a.pairs, a.workspace, &s);
-    s.stream = streamed(a.in);
     LossArgs rows = {};
     rows.in = a.in;
     rows.kind = LOSS_LOGPROBS;
@@ -910,7 +927,7 @@ void run_preference(const PreferenceArgs &a, hipStream_t stream) {
     } else {
         of_rows.exact = nullptr;
         if (held_for_gradient(a.in)) {
-            run_rows<T, false, true>(rows, of_rows, stream);
+            run_rows<T, false>(rows, of_rows, stream);
         } else {
             parts = run_parts<T, false>(rows, of_rows, false, stream);
             run_gradient<T, false>(rows, of_rows, parts, false, stream);
