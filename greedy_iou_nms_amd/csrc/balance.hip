@@ -22,9 +22,10 @@ constexpr int CT = 1024;  // threads that count
 constexpr int MAX_PARTS = 64, PART_IDS = 8192;
 
 // The counts of each part of a sequence, the tokens of the parts and of the
-// whole, the sequence of each token, the factors a, the terms.
+// whole, the sequence of each token, or where there is only one its first token
+// and the one behind its last, the factors a, the terms.
 struct BalanceSpace {
-    int32_t *parts, *part_tokens, *tokens, *owner;
+    int32_t *parts, *part_tokens, *tokens, *owner, *range;
     float *factors;
     double *terms;
     int64_t blocks;
@@ -70,13 +71,15 @@ size_t lay_out(int64_t tokens, int experts, int64_t sequences, int top_k, void *
     char *counted = take(parts > 1 ? parts * cells * sizeof(int32_t) : 0);
     char *part_tokens = take((size_t)parts * sequences * sizeof(int32_t));
     char *seq = take((size_t)sequences * sizeof(int32_t));
-    char *owner = take((size_t)tokens * sizeof(int32_t));
+    char *range = take(2 * sizeof(int32_t));
+    char *owner = take(sequences > 1 ? (size_t)tokens * sizeof(int32_t) : 0);
     char *factors = take(cells * sizeof(float));
     char *terms = take((size_t)blocks * sizeof(double));
     if (s)
         *s = {reinterpret_cast<int32_t *>(counted), reinterpret_cast<int32_t *>(part_tokens),
               reinterpret_cast<int32_t *>(seq),     reinterpret_cast<int32_t *>(owner),
-              reinterpret_cast<float *>(factors),   reinterpret_cast<double *>(terms), blocks};
+              reinterpret_cast<int32_t *>(range),   reinterpret_cast<float *>(factors),
+              reinterpret_cast<double *>(terms),    blocks};
     return n;
 }
 
@@ -172,12 +175,17 @@ __global__ __launch_bounds__(CT) void count_kernel(BalanceArgs a, BalanceSpace s
     __syncthreads();
     const int size = (end - begin + parts - 1) / parts;
     const int from = min(begin + part * size, end), to = min(from + size, end);
-    const int used = count_tokens(a, from, to, (int)q, s.owner, hist);
+    const bool several = a.sequences > 1;
+    const int used = count_tokens(a, from, to, (int)q, several ? s.owner : nullptr, hist);
     // the tokens of no sequence
-    if (q == 0 && part == 0)
+    if (several && q == 0 && part == 0)
         for (int t = tid; t < begin; t += CT) s.owner[t] = -1;
-    if (q == a.sequences - 1 && part == 0)
+    if (several && q == a.sequences - 1 && part == 0)
         for (int64_t t = end + tid; t < a.tokens; t += CT) s.owner[t] = -1;
+    if (!several && tid == 0 && part == 0) {
+        s.range[0] = begin;
+        s.range[1] = end;
+    }
     __syncthreads();
     int count = 0;
     if (tid < a.experts) {
@@ -253,15 +261,17 @@ __device__ __forceinline__ float token_loss(float (&z)[VALUES], const float (&f)
         // m = min(largest logit, 0): below -88 a score itself is under
         // float32's range, its share is not
         const float m = fminf(base, 0.0f);
+        const bool under_0 = __ballot(m < 0.0f) != 0ull;
         float total = 0.0f, rest[VALUES];  // rest: 1 - score
 #pragma unroll
         for (int j = 0; j < VALUES; ++j) {
-            const float low = __builtin_amdgcn_exp2f(-fabsf(z[j]) * LOG2E);
-            const float part = 1.0f / (1.0f + low);
+            // (the inverse by one instruction, off by up to an ulp)
+            float low = __builtin_amdgcn_exp2f(-fabsf(z[j]) * LOG2E);
+            const float part = __builtin_amdgcn_rcpf(1.0f + low);
             const bool up = z[j] > 0.0f;
             rest[j] = up ? low * part : part;
-            const float score = up ? part : __builtin_amdgcn_exp2f((z[j] - m) * LOG2E) * part;
-            z[j] = z[j] == z[j] ? score : z[j];
+            if (under_0) low = __builtin_amdgcn_exp2f((z[j] - m) * LOG2E);
+            z[j] = (up ? 1.0f : low) * part;
             total += z[j];
         }
         total = all_sum<LANES>(total);
@@ -324,15 +334,20 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
     T *out = static_cast<T *>(a.grad_logits) + e0;
     int owner[TURNS];
     Raw<T, VALUES> raw[TURNS];
+    // (loaded whether the token counts or not, which another load says)
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
         const int64_t t = first + i * GROUPS;
-        owner[i] = t < a.tokens ? s.owner[t] : -1;
+        raw[i] = load_raw<T, VALUES>(logits + t * a.row_stride, left, t < a.tokens);
     }
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
         const int64_t t = first + i * GROUPS;
-        raw[i] = load_raw<T, VALUES>(logits + t * a.row_stride, left, owner[i] >= 0);
+        owner[i] = -1;
+        if (t < a.tokens) {
+            if (a.sequences > 1) owner[i] = s.owner[t];
+            else if (t >= s.range[0] && t < s.range[1] && (!a.live || a.live[t])) owner[i] = 0;
+        }
     }
     float per = 0.0f;
     if (a.z != 0.0f) {
@@ -347,7 +362,7 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
         const int64_t t = first + i * GROUPS;
-        if (i == 0 || owner[i] != held) {
+        if (i == 0 || (a.sequences > 1 && owner[i] != held)) {
             const float *from = s.factors + (int64_t)max(owner[i], 0) * E + e0;
             if (left >= VALUES) {
                 __builtin_memcpy(f, from, sizeof(f));
@@ -359,7 +374,7 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
         }
         float z[VALUES];
 #pragma unroll
-        for (int j = 0; j < VALUES; ++j) z[j] = to_f32(raw[i].v[j]);
+        for (int j = 0; j < VALUES; ++j) z[j] = owner[i] >= 0 ? to_f32(raw[i].v[j]) : NEG_INF;
         const float mine = token_loss<LANES, VALUES>(z, f, a.score == NMS_ROUTE_SOFTMAX, per);
         if (sub == 0) term += (double)mine;
         if (a.grad_logits && t < a.tokens)

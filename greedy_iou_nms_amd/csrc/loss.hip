@@ -700,93 +700,115 @@ __global__ __launch_bounds__(TOTAL_THREADS) void total_kernel(const double *term
 
 // -------------------------------------------------------------- preference
 
-// Where a sequence starts: the largest offset up to its own, within the rows,
-// so that the sequences never overlap.
-__device__ __forceinline__ int64_t start_of(const int64_t *offsets, int64_t q, int64_t rows,
-                                            double *shared) {
-    int64_t top = 0;
-    for (int64_t i = threadIdx.x; i <= q; i += blockDim.x) top = max(top, offsets[i]);
-    top = min(top, rows);
-    int v = wave_max((int)top);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = (double)v;
-    __syncthreads();
-    for (int w = 0; w < (int)blockDim.x / 64; ++w) v = max(v, (int)shared[w]);
-    return v;
-}
+// What the waves of a pair's workgroup tell each other.
+struct PairShared {
+    int top[TOTAL_THREADS / 64][2];
+    double sum[TOTAL_THREADS / 64][2], used[TOTAL_THREADS / 64][2];
+    float alpha[2];
+};
 
 // A workgroup per pair: the log probabilities of its sequences, its loss, and
 // the gradient in the log probability of each of their rows.
 __global__ __launch_bounds__(TOTAL_THREADS) void pair_kernel(PreferenceArgs a, LossSpace space) {
-    __shared__ double shared[TOTAL_THREADS / 64];
-    const int64_t pair = blockIdx.x;
-    int64_t begin[2], end[2];
-    double sum[2], n[2];
+    __shared__ PairShared shared;
+    constexpr int WAVES = TOTAL_THREADS / 64;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int64_t pair = blockIdx.x, other = a.pairs + pair;
+    const bool forward = a.known_margins == nullptr;
+    // A sequence starts at the largest offset up to its own, within the rows, so
+    // that the sequences never overlap.
+    const int64_t next[2] = {a.offsets[pair + 1], a.offsets[other + 1]};
+    int64_t top[2] = {0, 0};
+    for (int64_t i = tid; i <= other; i += TOTAL_THREADS) {
+        const int64_t at = a.offsets[i];
+        if (i <= pair) top[0] = max(top[0], at);
+        top[1] = max(top[1], at);
+    }
     for (int side = 0; side < 2; ++side) {
-        const int64_t q = side * a.pairs + pair;
-        begin[side] = start_of(a.offsets, q, a.in.rows, shared);
-        end[side] = start_of(a.offsets, q + 1, a.in.rows, shared);
-        double total = 0.0, used = 0.0;
-        for (int64_t i = begin[side] + threadIdx.x; i < end[side]; i += TOTAL_THREADS) {
+        const int v = wave_max((int)min(top[side], a.in.rows));
+        if ((tid & 63) == 0) shared.top[wave][side] = v;
+    }
+    __syncthreads();
+    int begin[2] = {0, 0}, end[2];
+    for (int side = 0; side < 2; ++side) {
+        for (int w = 0; w < WAVES; ++w) begin[side] = max(begin[side], shared.top[w][side]);
+        end[side] = max(begin[side], (int)min(max(next[side], (int64_t)0), a.in.rows));
+    }
+    for (int side = 0; side < 2; ++side) {
+        double sum = 0.0, used = 0.0;
+        for (int i = begin[side] + tid; i < end[side]; i += TOTAL_THREADS) {
             const bool counts = (unsigned)a.in.tokens[i] < (unsigned)a.in.vocab;
             if (counts) used += 1.0;
-            if (counts && a.known_margins == nullptr) total += space.exact[i];
+            if (counts && forward) sum += space.exact[i];
         }
-        n[side] = a.average ? fmax(block_sum(used, shared), 1.0) : 1.0;
-        sum[side] = a.known_margins == nullptr ? block_sum(total, shared) / n[side] : 0.0;
+        sum = wave_sum(sum);
+        used = wave_sum(used);
+        if ((tid & 63) == 0) {
+            shared.sum[wave][side] = sum;
+            shared.used[wave][side] = used;
+        }
     }
-    double h;
-    if (a.known_margins) {
-        h = (double)a.known_margins[pair];
-    } else {
-        double rel[2];
-        for (int side = 0; side < 2; ++side)
-            rel[side] = sum[side] -
-                        (a.ref_logprobs ? (double)a.ref_logprobs[side * a.pairs + pair] : 0.0);
-        h = (double)a.beta * (rel[0] - rel[1]) - (double)a.margin;
-    }
-    const double weight = a.weights ? (double)a.weights[pair] : (double)a.weight;
-    const double beta = (double)a.beta, smooth = (double)a.smoothing;
-    double each, slope;
-    if (a.kind == NMS_PREFERENCE_SIGMOID) {
-        // log(1 + exp(-h)) and log(1 + exp(h)), one of which is near 0
-        const double rest = log1p(exp(-fabs(h)));
-        const double up = rest + fmax(-h, 0.0), down = rest + fmax(h, 0.0);
-        each = (1.0 - smooth) * up + (smooth > 0.0 ? smooth * down : 0.0);
-        slope = smooth * exp(-up) - (1.0 - smooth) * exp(-down);
-        if (h != h) each = slope = h;
-    } else if (a.kind == NMS_PREFERENCE_HINGE) {
-        each = h < 1.0 ? 1.0 - h : h - h;
-        slope = h < 1.0 ? -1.0 : h - h;
-        if (h > 1.0) each = slope = 0.0;
-    } else {
-        each = (h - 0.5) / beta * ((h - 0.5) / beta);
-        slope = 2.0 * (h - 0.5) / (beta * beta);
-    }
-    if (weight == 0.0) each = slope = 0.0;
-    if (threadIdx.x == 0) {
+    __syncthreads();
+    if (tid == 0) {
+        double l[2], n[2];
+        for (int side = 0; side < 2; ++side) {
+            double sum = 0.0, used = 0.0;
+            for (int w = 0; w < WAVES; ++w) {
+                sum += shared.sum[w][side];
+                used += shared.used[w][side];
+            }
+            n[side] = a.average ? fmax(used, 1.0) : 1.0;
+            l[side] = sum / n[side];
+        }
+        double h;
+        if (forward) {
+            const float *ref = a.ref_logprobs;
+            const double first = l[0] - (ref ? (double)ref[pair] : 0.0);
+            const double second = l[1] - (ref ? (double)ref[other] : 0.0);
+            h = (double)a.beta * (first - second) - (double)a.margin;
+        } else {
+            h = (double)a.known_margins[pair];
+        }
+        const double weight = a.weights ? (double)a.weights[pair] : (double)a.weight;
+        const double beta = (double)a.beta, smooth = (double)a.smoothing;
+        double each, slope;
+        if (a.kind == NMS_PREFERENCE_SIGMOID) {
+            // log(1 + exp(-h)) and log(1 + exp(h)), one of which is near 0
+            const double rest = log1p(exp(-fabs(h)));
+            const double up = rest + fmax(-h, 0.0), down = rest + fmax(h, 0.0);
+            each = (1.0 - smooth) * up + (smooth > 0.0 ? smooth * down : 0.0);
+            slope = smooth * exp(-up) - (1.0 - smooth) * exp(-down);
+            if (h != h) each = slope = h;
+        } else if (a.kind == NMS_PREFERENCE_HINGE) {
+            each = h < 1.0 ? 1.0 - h : h - h;
+            slope = h < 1.0 ? -1.0 : h - h;
+            if (h > 1.0) each = slope = 0.0;
+        } else {
+            each = (h - 0.5) / beta * ((h - 0.5) / beta);
+            slope = 2.0 * (h - 0.5) / (beta * beta);
+        }
+        if (weight == 0.0) each = slope = 0.0;
         space.terms[pair] = weight * each;
         if (a.logprobs) {
-            a.logprobs[pair] = (float)sum[0];
-            a.logprobs[a.pairs + pair] = (float)sum[1];
+            a.logprobs[pair] = (float)l[0];
+            a.logprobs[other] = (float)l[1];
         }
         if (a.margins) a.margins[pair] = (float)h;
+        const double up = a.grad_loss ? (double)a.grad_loss[0] : 1.0;
+        const double by = slope == 0.0 ? 0.0 : up * weight * slope * beta;
+        shared.alpha[0] = (float)(by / n[0]);
+        shared.alpha[1] = (float)(-by / n[1]);
     }
     if (a.grad_logits == nullptr) return;
-    const double up = a.grad_loss ? (double)a.grad_loss[0] : 1.0;
-    for (int side = 0; side < 2; ++side) {
-        const float alpha = (float)((side ? -1.0 : 1.0) * up * weight * slope * beta / n[side]);
-        for (int64_t i = begin[side] + threadIdx.x; i < end[side]; i += TOTAL_THREADS)
-            space.alpha[i] = alpha;
-    }
+    __syncthreads();
+    for (int side = 0; side < 2; ++side)
+        for (int i = begin[side] + tid; i < end[side]; i += TOTAL_THREADS)
+            space.alpha[i] = shared.alpha[side];
     // the rows of no sequence
-    if (pair == 0) {
-        for (int64_t i = threadIdx.x; i < begin[0]; i += TOTAL_THREADS) space.alpha[i] = 0.0f;
-    }
-    if (pair == a.pairs - 1) {
-        for (int64_t i = end[1] + threadIdx.x; i < a.in.rows; i += TOTAL_THREADS)
-            space.alpha[i] = 0.0f;
-    }
+    if (pair == 0)
+        for (int i = tid; i < begin[0]; i += TOTAL_THREADS) space.alpha[i] = 0.0f;
+    if (pair == a.pairs - 1)
+        for (int64_t i = end[1] + tid; i < a.in.rows; i += TOTAL_THREADS) space.alpha[i] = 0.0f;
 }
 
 // ----------------------------------------------------------------- launches
