@@ -159,7 +159,9 @@ __device__ __forceinline__ float base_of(float m) { return m == NEG_INF ? 0.0f :
 
 __device__ __forceinline__ float exp2_of(float u) { return __builtin_amdgcn_exp2f(u); }
 
-// The maximum of three in one instruction, without quietening them first.
+// The maximum of three in one instruction, without quietening them first.  (None
+// of the instructions written here reads what an exponential has just made: the
+// hardware wants a wait there, which the compiler puts before its own only.)
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
@@ -194,6 +196,47 @@ __device__ __forceinline__ double log_of(double s) {
     return s > 0.0 ? y : s == 0.0 ? (double)NEG_INF : s;
 }
 
+// float16 two at a time, converted at the end
+template <int K>
+__device__ __forceinline__ float largest_half(float top, const Pack<half_t> *e) {
+    Pack<half_t> most = e[0];
+#pragma unroll
+    for (int q = 0; q < K; ++q)
+#pragma unroll
+        for (int i = q == 0 ? 1 : 0; i < 4; ++i)
+            asm("v_pk_max_f16 %0, %0, %1" : "+v"(most.w[0]) : "v"(e[q].w[i]));
+    return max3(top, element(most, 0), element(most, 1));
+}
+
+// The largest of some packs' elements and `top`.
+template <typename T, int K>
+__device__ __forceinline__ float largest(float top, const Pack<T> *e) {
+    if constexpr (__is_same(T, half_t)) return largest_half<K>(top, e);
+#pragma unroll
+    for (int q = 0; q < K; ++q)
+#pragma unroll
+        for (int j = 0; j < Pack<T>::N; j += 2)
+            top = max3(top, element(e[q], j), element(e[q], j + 1));
+    return top;
+}
+
+// An element less a base, rounded once.
+template <typename T>
+__device__ __forceinline__ float less(const Pack<T> &e, int j, float base) {
+    return element(e, j) - base;
+}
+// of float16 in one instruction, with its conversion
+__device__ __forceinline__ float less(const Pack<half_t> &e, int j, float base) {
+    float d;
+    if (j % 2)
+        asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+            : "=v"(d) : "v"(e.w[j / 2]), "v"(base));
+    else
+        asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[0,0,0] op_sel_hi:[1,0,0]"
+            : "=v"(d) : "v"(e.w[j / 2]), "v"(base));
+    return d;
+}
+
 // u as a factor of an exponential that is 0 from -150 down
 __device__ __forceinline__ float factor(float u) { return fmaxf(u, -200.0f); }
 
@@ -225,11 +268,7 @@ __device__ __forceinline__ float sum_of(const float *v) {
 template <typename T, bool ENTROPY, int K>
 __device__ __forceinline__ void add_packs(Part &p, const Pack<T> *e, const Scale &k) {
     constexpr int N = Pack<T>::N;
-    float top = p.m;
-#pragma unroll
-    for (int q = 0; q < K; ++q)
-#pragma unroll
-        for (int j = 0; j < N; j += 2) top = max3(top, element(e[q], j), element(e[q], j + 1));
+    const float top = largest<T, K>(p.m, e);
     const float base = base_of(top);
     const Shift f = shift_to(p.m, base, k.hi);
     float s[K], w[K];
@@ -238,8 +277,8 @@ __device__ __forceinline__ void add_packs(Part &p, const Pack<T> *e, const Scale
         float x[N], y[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const float d = element(e[q], j) - base;
-            const float u = fmaf(d, k.hi, d * k.lo);
+            const float d = less(e[q], j, base);
+            const float u = ENTROPY ? d * k.hi : fmaf(d, k.hi, d * k.lo);
             x[j] = exp2_of(u);
             if (ENTROPY) y[j] = factor(u) * x[j];
         }
@@ -329,7 +368,9 @@ __device__ __forceinline__ RowResult result_of(const LossArgs &a, const RowGiven
     RowResult r = {};
     if (!given.counts) return r;
     // in binary64: sums over rows are made of these
-    r.log_s = log_of(p.s);
+    // (with entropies the exponentials are those of k.hi alone: one of k.hi + k.lo is
+    // (1 + ln 2 u k.lo / k.hi) times that, and w is the sum of u times that)
+    r.log_s = log_of(ENTROPY ? p.s + LN2 * (double)(k.lo / k.hi) * p.w : p.s);
     r.exact = p.s == 0.0        ? (double)NEG_INF
               : p.at == NEG_INF ? (double)NEG_INF - r.log_s
                                 : ((double)p.at - (double)p.m) * (double)k.inverse - r.log_s;
@@ -443,10 +484,10 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
     return g;
 }
 
-// The gradient of one logit that is not the token's.
+// The gradient of one logit that is not the token's, from it less the base.
 template <bool ENTROPY>
-__device__ __forceinline__ float gradient_of(float z, const Slope &g) {
-    const float u = (z - g.base) * g.k;
+__device__ __forceinline__ float gradient_of(float less, const Slope &g) {
+    const float u = less * g.k;
     const float x = exp2_of(u);
     return ENTROPY ? x * fmaf(g.Q, factor(u), g.P) : x * g.P;
 }
@@ -457,7 +498,7 @@ __device__ __forceinline__ void to_gradient(Pack<T> &e, const Slope &g) {
     constexpr int N = Pack<T>::N;
     float d[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) d[j] = gradient_of<ENTROPY>(element(e, j), g);
+    for (int j = 0; j < N; ++j) d[j] = gradient_of<ENTROPY>(less(e, j, g.base), g);
     set_elements(e, d);
 }
 
@@ -475,7 +516,7 @@ __device__ __forceinline__ void write_edges(const Row<T> &r, T *dz, const Slope 
     const int i = r.edge(threadIdx.x);
     float d = 0.0f;
     if (g.any) {
-        d = gradient_of<ENTROPY>(to_f32(r.z[i]), g);
+        d = gradient_of<ENTROPY>(to_f32(r.z[i]) - g.base, g);
         if (i == r.token) d += g.more;
     }
     store_one(dz + i, d);
@@ -487,7 +528,7 @@ __device__ __forceinline__ void write_token(const Row<T> &r, T *dz, const Slope 
                                             int end, int group) {
     if (r.token >= lo && r.token < end &&
         (int)threadIdx.x == (r.token - lo) / Pack<T>::N % group)
-        store_one(dz + r.token, gradient_of<ENTROPY>(z, g) + g.more);
+        store_one(dz + r.token, gradient_of<ENTROPY>(z - g.base, g) + g.more);
 }
 
 // ----------------------------------------------------------------- kernels
