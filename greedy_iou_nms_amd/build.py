@@ -46,11 +46,13 @@ FLAGS = [
 # register set compiled to exactly 256 VGPRs and returned wrong kept sets.
 # The team sort's workgroups wait on one another, so all of them must be
 # resident at once; scratch memory could limit that.  The selection kernels
-# keep a row's values in registers (slices that spilled took 72 us for 55).
+# and the losses keep a row's values in registers (slices that spilled took 72 us
+# for 55, rows of a loss 87 for 62).
 GUARDED_KERNELS = ("12sweep_kernel", "17mask_sweep_kernel", "18group_sweep_kernel",
                    "16small_nms_kernel", "16team_sort_kernel", "18team_sample_kernel",
                    "12quick_kernel", "12exact_kernel", "11back_kernel", "13adjust_kernel",
-                   "12slice_kernel", "12whole_kernel", "11join_kernel")
+                   "12slice_kernel", "12whole_kernel", "11join_kernel", "11part_kernel",
+                   "10row_kernel", "15gradient_kernel", "14balance_kernel", "12small_kernel")
 MAX_VGPRS = 255
 
 

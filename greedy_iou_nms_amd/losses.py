@@ -76,11 +76,11 @@ def _balance_workspace_size(tokens: int, experts: int, sequences: int, top_k: in
     return int(out.value)
 
 
-def _space(nbytes: int, device, stream: int) -> int:
-    """The address of a workspace: kept per thread and stream; a captured call
-    takes one of its own from the graph's memory, so that no two graphs share it."""
+def _space(nbytes: int, device, stream: int) -> torch.Tensor:
+    """A workspace, kept per thread and stream; a captured call takes one of its
+    own from the graph's memory, so that no two graphs share it."""
     kept = Workspace(device) if _capturing() else _default_workspace(device, stream, "loss")
-    return kept.get(nbytes, device).data_ptr()
+    return kept.get(nbytes, device)
 
 
 def _constant(name: str, **tensors) -> None:
@@ -159,9 +159,10 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor,
     stream = _raw_stream(device)
     logprobs = torch.empty(rows, dtype=torch.float32, device=device)
     entropies = torch.empty_like(logprobs) if entropy else None
+    space = _space(nbytes, device, stream)
     status = _lib.nms_token_logprobs(logits.data_ptr(), code, rows, vocab, stride, a, t,
                                      logprobs.data_ptr(), _address(entropies),
-                                     _space(nbytes, device, stream), nbytes, stream)
+                                     space.data_ptr(), nbytes, stream)
     if status:
         _check(status)
     return (logprobs, entropies) if entropy else logprobs
@@ -216,9 +217,10 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor,
     nbytes = _loss_workspace_size(rows, vocab, 0)
     out, out_stride = _gradient_of(logits, rows, vocab, stride, out, "token_logprobs_backward")
     stream = _raw_stream(device)
+    space = _space(nbytes, device, stream)
     status = _lib.nms_token_logprobs_backward(
         logits.data_ptr(), code, rows, vocab, stride, a, t, g, h, out.data_ptr(), out_stride,
-        _space(nbytes, device, stream), nbytes, stream)
+        space.data_ptr(), nbytes, stream)
     if status:
         _check(status)
     return out
@@ -255,10 +257,11 @@ def _run_policy(logits, tokens, old_logprobs, advantages, weights, ref_logprobs,
     logprobs = torch.empty_like(old_logprobs) if results else None
     entropies = torch.empty_like(old_logprobs) if results and entropy is not None else None
     stream = _raw_stream(device)
+    space = _space(nbytes, device, stream)
     status = _lib.nms_policy_loss(
         logits.data_ptr(), code, rows, vocab, stride, a, old, adv, w, ref, t, options, up,
         _address(loss), _address(logprobs), _address(entropies), _address(grad), grad_stride,
-        _space(nbytes, device, stream), nbytes, stream)
+        space.data_ptr(), nbytes, stream)
     if status:
         _check(status)
     return loss, grad, logprobs, entropies
@@ -372,15 +375,17 @@ def _run_preference(logits, tokens, offsets, ref_logprobs, weights, options, gra
         loss = _scalar(device)
         logprobs = torch.empty(n, dtype=torch.float32, device=device)
         margins = torch.empty(n // 2, dtype=torch.float32, device=device)
+        space = _space(nbytes, device, stream)
         status = _lib.nms_preference_loss(
             logits.data_ptr(), code, rows, vocab, stride, a, at, n // 2, ref, w, ref_options, up,
             loss.data_ptr(), logprobs.data_ptr(), margins.data_ptr(), _address(grad), grad_stride,
-            _space(nbytes, device, stream), nbytes, stream)
+            space.data_ptr(), nbytes, stream)
     else:
+        space = _space(nbytes, device, stream)
         status = _lib.nms_preference_loss_backward(
             logits.data_ptr(), code, rows, vocab, stride, a, at, n // 2, w, ref_options,
             margins.data_ptr(), up, grad.data_ptr(), grad_stride,
-            _space(nbytes, device, stream), nbytes, stream)
+            space.data_ptr(), nbytes, stream)
     if status:
         _check(status)
     return loss, grad, logprobs, margins
@@ -507,10 +512,11 @@ def _run_balance(logits, ids, counts, score, balance, z, offsets, live, grad_los
     if counts is None and results:
         counts = torch.empty(shape, dtype=torch.int32, device=device)
     stream = _raw_stream(device)
+    space = _space(nbytes, device, stream)
     status = _lib.nms_balance_loss(
         logits.data_ptr(), code, tokens, experts, stride, chosen, alive, at, sequences, options,
         up, _address(loss), _address(counts), _address(grad), grad_stride,
-        _space(nbytes, device, stream), nbytes, stream)
+        space.data_ptr(), nbytes, stream)
     if status:
         _check(status)
     return loss, grad, counts

@@ -609,7 +609,8 @@ nms_status nms_pick_tokens(const void *logits, nms_dtype dtype, int64_t rows, in
  * -infinity and entropy and gradient are 0.  A temperature of 0 or below, or
  * NaN, counts as 1 (the log probability that nms_pick_tokens gives for it); at
  * +infinity all tokens but those at -infinity weigh alike.
- * Terms are computed in float32, sums over rows in binary64.
+ * Terms are computed in float32, sums over rows in binary64; a probability
+ * below 2^-126 of the row's largest counts as 0.
  *
  * grad_logits: device, rows of elements of dtype, grad_stride elements apart,
  * every element is written (0 in rows that do not count); may be logits, with

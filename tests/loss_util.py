@@ -11,7 +11,9 @@ probability and X1, X2 the sums of p x and p x^2 of a row:
 * a log probability: that of log s, 3 U of (m - z) / t, and its own rounding;
 * an entropy log s - ln 2 w / s: w's terms have 2 U more each;
 * a gradient p (...) / t: its exponential, 1 / s and six products and sums;
-  then once to the logits' type, half a step of it.
+  then once to the logits' type, half a step of it.  An exponential below
+  2^-126 of the largest is 0 (the instruction has no subnormal results), which
+  takes at most 2^-126 of (...) / t off, as s is 1 at least.
 """
 import numpy as np
 
@@ -72,6 +74,7 @@ class Bounds:
             y = np.stack([plain.log_softmax(z[r], self.t[r]) for r in range(T)])
             p = np.exp(y)
             self.x = np.where(p > 0, x, 0.0)
+            self.s0 = np.full(T, np.log(V))  # log s at most
             self.y = np.where(p > 0, y, 0.0)
         self.p = np.where(np.isfinite(p), p, 0.0)
         x1, x2 = (self.p * self.x).sum(1), (self.p * self.x ** 2).sum(1)
@@ -90,6 +93,8 @@ class Bounds:
         per = self.p / self.t[:, None]
         size = per * (g + h * (np.abs(self.y) + self.h[:, None]))
         err = rel * size + per * h * self.entropy[:, None]
+        y = np.where(np.isfinite(self.x), self.x, 0.0) + self.s0[:, None]
+        err += 2.0 ** -126 * (g + h * (y + self.h[:, None])) / self.t[:, None]
         err += np.abs(self.dlp) * (np.broadcast_to(dg, self.lp.shape)[:, None] + 3 * U * g)
         half = torch.finfo(dtype).eps / 2
         return np.nan_to_num(err * (1 + half) + half * np.abs(want)) + SMALL[dtype]

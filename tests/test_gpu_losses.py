@@ -15,7 +15,11 @@ pytestmark = pytest.mark.gpu
 # boundary of 8, 64, 256 elements, rows that split into slices and those that do not
 SHAPES = [(1, 1), (3, 1), (5, 2), (4, 7), (3, 8), (2, 9), (7, 63), (5, 64), (3, 65), (33, 257),
           (1, 1000), (9, 2047), (2, 2049), (3, 4097), (2, 8191), (1, 32000), (2, 100003),
-          (2100, 41), (2500, 130), (70, 5001)]
+          (2100, 41), (2500, 130), (70, 5001),
+          # around the sizes that a workgroup of 64, 128, 512 and 1024 threads holds
+          (3, 1024), (2, 1025), (3, 2048), (2, 2049), (2, 4096), (3, 4097), (2, 8192), (2, 8193),
+          (2, 16384), (2, 16385), (2, 32768), (2, 32769), (64, 40000), (70, 66000), (3, 65536),
+          (2, 65537), (96, 70001), (2, 131072), (2, 131073), (1, 262144), (2, 300007)]
 
 
 def tokens_of(rng, T, V, masked=0.2):
