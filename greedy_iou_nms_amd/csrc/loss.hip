@@ -637,8 +637,15 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
 // A workgroup per row: its results and, with GRADIENT, its gradient.  The first
 // HELD packs of each thread stay in registers between the two, the others are
 // read again.
+// Waves of a vector unit: as many as leave the registers that the packs and a
+// chunk of 16 exponentials need (with entropies also 16 products; chunks of 8
+// of them take fewer, but 224 us for 215 at 4096 x 65536 float16).
+constexpr int waves_of(bool entropy, int held) {
+    return held <= 4 ? 8 - entropy : held <= 8 ? 6 - entropy : 4;
+}
+
 template <typename T, bool ENTROPY, bool GRADIENT, bool STREAM, int GROUP, int HELD>
-__global__ __launch_bounds__(GROUP, HELD <= 4 ? 8 : HELD <= 8 ? 6 : 4) void row_kernel(LossArgs a, LossSpace space) {
+__global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(LossArgs a, LossSpace space) {
     constexpr int N = Pack<T>::N, UNROLL = 16 / N, SPAN = GROUP * N;
     constexpr int CHUNK = HELD < UNROLL ? HELD : UNROLL;
     static_assert(HELD % CHUNK == 0, "whole chunks");
