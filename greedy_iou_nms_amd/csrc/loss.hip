@@ -23,9 +23,11 @@ constexpr double LN2 = 0.693147180559945309;
 
 // The largest logit m of a part of a row, the sum s of the exponentials and the
 // weighted sum w.  m may be -infinity (no logit above it); then s and w are 0,
-// or NaN where one was NaN.  The sums of 32 exponentials at a time are added up
-// in binary64: in float32 the thread with the row's largest logit, 1 of the
-// sum, lost 2^-24 of the log probability with each of its other sums.
+// or NaN where one was NaN.  s is a sum in binary64 of float32 exponentials:
+// where the largest logit, 1 of the sum, is the token's, log s is what the others
+// add to 1, and float32 loses 2^-25 with each (of log probabilities around -0.01
+// 6e-6 of the value for 6e-8; 2 % of the time where entropies are wanted, none
+// where memory is the bound).
 // at: the logit of the row's token, which a gradient in place of the logits
 // overwrites.
 struct Part {
@@ -240,14 +242,22 @@ __device__ __forceinline__ float less(const Pack<half_t> &e, int j, float base) 
 // u as a factor of an exponential that is 0 from -150 down
 __device__ __forceinline__ float factor(float u) { return fmaxf(u, -200.0f); }
 
+// u of a logit less the largest one.  (With entropies by k.hi alone: w is at hand
+// then, and corrects the sum at the end.)
+template <bool ENTROPY>
+__device__ __forceinline__ float scaled(float d, const Scale &k) {
+    return ENTROPY ? d * k.hi : fmaf(d, k.hi, d * k.lo);
+}
+
 // What a part's sums are multiplied by, and w's are shifted by, when its
 // largest logit becomes top.
 struct Shift {
     double by;
     float u;
 };
-__device__ __forceinline__ Shift shift_to(float m, float top, float k) {
-    const float u = m == NEG_INF ? 0.0f : (m - top) * k;
+template <bool ENTROPY>
+__device__ __forceinline__ Shift shift_to(float m, float top, const Scale &k) {
+    const float u = m == NEG_INF ? 0.0f : scaled<ENTROPY>(m - top, k);
     return {(double)exp2_of(u), factor(u)};
 }
 
@@ -270,23 +280,25 @@ __device__ __forceinline__ void add_packs(Part &p, const Pack<T> *e, const Scale
     constexpr int N = Pack<T>::N;
     const float top = largest<T, K>(p.m, e);
     const float base = base_of(top);
-    const Shift f = shift_to(p.m, base, k.hi);
-    float s[K], w[K];
+    const Shift f = shift_to<ENTROPY>(p.m, base, k);
+    float w[K];
+    double sum = 0.0;
 #pragma unroll
     for (int q = 0; q < K; ++q) {
         float x[N], y[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const float d = less(e[q], j, base);
-            const float u = ENTROPY ? d * k.hi : fmaf(d, k.hi, d * k.lo);
+            const float u = scaled<ENTROPY>(d, k);
             x[j] = exp2_of(u);
             if (ENTROPY) y[j] = factor(u) * x[j];
         }
-        s[q] = sum_of<N>(x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum += (double)x[j];
         if (ENTROPY) w[q] = sum_of<N>(y);
     }
     if (ENTROPY) p.w = (p.w + (double)f.u * p.s) * f.by + (double)sum_of<K>(w);
-    p.s = p.s * f.by + (double)sum_of<K>(s);
+    p.s = p.s * f.by + sum;
     p.m = top;
 }
 
@@ -294,7 +306,7 @@ __device__ __forceinline__ void add_packs(Part &p, const Pack<T> *e, const Scale
 template <bool ENTROPY>
 __device__ __forceinline__ Part join_wave(Part p, const Scale &k) {
     const float top = wave_max(p.m);
-    const Shift f = shift_to(p.m, top, k.hi);
+    const Shift f = shift_to<ENTROPY>(p.m, top, k);
     if (ENTROPY) p.w = wave_sum((p.w + (double)f.u * p.s) * f.by);
     p.s = wave_sum(p.s * f.by);
     p.m = top;
@@ -460,12 +472,13 @@ size_t lay_out(int64_t rows, int vocab, int64_t pairs, void *at, LossSpace *s) {
 
 // ---------------------------------------------------------------- gradient
 
-// What makes a row's gradient: dz_j = e_j (P + Q u_j), and `more` at the token;
-// any: it is not 0.  (A whole word: bytes behind it were copied through LDS at
+// What makes a row's gradient: dz_j = e_j (P + Q u_j), but for the token's, which
+// is made in binary64: where its probability is near 1, it is a difference of
+// nearly equal ones.  any: the gradient is not 0.  (A whole word: bytes behind it were copied through LDS at
 // the thread's number, for which every workgroup read the launch's packet in
 // host memory: 256 x 32000 25 us for 17.)
 struct Slope {
-    float base, k, P, Q, more;
+    float base, k, P, Q, token;
     int any;
 };
 
@@ -478,9 +491,13 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
     g.k = k.hi;
     const double per = (double)k.inverse * inverse_of(p.s);
     const double eta = ENTROPY ? (double)r.eta : 0.0;
-    g.P = (float)(-((double)r.alpha + eta * ((double)r.entropy - r.log_s)) * per);
-    g.Q = ENTROPY ? (float)(-eta * LN2 * per) : 0.0f;
-    g.more = r.alpha * k.inverse;
+    const double P = -((double)r.alpha + eta * ((double)r.entropy - r.log_s)) * per;
+    const double Q = -eta * LN2 * per;
+    const float u = factor((p.at - g.base) * g.k);
+    g.P = (float)P;
+    g.Q = (float)Q;
+    g.token = (float)((double)r.alpha * (double)k.inverse +
+                      (double)exp2_of(u) * (P + Q * (double)u));
     return g;
 }
 
@@ -516,19 +533,18 @@ __device__ __forceinline__ void write_edges(const Row<T> &r, T *dz, const Slope 
     const int i = r.edge(threadIdx.x);
     float d = 0.0f;
     if (g.any) {
-        d = gradient_of<ENTROPY>(to_f32(r.z[i]) - g.base, g);
-        if (i == r.token) d += g.more;
+        d = i == r.token ? g.token : gradient_of<ENTROPY>(to_f32(r.z[i]) - g.base, g);
     }
     store_one(dz + i, d);
 }
 
 // The token's gradient, over what its pack's thread has written there.
-template <typename T, bool ENTROPY>
-__device__ __forceinline__ void write_token(const Row<T> &r, T *dz, const Slope &g, float z, int lo,
-                                            int end, int group) {
+template <typename T>
+__device__ __forceinline__ void write_token(const Row<T> &r, T *dz, const Slope &g, int lo, int end,
+                                            int group) {
     if (r.token >= lo && r.token < end &&
         (int)threadIdx.x == (r.token - lo) / Pack<T>::N % group)
-        store_one(dz + r.token, gradient_of<ENTROPY>(z - g.base, g) + g.more);
+        store_one(dz + r.token, g.token);
 }
 
 // ----------------------------------------------------------------- kernels
@@ -613,14 +629,12 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
     const int lo = (int)blockIdx.y * size;
     const int end = min(lo + size, r.size);
     Slope g = {};
-    float at_token = 0.0f;
     if (given.counts || results) {
         const Part p = row_part<ENTROPY>(space, row, part_slices, k);
         const RowResult result = result_of<ENTROPY>(a, given, p, k);
         if (results && blockIdx.y == 0 && threadIdx.x == 0)
             write_result<ENTROPY>(a, row, result, nullptr, space.terms);
         g = slope_of<ENTROPY>(result, p, k, given.counts);
-        at_token = p.at;
     }
     if (blockIdx.y == 0) write_edges<T, ENTROPY>(r, dz, g);
     for (int i = lo + (int)threadIdx.x * N; i < end; i += THREADS * N) {
@@ -631,7 +645,7 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
         }
         store_pack<STREAM>(dz + i, e);
     }
-    if (g.any) write_token<T, ENTROPY>(r, dz, g, at_token, lo, end, THREADS);
+    if (g.any) write_token<T>(r, dz, g, lo, end, THREADS);
 }
 
 // A workgroup per row: its results and, with GRADIENT, its gradient.  The first
@@ -660,9 +674,8 @@ __global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(Los
     T *dz = static_cast<T *>(a.grad_logits) + row * a.grad_stride + r.head;
     Pack<T> held[HELD];
     Slope g = {};
-    float at_token = 0.0f;
     if (given.counts) {
-        at_token = r.at_token();
+        const float at_token = r.at_token();
 #pragma unroll
         for (int c = 0; c < HELD; c += CHUNK)
             if (c == 0 || c * SPAN < V) {
@@ -719,7 +732,7 @@ __global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(Los
         to_gradient<T, ENTROPY>(e, g);
         store_pack<STREAM>(dz + i, e);
     }
-    write_token<T, ENTROPY>(r, dz, g, at_token, 0, V, GROUP);
+    write_token<T>(r, dz, g, 0, V, GROUP);
 }
 
 // ---------------------------------------------------------- sums of a loss
