@@ -547,6 +547,29 @@ __device__ __forceinline__ void write_token(const Row<T> &r, T *dz, const Slope 
         store_one(dz + r.token, g.token);
 }
 
+// ---------------------------------------------------------- sums of a loss
+
+constexpr int TOTAL_THREADS = 1024;
+
+// The sum of n terms by a workgroup of GROUP threads, in a fixed order.
+template <int GROUP>
+__device__ __forceinline__ void write_total(const double *terms, int64_t n, float *out) {
+    __shared__ double shared[GROUP / 64];
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += GROUP) sum += terms[i];
+    sum = wave_sum(sum);
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int q = 1; q < GROUP / 64; ++q) sum += shared[q];
+    out[0] = (float)sum;
+}
+
+__global__ __launch_bounds__(TOTAL_THREADS) void total_kernel(const double *terms, int64_t n,
+                                                              float *out) {
+    write_total<TOTAL_THREADS>(terms, n, out);
+}
+
 // ----------------------------------------------------------------- kernels
 
 // A workgroup per (row, slice): the slice's part, and where it is the row's
@@ -613,14 +636,19 @@ __global__ __launch_bounds__(THREADS) void finish_kernel(LossArgs a, LossSpace s
 }
 
 // A workgroup per (row, slice): the gradient in its logits; the first of a
-// row writes the row's results.
+// row writes the row's results.  With `pairs`, workgroups behind the rows' add up
+// the terms of so many pairs, which would be a launch of its own else.
 template <typename T, bool ENTROPY, bool STREAM>
 __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace space,
                                                            int part_slices, int slices,
-                                                           bool results) {
+                                                           bool results, int64_t pairs) {
     constexpr int N = Pack<T>::N;
+    if ((int64_t)blockIdx.x >= a.in.rows) {
+        if (blockIdx.y == 0) write_total<THREADS>(space.terms, pairs, a.loss);
+        return;
+    }
     // the rows that were read last are still in the last cache
-    const int64_t row = (int64_t)gridDim.x - 1 - blockIdx.x;
+    const int64_t row = a.in.rows - 1 - blockIdx.x;
     const RowGiven given = given_of<ENTROPY>(a, row);
     const Scale k = scale_of(a.in, row);
     const Row<T> r(a.in, row, given.token);
@@ -637,13 +665,19 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
         g = slope_of<ENTROPY>(result, p, k, given.counts);
     }
     if (blockIdx.y == 0) write_edges<T, ENTROPY>(r, dz, g);
-    for (int i = lo + (int)threadIdx.x * N; i < end; i += THREADS * N) {
-        Pack<T> e = {};
+    constexpr int SPAN = THREADS * N, UNROLL = 4;
+    for (int i = lo + (int)threadIdx.x * N; i < end; i += UNROLL * SPAN) {
+        Pack<T> e[UNROLL] = {};
         if (g.any) {
-            e = load_pack<STREAM>(r.z + i, true);
-            to_gradient<T, ENTROPY>(e, g);
+#pragma unroll
+            for (int q = 0; q < UNROLL; ++q)
+                e[q] = load_pack<STREAM>(r.z + i + q * SPAN, i + q * SPAN < end);
+#pragma unroll
+            for (int q = 0; q < UNROLL; ++q) to_gradient<T, ENTROPY>(e[q], g);
         }
-        store_pack<STREAM>(dz + i, e);
+#pragma unroll
+        for (int q = 0; q < UNROLL; ++q)
+            if (i + q * SPAN < end) store_pack<STREAM>(dz + i + q * SPAN, e[q]);
     }
     if (g.any) write_token<T>(r, dz, g, lo, end, THREADS);
 }
@@ -733,30 +767,6 @@ __global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(Los
         store_pack<STREAM>(dz + i, e);
     }
     write_token<T>(r, dz, g, 0, V, GROUP);
-}
-
-// ---------------------------------------------------------- sums of a loss
-
-constexpr int TOTAL_THREADS = 1024;
-
-// The sum over the workgroup, in a fixed order, the same in every thread.
-__device__ __forceinline__ double block_sum(double v, double *shared) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double sum = 0.0;
-    for (int q = 0; q < (int)blockDim.x / 64; ++q) sum += shared[q];
-    return sum;
-}
-
-__global__ __launch_bounds__(TOTAL_THREADS) void total_kernel(const double *terms, int64_t n,
-                                                              float *out) {
-    __shared__ double shared[TOTAL_THREADS / 64];
-    double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += TOTAL_THREADS) sum += terms[i];
-    sum = block_sum(sum, shared);
-    if (threadIdx.x == 0) out[0] = (float)sum;
 }
 
 // -------------------------------------------------------------- preference
@@ -950,18 +960,18 @@ int run_parts(const LossArgs &a, const LossSpace &s, bool results, hipStream_t s
     return slices;
 }
 
-// The gradient from the parts.
+// The gradient from the parts; pairs: of those whose terms make a.loss.
 template <typename T, bool ENTROPY>
-void run_gradient(const LossArgs &a, const LossSpace &s, int parts, bool results,
+void run_gradient(const LossArgs &a, const LossSpace &s, int parts, bool results, int64_t pairs,
                   hipStream_t stream) {
     const int slices = slices_of(a.in.rows, a.in.vocab);
-    const dim3 grid((unsigned)a.in.rows, (unsigned)slices);
+    const dim3 grid((unsigned)(a.in.rows + (pairs > 0)), (unsigned)slices);
     if (a.in.rows * row_bytes(a.in) > STREAMED_TWICE)
         gradient_kernel<T, ENTROPY, true>
-            <<<grid, THREADS, 0, stream>>>(a, s, parts, slices, results);
+            <<<grid, THREADS, 0, stream>>>(a, s, parts, slices, results, pairs);
     else
         gradient_kernel<T, ENTROPY, false>
-            <<<grid, THREADS, 0, stream>>>(a, s, parts, slices, results);
+            <<<grid, THREADS, 0, stream>>>(a, s, parts, slices, results, pairs);
 }
 
 template <typename T, bool ENTROPY>
@@ -976,7 +986,7 @@ void run(const LossArgs &a, hipStream_t stream) {
         run_rows<T, ENTROPY>(a, s, stream);
     } else {
         const int parts = run_parts<T, ENTROPY>(a, s, false, stream);
-        run_gradient<T, ENTROPY>(a, s, parts, a.logprobs || a.entropies || a.loss, stream);
+        run_gradient<T, ENTROPY>(a, s, parts, a.logprobs || a.entropies || a.loss, 0, stream);
     }
 }
 
@@ -999,21 +1009,24 @@ void run_preference(const PreferenceArgs &a, hipStream_t stream) {
     int parts = 1;
     if (forward && some) parts = run_parts<T, false>(rows, of_rows, true, stream);
     pair_kernel<<<(unsigned)a.pairs, TOTAL_THREADS, 0, stream>>>(a, s);
-    if (forward) launch_total(s.terms, a.pairs, a.loss, stream);
-    if (a.grad_logits == nullptr || !some) return;
+    if (a.grad_logits == nullptr || !some) {
+        if (forward) launch_total(s.terms, a.pairs, a.loss, stream);
+        return;
+    }
     rows.kind = LOSS_GIVEN;
     rows.grad_logprobs = s.alpha;
     rows.grad_logits = a.grad_logits;
     rows.grad_stride = a.grad_stride;
     if (forward) {
-        run_gradient<T, false>(rows, of_rows, parts, false, stream);
+        rows.loss = a.loss;
+        run_gradient<T, false>(rows, s, parts, false, a.pairs, stream);
     } else {
         of_rows.exact = nullptr;
         if (held_for_gradient(a.in)) {
             run_rows<T, false>(rows, of_rows, stream);
         } else {
             parts = run_parts<T, false>(rows, of_rows, false, stream);
-            run_gradient<T, false>(rows, of_rows, parts, false, stream);
+            run_gradient<T, false>(rows, of_rows, parts, false, 0, stream);
         }
     }
 }
