@@ -161,9 +161,7 @@ __device__ __forceinline__ float base_of(float m) { return m == NEG_INF ? 0.0f :
 
 __device__ __forceinline__ float exp2_of(float u) { return __builtin_amdgcn_exp2f(u); }
 
-// The maximum of three in one instruction, without quietening them first.  (None
-// of the instructions written here reads what an exponential has just made: the
-// hardware wants a wait there, which the compiler puts before its own only.)
+// The maximum of three in one instruction, without quietening them first.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
@@ -239,6 +237,15 @@ __device__ __forceinline__ float less(const Pack<half_t> &e, int j, float base) 
     return d;
 }
 
+// u x for an exponential x = 2^u: 0 where u is -infinity, by the multiplication
+// whose product with 0 is 0.  What the exponential has just made may be read after
+// a wait only, which the compiler puts before its own instructions and not here.
+__device__ __forceinline__ float times_exponential(float u, float x) {
+    float d;
+    asm("s_nop 0\n\tv_mul_legacy_f32 %0, %1, %2" : "=v"(d) : "v"(u), "v"(x));
+    return d;
+}
+
 // u as a factor of an exponential that is 0 from -150 down
 __device__ __forceinline__ float factor(float u) { return fmaxf(u, -200.0f); }
 
@@ -291,7 +298,7 @@ __device__ __forceinline__ void add_packs(Part &p, const Pack<T> *e, const Scale
             const float d = less(e[q], j, base);
             const float u = scaled<ENTROPY>(d, k);
             x[j] = exp2_of(u);
-            if (ENTROPY) y[j] = factor(u) * x[j];
+            if (ENTROPY) y[j] = times_exponential(u, x[j]);
         }
 #pragma unroll
         for (int j = 0; j < N; ++j) sum += (double)x[j];
@@ -506,7 +513,7 @@ template <bool ENTROPY>
 __device__ __forceinline__ float gradient_of(float less, const Slope &g) {
     const float u = less * g.k;
     const float x = exp2_of(u);
-    return ENTROPY ? x * fmaf(g.Q, factor(u), g.P) : x * g.P;
+    return ENTROPY ? times_exponential(fmaf(g.Q, u, g.P), x) : x * g.P;
 }
 
 // A pack of logits becomes its gradient, but for what the token's has more.
@@ -689,7 +696,7 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
 // chunk of 16 exponentials need (with entropies also 16 products; chunks of 8
 // of them take fewer, but 224 us for 215 at 4096 x 65536 float16).
 constexpr int waves_of(bool entropy, int held) {
-    return held <= 4 ? 8 - entropy : held <= 8 ? 6 - entropy : 4;
+    return held <= 4 ? 8 - 2 * entropy : held <= 8 ? 6 - entropy : 4;
 }
 
 template <typename T, bool ENTROPY, bool GRADIENT, bool STREAM, int GROUP, int HELD>
