@@ -381,10 +381,13 @@ def test_sizes_past_the_caches(T, V, dtype):
     note("past the caches %d %d %s" % (T, V, dtype))
     rng = np.random.default_rng(10)
     g = lib()
-    z = torch.randn(T, V, device=device()).mul_(2.5).to(dtype)
+    seeded = torch.Generator(device=device())
+    seeded.manual_seed(T)
+    z = torch.randn(T, V, generator=seeded, device=device()).mul_(2.5).to(dtype)
     tokens = tokens_of(rng, T, V)
     w = (rng.random(T) * (rng.random(T) < 0.8)).astype(np.float32)
-    old = (-10 + rng.normal(size=T)).astype(np.float32)
+    # (ratios near 1: 64 w A times one of 10^4 is past float16)
+    old = (host(g.token_logprobs(z, dev(tokens))) + 0.4 * rng.normal(size=T)).astype(np.float32)
     adv = rng.normal(size=T).astype(np.float32)
     at = np.array([0, T // 4, T // 2, 3 * T // 4, T - 3], np.int64)
     rows = np.array([0, 1, T // 2, T - 2, T - 1] + rng.integers(0, T, 5).tolist())
