@@ -10,6 +10,11 @@
 //     softmax:  dz_j = s_j (a_j - sum a s)
 //     sigmoid:  dz_j = s_j (1 - sigmoid_j) (a_j - sum a s)
 //     both:     + 2 z / N lse softmax_j.
+// What bounds it is the caller's time: three or four launches (3.3 us each), three
+// outputs and the binding take 18 to 21 us, the kernels about as long.  Of these,
+// 16384 x 256 float32 in 16 sequences: counting 6.8 us (five trips to memory one
+// after another), the pass 11.2 us for 33 MB (350 instructions for a wave's two
+// tokens), the sum 1.5.
 #include "loss_internal.h"
 
 #pragma clang fp contract(off)
@@ -47,7 +52,8 @@ int lanes_of(int experts) {
     return experts <= 64 ? 8 : experts <= 128 ? 16 : experts <= 256 ? 32 : 64;
 }
 
-// Tokens that a group of lanes takes in turn, their logits loaded together.
+// Tokens that a group of lanes takes in turn, their logits loaded together: 131072 x
+// 128 float32 43.1 us with four, 44.3 with one; of fewer tokens it makes no odds.
 int turns_of(int64_t tokens, int experts) {
     return tokens * lanes_of(experts) >= (int64_t)4096 * MT ? 4 : 1;
 }
@@ -392,7 +398,9 @@ __global__ __launch_bounds__(MT) void balance_kernel(BalanceArgs a, BalanceSpace
     }
 }
 
-// All of a small call in one workgroup.
+// All of a small call in one workgroup, which saves two launches: 512 x 64 in 13.0
+// us of the caller's time for 18.4, though in a graph it takes 9.0 for 8.0 (16 x 64
+// 4.9 for 7.1); 1024 x 64 would take 14.2 for 8.5.
 template <typename T, int LANES, int VALUES>
 __global__ __launch_bounds__(CT) void small_kernel(BalanceArgs a) {
     __shared__ int hist[NMS_ROUTE_MAX_EXPERTS];

@@ -8,8 +8,19 @@
 // and, where alpha and eta are the gradients in these two,
 //     dz_j = e_j (P + Q u_j) + [j = token] alpha / t,
 //     P = -(alpha + eta (entropy - log s)) / (s t),  Q = -eta ln 2 / (s t).
-// So a row is read once for its (m, s, w), which join by rescaling, and once
-// more for its gradient.
+// So a row is looked through for its (m, s, w), which join by rescaling, and then
+// for its gradient.  Memory is the bound: 6.5 vector instructions an element for
+// the sums and 5.5 for the gradient, with an exponential that takes the time of
+// two, are 57 % of the vector units' time where rows are read and written at a
+// copy's rate (with entropies 9.5 for the sums, 84 % where rows are only read).
+// Hence
+//   * row_kernel, a workgroup that holds a row in its registers in between: logits
+//     are read once and the gradient is written once, 4096 x 131072 bfloat16 in 390 us
+//     for 2.04 GB, a copy's 5.2 TB/s;
+//   * part_kernel and gradient_kernel, which read a row twice: where a loss needs
+//     all rows before any gradient (preference), where the rows are few and a row is
+//     shared by workgroups, and, the first alone, for results of long rows (4097 x
+//     131072 with entropies 189 us, 5.7 TB/s).
 #include "loss_internal.h"
 
 #pragma clang fp contract(off)
@@ -481,9 +492,9 @@ size_t lay_out(int64_t rows, int vocab, int64_t pairs, void *at, LossSpace *s) {
 
 // What makes a row's gradient: dz_j = e_j (P + Q u_j), but for the token's, which
 // is made in binary64: where its probability is near 1, it is a difference of
-// nearly equal ones.  any: the gradient is not 0.  (A whole word: bytes behind it were copied through LDS at
-// the thread's number, for which every workgroup read the launch's packet in
-// host memory: 256 x 32000 25 us for 17.)
+// nearly equal ones.  any: the gradient is not 0.  (A whole word: the bytes behind
+// a smaller one were copied through LDS at the thread's number, for which every
+// workgroup read the launch's packet in host memory: 256 x 32000 25 us for 13.)
 struct Slope {
     float base, k, P, Q, token;
     int any;
@@ -689,9 +700,6 @@ __global__ __launch_bounds__(THREADS) void gradient_kernel(LossArgs a, LossSpace
     if (g.any) write_token<T>(r, dz, g, lo, end, THREADS);
 }
 
-// A workgroup per row: its results and, with GRADIENT, its gradient.  The first
-// HELD packs of each thread stay in registers between the two, the others are
-// read again.
 // Waves of a vector unit: as many as leave the registers that the packs and a
 // chunk of 16 exponentials need (with entropies also 16 products; chunks of 8
 // of them take fewer, but 224 us for 215 at 4096 x 65536 float16).
@@ -699,8 +707,14 @@ constexpr int waves_of(bool entropy, int held) {
     return held <= 4 ? 8 - 2 * entropy : held <= 8 ? 6 - entropy : 4;
 }
 
+// A workgroup per row: its results and, with GRADIENT, its gradient.  The first
+// HELD packs of each thread stay in registers between the two, the others are
+// read again.  All of them are asked for at once: a row's time is one trip to
+// memory, its two passes of instructions (2 and 2.1 us for 32000 elements by 256
+// threads) and 0.9 us for its results, which other rows of the compute unit fill.
 template <typename T, bool ENTROPY, bool GRADIENT, bool STREAM, int GROUP, int HELD>
-__global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(LossArgs a, LossSpace space) {
+__global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(LossArgs a,
+                                                                             LossSpace space) {
     constexpr int N = Pack<T>::N, UNROLL = 16 / N, SPAN = GROUP * N;
     constexpr int CHUNK = HELD < UNROLL ? HELD : UNROLL;
     static_assert(HELD % CHUNK == 0, "whole chunks");
@@ -732,7 +746,8 @@ __global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(Los
         for (int i = HELD * SPAN + first; i < V; i += UNROLL * SPAN) {
             Pack<T> e[UNROLL];
 #pragma unroll
-            for (int q = 0; q < UNROLL; ++q) e[q] = load_pack<false>(r.z + i + q * SPAN, i + q * SPAN < V);
+            for (int q = 0; q < UNROLL; ++q)
+                e[q] = load_pack<false>(r.z + i + q * SPAN, i + q * SPAN < V);
             add_packs<T, ENTROPY, UNROLL>(p, e, k);
         }
         p = GROUP == 64 ? join_wave<ENTROPY>(p, k) : join_group<ENTROPY, GROUP / 64>(p, k, shared);
@@ -905,9 +920,9 @@ bool held_for_results(const LossRows &in) {
     return row_bytes(in) <= 65536 || (row_bytes(in) <= 131072 && in.rows >= 64);
 }
 
-// For the gradient, which slices read a second time: 256 x 131072 bfloat16 29.6
-// us, 38.9 by slices; 4096 x 131072 398 and 611.  Few long rows leave the GPU
-// empty: 16 x 131072 19.1 and 10.0, 64 x 131072 21.9 and 18.1, 96 even.
+// For the gradient, which slices read a second time: policy loss of 256 x 131072
+// bfloat16 29.6 us, 38.9 by slices; of 4096 x 131072 395 and 611.  Few long rows
+// leave the GPU empty: 16 x 131072 19.1 and 10.0, 64 x 131072 21.9 and 17.2, 96 even.
 bool held_for_gradient(const LossRows &in) {
     return row_bytes(in) <= 65536 || in.rows >= (row_bytes(in) <= 131072 ? 64 : 96);
 }
@@ -935,10 +950,10 @@ void launch_rows(const LossArgs &a, const LossSpace &s, hipStream_t stream) {
 // Logits of more bytes than this pass the caches when they are read for the last
 // time, and so does their gradient.  What was read of them before, or is yet
 // to be, stays there: preference loss of 8192 x 32000 bfloat16 189 us, 248
-// without, of 4001 x 131072 507 and 574; policy loss of 4096 x 131072 389 and 399,
-// of 3000 x 32000 (183 MB) 66 and 80, but of 1024 x 32000 31 and 28.  Below, whatever
-// comes next finds the gradient in the caches; where logits are read twice
-// (2048 x 32000, 125 MB: 63 and 73 us) they are streamed earlier.
+// without, of 4001 x 131072 507 and 574; policy loss of 4096 x 131072 389 and
+// 399, of 3000 x 32000 (183 MB) 66 and 80, but of 1024 x 32000 31 and 28.  Below,
+// whatever comes next finds the gradient in the caches; where logits are read
+// twice (2048 x 32000, 125 MB: 63 and 73 us) they are streamed earlier.
 constexpr int64_t STREAMED_ONCE = (int64_t)160 << 20, STREAMED_TWICE = (int64_t)96 << 20;
 
 template <typename T, bool ENTROPY>

@@ -8,7 +8,10 @@ Each loss comes in two forms.  ``policy_loss`` and the like carry their
 gradient through autograd.  ``policy_loss_with_grad`` and the like return the
 gradient in the logits with the loss, from one call that need not read the
 logits a second time (``torch.autograd.backward(logits, grad)`` takes it from
-there).  The calls do not wait for the GPU and may be captured into a graph.
+there).  Gradients have none of their own.  The calls do not wait for the GPU
+and may be captured into a graph; while a step is captured with its backward
+pass, no eager graph of the same leaves may be alive, as with torch's own
+operators.
 """
 from __future__ import annotations
 

@@ -457,7 +457,8 @@ def pick_tokens(logits: torch.Tensor, uniform: torch.Tensor, max_top_k: int = 64
     ``top_k`` of them; a ``top_k`` of 0 or below takes the first token and does
     not lift the limit.  The logprob is that of the token under the softmax over all
     allowed tokens.  A row without an allowed token gets -1 and -infinity.
-    The logprobs have no gradient: a backward pass through them raises."""
+    The logprobs have no gradient: a backward pass through them raises
+    (``token_logprobs`` of the tokens has one)."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
     if logits.requires_grad and torch.is_grad_enabled():
