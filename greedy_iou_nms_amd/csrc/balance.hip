@@ -12,9 +12,9 @@
 //     both:     + 2 z / N lse softmax_j.
 // What bounds it is the caller's time: three or four launches (3.3 us each), three
 // outputs and the binding take 18 to 21 us, the kernels about as long.  Of these,
-// 16384 x 256 float32 in 16 sequences: counting 6.8 us (five trips to memory one
-// after another), the pass 11.2 us for 33 MB (350 instructions for a wave's two
-// tokens), the sum 1.5.
+// 16384 x 256 float32 in 16 sequences: counting 8.2 us (five trips to memory one
+// after another), the pass 11.6 us for 33 MB (345 vector instructions for a wave's
+// two tokens), the sum 1.9.
 #include "loss_internal.h"
 
 #pragma clang fp contract(off)

@@ -9,18 +9,18 @@
 //     dz_j = e_j (P + Q u_j) + [j = token] alpha / t,
 //     P = -(alpha + eta (entropy - log s)) / (s t),  Q = -eta ln 2 / (s t).
 // So a row is looked through for its (m, s, w), which join by rescaling, and then
-// for its gradient.  Memory is the bound: 6.5 vector instructions an element for
-// the sums and 5.5 for the gradient, with an exponential that takes the time of
-// two, are 57 % of the vector units' time where rows are read and written at a
-// copy's rate (with entropies 9.5 for the sums, 84 % where rows are only read).
+// for its gradient.  Memory is the bound: 16.4 vector instructions an element for
+// both, by counters, are 59 % of the vector units' time where rows are read and
+// written at a copy's rate (with entropies 10.5 for the sums, 81 % where rows are
+// only read).
 // Hence
 //   * row_kernel, a workgroup that holds a row in its registers in between: logits
-//     are read once and the gradient is written once, 4096 x 131072 bfloat16 in 390 us
-//     for 2.04 GB, a copy's 5.2 TB/s;
+//     are read once and the gradient is written once, 4096 x 131072 bfloat16 in 395
+//     to 418 us for 2.04 GB, where a copy takes 393;
 //   * part_kernel and gradient_kernel, which read a row twice: where a loss needs
 //     all rows before any gradient (preference), where the rows are few and a row is
 //     shared by workgroups, and, the first alone, for results of long rows (4097 x
-//     131072 with entropies 189 us, 5.7 TB/s).
+//     131072 with entropies 191 us, 5.6 TB/s).
 #include "loss_internal.h"
 
 #pragma clang fp contract(off)
@@ -37,8 +37,9 @@ constexpr double LN2 = 0.693147180559945309;
 // or NaN where one was NaN.  s is a sum in binary64 of float32 exponentials:
 // where the largest logit, 1 of the sum, is the token's, log s is what the others
 // add to 1, and float32 loses 2^-25 with each (of log probabilities around -0.01
-// 6e-6 of the value for 6e-8; 2 % of the time where entropies are wanted, none
-// where memory is the bound).
+// 6e-6 of the value for 6e-8).  With the other steps to that end it cost 389 -> 395
+// us for a policy step of 4096 x 131072, and with entropies of 1003 x 150001 186 ->
+// 195.
 // at: the logit of the row's token, which a gradient in place of the logits
 // overwrites.
 struct Part {
@@ -136,7 +137,7 @@ __device__ __forceinline__ Scale scale_of(const LossRows &r, int64_t row) {
 // before and behind it, fewer than two packs, which threads take one each.  (Packs
 // at odd elements of 16 bits took 20 % longer: 4096 x 131073 float16 255 us for
 // 211 read, 541 for 440 read and written; and branches for a pack that is not
-// whole, at each pack that a thread holds, made code of 45 KB and 10 us a call.)
+// whole, at each pack that a thread holds, made 256 x 32000 27.7 us for 25.6.)
 template <typename T>
 struct Row {
     const T *z;       // the body
@@ -494,7 +495,8 @@ size_t lay_out(int64_t rows, int vocab, int64_t pairs, void *at, LossSpace *s) {
 // is made in binary64: where its probability is near 1, it is a difference of
 // nearly equal ones.  any: the gradient is not 0.  (A whole word: the bytes behind
 // a smaller one were copied through LDS at the thread's number, for which every
-// workgroup read the launch's packet in host memory: 256 x 32000 25 us for 13.)
+// workgroup read the launch's packet in host memory: those of 256 x 32000 started
+// over 13 us.)
 struct Slope {
     float base, k, P, Q, token;
     int any;
@@ -710,8 +712,8 @@ constexpr int waves_of(bool entropy, int held) {
 // A workgroup per row: its results and, with GRADIENT, its gradient.  The first
 // HELD packs of each thread stay in registers between the two, the others are
 // read again.  All of them are asked for at once: a row's time is one trip to
-// memory, its two passes of instructions (2 and 2.1 us for 32000 elements by 256
-// threads) and 0.9 us for its results, which other rows of the compute unit fill.
+// memory, its two passes of instructions and its results, which other rows of the
+// compute unit fill.
 template <typename T, bool ENTROPY, bool GRADIENT, bool STREAM, int GROUP, int HELD>
 __global__ __launch_bounds__(GROUP, waves_of(ENTROPY, HELD)) void row_kernel(LossArgs a,
                                                                              LossSpace space) {
@@ -921,8 +923,9 @@ bool held_for_results(const LossRows &in) {
 }
 
 // For the gradient, which slices read a second time: policy loss of 256 x 131072
-// bfloat16 29.6 us, 38.9 by slices; of 4096 x 131072 395 and 611.  Few long rows
-// leave the GPU empty: 16 x 131072 19.1 and 10.0, 64 x 131072 21.9 and 17.2, 96 even.
+// bfloat16 30.7 us, 39.4 by slices; of 4096 x 131072 401 and 559.  Few long rows
+// leave the GPU empty: 16 x 131072 19.8 and 10.3, 64 x 131072 22.6 and 17.0, 96
+// even; 16 x 65536 12.4 and 9.0, 64 x 65536 13.8 and 15.8.
 bool held_for_gradient(const LossRows &in) {
     return row_bytes(in) <= 65536 || in.rows >= (row_bytes(in) <= 131072 ? 64 : 96);
 }
