@@ -189,3 +189,29 @@ def test_balance_beside_routing():
     a = g.route_experts_backward(z, ids, factor, "sigmoid")
     b = g.balance_loss_with_grad(z, ids, "sigmoid", balance=0.01, z=0.001, live=live)[1]
     assert torch.equal(leaf.grad, a + b) or torch.equal(leaf.grad, b + a)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [(40, 12, None), (5000, 60, None), (900, 33, [0, 1, 500, 890])])
+def test_balance_by_given_counts_through_autograd(size, score):
+    """Counts that are given go through autograd as ids do: the factors come from
+    the same counts, so that loss and gradient have the same bits; the counts
+    themselves stay as they are, and take no gradient."""
+    note("balance by counts %s %s" % (size, score))
+    T, E, offsets = size
+    rng = np.random.default_rng(12)
+    z = logits_of(rng, T, E, torch.float32)
+    ids = dev(rng.integers(-1, E, (T, 3)).astype(np.int32))
+    given = dict(score=score, balance=0.3, z=0.01, live=dev(rng.random(T) < 0.9),
+                 offsets=None if offsets is None else dev(np.array(offsets, np.int64)))
+    up = dev(np.float32([1.5]))
+    want = lib().balance_loss_with_grad(z, ids, grad_loss=up, **given)
+    counts = want[2].clone()
+    for _ in range(2):  # the same tensor twice
+        leaf = z.clone().requires_grad_()
+        loss, got = lib().balance_loss(leaf, counts=counts, **given)
+        assert not got.requires_grad and not counts.requires_grad
+        (loss * up[0]).backward()
+        assert torch.equal(loss.detach(), want[0])
+        assert torch.equal(leaf.grad, want[1])
+        assert torch.equal(got, want[2]) and torch.equal(counts, want[2])
