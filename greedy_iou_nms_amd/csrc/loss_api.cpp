@@ -283,8 +283,8 @@ nms_status nms_balance_loss(const void *logits, nms_dtype dtype, int64_t tokens,
             st = check_matrix(grad_logits, dtype, tokens, experts, grad_stride);
         if (st != NMS_OK) return st;
     }
-    // (the ids of no tokens, or of no places, have no address)
-    if (ids == nullptr && counts == nullptr && tokens > 0 && o.top_k > 0) return NMS_INVALID_ARG;
+    // without ids the kernels read the counts, those of an empty batch too
+    if (ids == nullptr && counts == nullptr) return NMS_INVALID_ARG;
     if (loss == nullptr && counts == nullptr && grad_logits == nullptr) return NMS_INVALID_ARG;
     st = check_workspace(workspace, workspace_bytes, needed);
     if (st != NMS_OK) return st;

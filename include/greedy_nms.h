@@ -778,7 +778,9 @@ typedef struct nms_balance_options {
  *   logits, dtype, tokens, experts, row_stride  as for nms_route_experts.
  *   ids        device int32[tokens * top_k], as nms_route_experts gives them
  *              (one outside 0..experts-1 is an empty place), or NULL: counts
- *              are given, of all ranks for instance.
+ *              are given, of all ranks for instance.  NULL has that meaning for
+ *              an empty batch too: where its counts are wanted (they are 0), or
+ *              neither is given, pass any other address, which is not read.
  *   live       device byte[tokens] or NULL: 0 marks a padded row.
  *   offsets    device int64[sequences + 1]: as for nms_preference_loss; NULL:
  *              one sequence.

@@ -169,6 +169,21 @@ def test_balance_arguments():
     assert balance(ws_bytes=64) == "NMS_WORKSPACE_TOO_SMALL"
 
 
+def test_balance_without_ids_or_counts():
+    """Where ids are NULL the counts are read, so that one of the two has to be
+    there, for an empty batch and for tokens without a place too."""
+    none = dict(ids=None, counts=None)
+    assert balance((0, 0, 1.0, 0.0), **none) == "NMS_INVALID_ARG"
+    assert balance((0, 0, 1.0, 0.0), tokens=9000, **none) == "NMS_INVALID_ARG"
+    assert balance((0, 0, 1.0, 0.0), offsets=FAKE, sequences=3, **none) == "NMS_INVALID_ARG"
+    for top_k in (0, 2):
+        o = (0, top_k, 1.0, 0.0)
+        assert balance(o, tokens=0, **none) == "NMS_INVALID_ARG"
+        assert balance(o, tokens=0, logits=None, out=None, **none) == "NMS_INVALID_ARG"
+        assert balance(o, tokens=0, loss=None, **none) == "NMS_INVALID_ARG"
+        assert balance(o, tokens=0, offsets=FAKE, sequences=3, **none) == "NMS_INVALID_ARG"
+
+
 # ------------------------------------------------------------------ the binding
 
 class Claimed(torch.Tensor):
