@@ -356,7 +356,7 @@ struct RowGiven {
 };
 
 // array[row], or what stands for an array that is not given.  The load is made
-// either way, from `any` if need be, so that all of them are in flight
+// either way, of the row's token in its place, so that all of them are in flight
 // together: behind a branch each, or behind the token, they cost a round trip
 // each.
 __device__ __forceinline__ float parameter(const float *array, int64_t row, float otherwise,
@@ -368,9 +368,7 @@ __device__ __forceinline__ float parameter(const float *array, int64_t row, floa
 template <bool ENTROPY>
 __device__ __forceinline__ RowGiven given_of(const LossArgs &a, int64_t row) {
     RowGiven r = {};
-    const uintptr_t z = reinterpret_cast<uintptr_t>(a.in.logits) +
-                        row * a.in.row_stride * (a.in.dtype == NMS_F32 ? 4 : 2);
-    const void *any = reinterpret_cast<const void *>(z & ~(uintptr_t)3);
+    const void *any = a.in.tokens + row;
     r.token = a.in.tokens[row];
     r.weight = parameter(a.in.weights, row, a.weight, any);
     r.old = parameter(a.old_logprobs, row, 0.0f, any);
