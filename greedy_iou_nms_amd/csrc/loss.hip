@@ -378,6 +378,7 @@ __device__ __forceinline__ RowGiven given_of(const LossArgs &a, int64_t row) {
     r.alpha = parameter(a.grad_logprobs, row, 0.0f, any);
     r.eta = ENTROPY ? parameter(a.grad_entropies, row, 0.0f, any) : 0.0f;
     r.counts = (unsigned)r.token < (unsigned)a.in.vocab;
+    if (!r.counts) r.token = -1;  // places are reckoned from it
     if (a.in.weights) r.counts &= r.weight != 0.0f;
     // (a row without a gradient in its results has none, whatever it holds)
     if (a.kind == LOSS_GIVEN) r.counts &= r.alpha != 0.0f || r.eta != 0.0f;
