@@ -513,6 +513,9 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
     const double P = -((double)r.alpha + eta * ((double)r.entropy - r.log_s)) * per;
     const double Q = -eta * LN2 * per;
     const float u = factor((p.at - g.base) * g.k);
+    // (of NaN every element's exponential is made NaN: 0 would give 0 in a product
+    // with entropies)
+    if (P != P || Q != Q) g.base = __uint_as_float(0x7fc00000u);
     g.P = (float)P;
     g.Q = (float)Q;
     g.token = (float)((double)r.alpha * (double)k.inverse +

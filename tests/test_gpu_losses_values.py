@@ -1,0 +1,49 @@
+"""Gradients of the losses where values are at the ends of their types: NaN and
+infinities beside masked logits, temperatures whose inverse float32 does not
+hold, against the plain 64-bit ones (bounds: loss_util.py)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gpu_util import note  # noqa: E402
+from loss_util import TYPES, dev, host, lib, logits_of  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# a row in a workgroup of 64 threads, of 1024, and shared by slices; of a workgroup
+# that reads the end of its row again
+SIZES = [(8, 9), (8, 300), (8, 9001), (8, 70001), (104, 70001)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", SIZES)
+@pytest.mark.parametrize("entropy", [False, True])
+def test_gradients_of_rows_with_nan_and_infinity(T, V, dtype, entropy):
+    """They are NaN throughout, also where a logit is masked or far below the
+    others, and other rows' are not."""
+    note("gradients of nan %d %d %s %s" % (T, V, dtype, entropy))
+    rng = np.random.default_rng(V)
+    z = logits_of(rng, T, V, dtype)
+    z[:, 4::5] = -float("inf")
+    z[:, 3] = torch.finfo(dtype).min
+    z[0, 1] = float("nan")
+    z[1, V - 1] = float("inf")
+    z[2, V // 2] = float("nan")
+    z[2, V // 2 + 1] = float("inf")
+    z[3] = float("nan")
+    z[4, 0] = float("nan")              # a row that does not count
+    bad = np.arange(T) < 4
+    tokens = np.full(T, 2, np.int32)
+    tokens[4] = -1
+    g, e = rng.normal(size=(2, T)).astype(np.float32)
+    d_h = dev(e) if entropy else None
+    heat = dev((0.5 + rng.random(T)).astype(np.float32))
+    for dz in (lib().token_logprobs_backward(z, dev(tokens), dev(g), None, d_h),
+               lib().token_logprobs_backward(z, dev(tokens), dev(0 * g), heat, dev(e)),
+               lib().token_logprobs_backward(z, dev(tokens), dev(g), heat, d_h),
+               lib().policy_loss_with_grad(z, dev(tokens), dev(g), dev(e),
+                                           entropy=0.01 if entropy else None)[1]):
+        dz = host(dz)
+        assert np.isnan(dz[bad]).all()
+        assert np.isfinite(dz[~bad]).all() and not dz[4].any()
