@@ -108,21 +108,22 @@ __device__ __forceinline__ void store_pack(T *p, const Pack<T> &e) {
 
 // log2(e) / t as a sum, whose second term keeps sums over many rows unbiased
 // (the first alone is off by up to 2^-25 of u, in one direction for all rows),
-// and 1 / t.  The second term is above 0, so that -infinity times it is
-// -infinity.
+// and 1 / t, in binary64: for t below 2^-128 float32 does not hold it.  The second
+// term is above 0, so that -infinity times it is -infinity.
 struct Scale {
-    float hi, lo, inverse;
+    float hi, lo;
+    double inverse;
 };
 
-// A temperature of 0 or below (or NaN) stands for 1; one beyond what its
-// inverse holds takes the largest or smallest that float32 has, so that the
-// largest logit keeps 2^0 and -infinity stays out.
+// A temperature of 0 or below (or NaN) stands for 1; a scale beyond float32
+// takes the largest or smallest that float32 has, so that the largest logit keeps
+// 2^0 and -infinity stays out.
 __device__ __forceinline__ Scale scale_of(const LossRows &r, int64_t row) {
     constexpr double LOG2E = 1.4426950408889634;
     constexpr float ONE = 1.44269502f, REST = (float)(LOG2E - (double)ONE);
     static_assert((double)ONE < LOG2E, "the rest is above 0");
     float t = r.temperature ? r.temperature[row] : 1.0f;
-    if (!(t > 0.0f) || t == 1.0f) return {ONE, REST, 1.0f};
+    if (!(t > 0.0f) || t == 1.0f) return {ONE, REST, 1.0};
     constexpr float LEAST = 1.4012985e-45f, MOST = 3.4028235e38f;
     const double k = LOG2E / (double)t;
     float hi = fminf(fmaxf((float)k, LEAST), MOST);
@@ -130,7 +131,7 @@ __device__ __forceinline__ Scale scale_of(const LossRows &r, int64_t row) {
     if ((double)hi > k && hi > LEAST) hi = __uint_as_float(__float_as_uint(hi) - 1u);
     float lo = fmaxf((float)(k - (double)hi), LEAST);
     if (hi == MOST) lo = LEAST;
-    return {hi, lo, fminf(1.0f / t, MOST)};
+    return {hi, lo, k * LN2};
 }
 
 // A row's logits: a body of whole packs at aligned addresses, and the elements
@@ -403,7 +404,7 @@ __device__ __forceinline__ RowResult result_of(const LossArgs &a, const RowGiven
     r.log_s = log_of(ENTROPY ? p.s + LN2 * (double)(k.lo / k.hi) * p.w : p.s);
     r.exact = p.s == 0.0        ? (double)NEG_INF
               : p.at == NEG_INF ? (double)NEG_INF - r.log_s
-                                : ((double)p.at - (double)p.m) * (double)k.inverse - r.log_s;
+                                : ((double)p.at - (double)p.m) * k.inverse - r.log_s;
     r.logprob = (float)r.exact;
     if (ENTROPY)
         r.entropy = p.s == 0.0 ? 0.0f : (float)(r.log_s - LN2 * p.w * inverse_of(p.s));
@@ -508,7 +509,7 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
     g.any = counts && p.s != 0.0 && (r.alpha != 0.0f || r.eta != 0.0f);
     g.base = base_of(p.m);
     g.k = k.hi;
-    const double per = (double)k.inverse * inverse_of(p.s);
+    const double per = k.inverse * inverse_of(p.s);
     const double eta = ENTROPY ? (double)r.eta : 0.0;
     const double P = -((double)r.alpha + eta * ((double)r.entropy - r.log_s)) * per;
     const double Q = -eta * LN2 * per;
@@ -518,7 +519,7 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
     if (P != P || Q != Q) g.base = __uint_as_float(0x7fc00000u);
     g.P = (float)P;
     g.Q = (float)Q;
-    g.token = (float)((double)r.alpha * (double)k.inverse +
+    g.token = (float)((double)r.alpha * k.inverse +
                       (double)exp2_of(u) * (P + Q * (double)u));
     return g;
 }

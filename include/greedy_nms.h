@@ -608,7 +608,8 @@ nms_status nms_pick_tokens(const void *logits, nms_dtype dtype, int64_t rows, in
  * not hide it); where all logits are -infinity, the log probability is
  * -infinity and entropy and gradient are 0.  A temperature of 0 or below, or
  * NaN, counts as 1 (the log probability that nms_pick_tokens gives for it); at
- * +infinity all tokens but those at -infinity weigh alike.
+ * +infinity all tokens but those at -infinity weigh alike; below 4.2e-39 log2(e) / t
+ * counts as float32's largest number in the probabilities.
  * Terms are computed in float32, sums over rows in binary64; a probability
  * below 2^-126 of the row's largest counts as 0.
  *

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from gpu_util import note  # noqa: E402
-from loss_util import TYPES, dev, host, lib, logits_of  # noqa: E402
+from loss_util import TYPES, U, dev, host, lib, logits_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,34 @@ def test_gradients_of_rows_with_nan_and_infinity(T, V, dtype, entropy):
         dz = host(dz)
         assert np.isnan(dz[bad]).all()
         assert np.isfinite(dz[~bad]).all() and not dz[4].any()
+
+
+@pytest.mark.parametrize("T,V", SIZES)
+@pytest.mark.parametrize("t", [1e-45, 1e-42, 2e-39, 4e-39, 1e-38])
+def test_log_probabilities_at_the_smallest_temperatures(T, V, t):
+    """Where float32 holds the distance to the largest logit divided by the
+    temperature, but not the temperature's inverse.  In the probabilities log2(e) /
+    temperature counts as float32's largest number where it is beyond that."""
+    note("smallest temperatures %d %d %g" % (T, V, t))
+    t = float(np.float32(t))
+    z = torch.zeros(T, V)
+    z[:, 1:] = -1e30
+    far = np.float32(t) * (10.0 ** np.linspace(5, 37, T))
+    z[:, V // 2] = torch.from_numpy(-far.astype(np.float32))
+    tokens = np.full(T, V // 2, np.int32)
+    d = host(z[:, V // 2])
+    u = d * min(np.log2(np.e) / t, float(np.finfo(np.float32).max))
+    x = 2.0 ** u
+    log_s = np.log1p(x)
+    want, h = d / t - log_s, log_s - np.log(2) * u * x / (1 + x)
+    # the exponent's product and the instruction are rounded; s = 1 + x to 2^-53, and
+    # the logarithm's series leaves 1.2e-14
+    err, log_err = U * (2 * np.abs(u) + 2) * x, 2.0 ** -53 + 1.2e-14
+    for entropy in (False, True):
+        got = lib().token_logprobs(dev(z.numpy()), dev(tokens), dev(np.full(T, t, np.float32)),
+                                   entropy=entropy)
+        lp = host(got[0] if entropy else got)
+        assert np.all(np.abs(lp - want) <= err + log_err + U * np.abs(want))
+        if entropy:
+            assert np.all(np.abs(host(got[1]) - h) <= err * (1 + np.abs(u)) + log_err +
+                          U * (4 * x + h))
