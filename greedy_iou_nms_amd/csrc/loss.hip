@@ -250,12 +250,13 @@ __device__ __forceinline__ float less(const Pack<half_t> &e, int j, float base) 
     return d;
 }
 
-// u x for an exponential x = 2^u: 0 where u is -infinity, by the multiplication
-// whose product with 0 is 0.  What the exponential has just made may be read after
-// a wait only, which the compiler puts before its own instructions and not here.
-__device__ __forceinline__ float times_exponential(float u, float x) {
+// v x for an exponential x: 0 where x is, whatever v (x's exponent of -infinity, a
+// slope beyond float32), by the multiplication whose product with 0 is 0.  What the
+// exponential has just made may be read after a wait only, which the compiler puts
+// before its own instructions and not here.
+__device__ __forceinline__ float times_exponential(float v, float x) {
     float d;
-    asm("s_nop 0\n\tv_mul_legacy_f32 %0, %1, %2" : "=v"(d) : "v"(u), "v"(x));
+    asm("s_nop 0\n\tv_mul_legacy_f32 %0, %1, %2" : "=v"(d) : "v"(v), "v"(x));
     return d;
 }
 
@@ -518,18 +519,22 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
     // with entropies)
     if (P != P || Q != Q) g.base = __uint_as_float(0x7fc00000u);
     g.P = (float)P;
-    g.Q = (float)Q;
+    // (P may be beyond float32, and the gradient then is; but not Q, whose product
+    // with the largest logit's exponent of 0 would be NaN)
+    constexpr double MOST = 3.4028235e38f;
+    g.Q = fabs(Q) < 1e300 ? (float)fmin(fmax(Q, -MOST), MOST) : (float)Q;
     g.token = (float)((double)r.alpha * k.inverse +
                       (double)exp2_of(u) * (P + Q * (double)u));
     return g;
 }
 
-// The gradient of one logit that is not the token's, from it less the base.
+// The gradient of one logit that is not the token's, from it less the base: 0
+// where its exponential is, also by a P that float32 does not hold.
 template <bool ENTROPY>
 __device__ __forceinline__ float gradient_of(float less, const Slope &g) {
     const float u = less * g.k;
     const float x = exp2_of(u);
-    return ENTROPY ? times_exponential(fmaf(g.Q, u, g.P), x) : x * g.P;
+    return times_exponential(ENTROPY ? fmaf(g.Q, u, g.P) : g.P, x);
 }
 
 // A pack of logits becomes its gradient, but for what the token's has more.

@@ -78,3 +78,42 @@ def test_log_probabilities_at_the_smallest_temperatures(T, V, t):
         if entropy:
             assert np.all(np.abs(host(got[1]) - h) <= err * (1 + np.abs(u)) + log_err +
                           U * (4 * x + h))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", SIZES)
+@pytest.mark.parametrize("t,g", [(1e-42, 2.0), (1e-35, 65536.0), (1e-38, -1e3), (1e-30, 1e10),
+                                 (1.0, 3e38), (1e-3, -3e36)])
+def test_gradients_beyond_float32(T, V, dtype, t, g):
+    """Where gradient / temperature is beyond float32, logits of probability 0 have
+    gradient 0 all the same, and those that have a share of it are infinite."""
+    note("gradients beyond float32 %d %d %s %g" % (T, V, dtype, t))
+    rng = np.random.default_rng(V)
+    t, g = float(np.float32(t)), float(np.float32(g))
+    z = logits_of(rng, T, V, dtype)
+    z[:, 4::5] = -float("inf")
+    z[:, 3] = torch.finfo(dtype).min
+    z[:, V // 2] = 1000.0               # a probability of 1
+    z[3, 0] = 1000.0                    # two of 1/2
+    tokens = np.full(T, V // 2, np.int32)
+    tokens[1], tokens[2] = 1, 4         # of probability 0, masked
+    p, one = np.zeros((2, T, V))
+    p[:, V // 2] = 1.0
+    p[3, [0, V // 2]] = 0.5
+    one[np.arange(T), tokens] = 1.0
+    want = (one - p) * (g / t)
+    half = torch.finfo(dtype).eps / 2
+    top = float(torch.finfo(dtype).max) * (1 + half)    # what is rounded to infinity
+    for e in (None, 0.0, 1.0):
+        d_h = None if e is None else dev(np.full(T, e, np.float32))
+        got = host(lib().token_logprobs_backward(z, dev(tokens), dev(np.full(T, g, np.float32)),
+                                                 dev(np.full(T, t, np.float32)), d_h))
+        assert not np.isnan(got).any()
+        rest = want == 0
+        assert not got[rest].any()
+        wild = np.abs(want) >= top
+        assert np.array_equal(got[wild], np.copysign(np.inf, want[wild]))
+        near = ~rest & ~wild
+        # gradient, 1 / t, 1 / s and their products are rounded, in float32 or 64 bits
+        err = (8 * 2.0 ** -24 + half) * np.abs(want[near])
+        assert np.all(np.abs(got[near] - want[near]) <= err)
