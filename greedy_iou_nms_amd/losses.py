@@ -8,7 +8,8 @@ Each loss comes in two forms.  ``policy_loss`` and the like carry their
 gradient through autograd.  ``policy_loss_with_grad`` and the like return the
 gradient in the logits with the loss, from one call that need not read the
 logits a second time (``torch.autograd.backward(logits, grad)`` takes it from
-there).  Gradients have none of their own.  The calls do not wait for the GPU
+there).  Gradients have none of their own, and inputs with a tangent (of
+forward-mode differentiation) are refused.  The calls do not wait for the GPU
 and may be captured into a graph; while a step is captured with its backward
 pass, no eager graph of the same leaves may be alive, as with torch's own
 operators.
@@ -20,6 +21,7 @@ import functools
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from . import Workspace, _check, _default_workspace, _lib, _raw_stream
 from .selection import (_SCORES, _address, _capturing, _current_device, _like, _matrix,
@@ -95,6 +97,14 @@ def _constant(name: str, **tensors) -> None:
                                    % (name, key))
 
 
+def _no_tangents(name: str, *tensors) -> None:
+    """Refuses tensors with a tangent, which the outputs would lack.  (They have
+    one within a level of forward-mode differentiation only.)"""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and _forward.unpack_dual(t).tangent is not None:
+            raise RuntimeError("%s has no forward-mode gradient: an input has a tangent" % name)
+
+
 def _float(t, name: str, n: int, device) -> Optional[int]:
     return None if t is None else _vector(t, name, n, torch.float32, device)
 
@@ -148,6 +158,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor,
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
     _constant("token_logprobs", temperature=temperature)
+    if _forward._current_level >= 0:
+        _no_tangents("token_logprobs", logits, temperature)
     if _graph(logits):
         got = _TokenLogprobs.apply(logits, tokens, temperature, bool(entropy))
         return got if entropy else got[0]
@@ -207,6 +219,9 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor,
     gradient 0, whatever it holds."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
+    if _forward._current_level >= 0:
+        _no_tangents("token_logprobs_backward", logits, grad_logprobs, temperature,
+                     grad_entropies, out)
     if tokens is None or grad_logprobs is None:
         raise TypeError("tokens and grad_logprobs must be torch tensors")
     a = _vector(tokens, "tokens", rows, torch.int32, device)
@@ -237,6 +252,9 @@ def _run_policy(logits, tokens, old_logprobs, advantages, weights, ref_logprobs,
     """(loss, grad_logits, logprobs, entropies), None what is not asked for."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
+    if _forward._current_level >= 0:
+        _no_tangents(name, logits, old_logprobs, advantages, weights, ref_logprobs, temperature,
+                     grad_loss, out)
     if tokens is None or old_logprobs is None or advantages is None:
         raise TypeError("tokens, old_logprobs and advantages must be torch tensors")
     a = _vector(tokens, "tokens", rows, torch.int32, device)
@@ -352,6 +370,8 @@ def _run_preference(logits, tokens, offsets, ref_logprobs, weights, options, gra
     margins."""
     code, rows, vocab, stride = _matrix(logits, "logits")
     device = logits.device
+    if _forward._current_level >= 0:
+        _no_tangents(name, logits, ref_logprobs, weights, grad_loss, out)
     if tokens is None:
         raise TypeError("tokens must be a torch tensor")
     if not isinstance(offsets, torch.Tensor):
@@ -470,6 +490,8 @@ def _run_balance(logits, ids, counts, score, balance, z, offsets, live, grad_los
     """(loss, grad_logits, counts)."""
     code, tokens, experts, stride = _matrix(logits, "logits")
     device = logits.device
+    if _forward._current_level >= 0:
+        _no_tangents(name, logits, grad_loss, out)
     sequences = 1
     if offsets is not None:
         if not isinstance(offsets, torch.Tensor):

@@ -180,3 +180,44 @@ def test_unused_outputs_and_an_upstream_of_the_wrong_kind(library):
     with pytest.raises(TypeError):
         g.policy_loss_with_grad(z, a, old, adv, grad_loss=1.0)
     assert not library.calls[2:]
+
+
+def test_tangents_are_refused(library):
+    """Forward-mode differentiation has no part in the calls: an input with a
+    tangent is refused, not stripped of it, whether or not gradients are recorded."""
+    z, a, old, adv = rows(6)
+    two, pair, up = on_gpu(2), on_gpu(1), on_gpu(1)
+    at, ids = on_gpu(3, dtype=torch.int64), on_gpu(6, 2, dtype=torch.int32)
+    calls = [(g.token_logprobs, [z, a, adv]),
+             (g.token_logprobs_backward, [z, a, old, adv, old]),
+             (g.policy_loss, [z, a, old, adv, adv, old, adv]),
+             (g.policy_loss_with_grad, [z, a, old, adv, adv, old, adv]),
+             (lambda *v: g.policy_loss_with_grad(*v[:-1], grad_loss=v[-1]), [z, a, old, adv, up]),
+             (g.preference_loss, [z, a, at, two, pair]),
+             (g.preference_loss_with_grad, [z, a, at, two, pair]),
+             (lambda *v: g.preference_loss_with_grad(*v[:-1], grad_loss=v[-1]), [z, a, at, up]),
+             (g.balance_loss, [z, ids]), (g.balance_loss_with_grad, [z, ids]),
+             (lambda *v: g.balance_loss_with_grad(*v[:-1], grad_loss=v[-1]), [z, ids, up])]
+    forward = torch.autograd.forward_ad
+    for call, args in calls:
+        with forward.dual_level():
+            call(*args)                     # nothing here has one
+            for i, t in enumerate(args):
+                if not t.is_floating_point():
+                    continue
+                with_tangent = list(args)
+                with_tangent[i] = forward.make_dual(t, torch.ones_like(t))
+                made = len(library.calls)
+                with pytest.raises(RuntimeError, match="tangent"):
+                    call(*with_tangent)
+                with torch.no_grad(), pytest.raises(RuntimeError, match="tangent"):
+                    call(*with_tangent)
+                assert len(library.calls) == made
+        call(*args)
+    with forward.dual_level():
+        out = forward.make_dual(on_gpu(6, 11), on_gpu(6, 11))
+        with pytest.raises(RuntimeError, match="tangent"):
+            g.policy_loss_with_grad(z, a, old, adv, out=out)
+        leaf = on_gpu(6, 11).requires_grad_()
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            g.token_logprobs(forward.make_dual(leaf, torch.ones_like(leaf)), a)
