@@ -117,3 +117,32 @@ def test_gradients_beyond_float32(T, V, dtype, t, g):
         # gradient, 1 / t, 1 / s and their products are rounded, in float32 or 64 bits
         err = (8 * 2.0 ** -24 + half) * np.abs(want[near])
         assert np.all(np.abs(got[near] - want[near]) <= err)
+
+
+@pytest.mark.parametrize("q", [1e-6, 1e-5, 1e-4, 1e-3, 1e-2, 0.1, 0.3, 0.49, 0.51, 0.7, 1.0, 3.0])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_divergence_from_a_near_reference(q, sign):
+    """exp(q) - q - 1 of a small q is q^2 / 2, not what is left of q less q."""
+    for V, dtype in ((4, torch.float32), (256, torch.float16), (65536, torch.bfloat16),
+                     (131072, torch.float32)):
+        note("divergence %g %d" % (sign * q, V))
+        z = torch.zeros(1, V)
+        ref = np.float32([-np.log(V) + sign * q])
+        exact_q = float(ref[0]) + np.log(V)     # V is exact, and so is s
+        x, want, n = exact_q, 0.0, 2
+        term = x * x / 2
+        while abs(term) > 1e-20 * want:         # for its tail to be of one size
+            want += term
+            n += 1
+            term *= x / n
+        one, zero = dev(np.ones(1, np.float32)), dev(np.zeros(1, np.float32))
+        given = [dev(z.numpy(), dtype), dev(np.zeros(1, np.int32)), zero, zero, one, dev(ref)]
+        for loss in (lib().policy_loss(*given, kl=1.0)[0],
+                     lib().policy_loss_with_grad(*given, kl=1.0)[0]):
+            # the logarithm is good to 1.2e-14, and the oracle's to 2^-52 log V; q is
+            # rounded (2 U of q^2), beyond 1/2 the exponential less 1 and the
+            # difference from q are (3 U of values up to 5 times the result, 8 at 3), below it 8
+            # steps of a polynomial whose later ones count half and less
+            err = (2 + 3 * 8) * U * want + (1.2e-14 + 2.0 ** -52 * np.log(V)) * abs(np.expm1(x))
+            assert abs(float(loss) - want) <= err, (V, float(loss), want)
+            assert float(loss) >= 0
