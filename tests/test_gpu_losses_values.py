@@ -7,7 +7,9 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from gpu_util import note  # noqa: E402
-from loss_util import TYPES, U, dev, host, lib, logits_of  # noqa: E402
+from loss_util import TYPES, U, Bounds, dev, host, lib, logits_of, within  # noqa: E402
+from oracle import losses as plain  # noqa: E402
+from test_gpu_losses import policy_bounds, tokens_of  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +148,74 @@ def test_divergence_from_a_near_reference(q, sign):
             err = (2 + 3 * 8) * U * want + (1.2e-14 + 2.0 ** -52 * np.log(V)) * abs(np.expm1(x))
             assert abs(float(loss) - want) <= err, (V, float(loss), want)
             assert float(loss) >= 0
+
+
+# ------------------------------------------------------------------ temperatures
+
+def representable(want, dtype):
+    """Infinite where a type rounds a value to infinity."""
+    info = torch.finfo(dtype)
+    over = np.abs(want) >= float(info.max) * (1 + info.eps / 4)
+    return np.where(over, np.copysign(np.inf, want), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", [(5, 7), (40, 257), (9, 2049), (3, 8191), (2, 50021), (300, 1000),
+                                 (70, 5001), (97, 66001)])
+@pytest.mark.parametrize("kl,entropy", [(0.0, None), (0.1, 0.05)])
+def test_policy_with_temperatures(T, V, dtype, kl, entropy):
+    """A temperature of each row's own, some that count as 1, in the call with the
+    gradient and through autograd, with held ratios, divergence and entropies."""
+    note("policy with temperatures %d %d %s %s" % (T, V, dtype, kl))
+    rng = np.random.default_rng(T + 7 * V)
+    z = logits_of(rng, T, V, dtype)
+    heat = (0.4 + 1.3 * rng.random(T)).astype(np.float32)
+    heat[::5] = rng.choice(np.float32([0, -2, np.nan, 1]), len(heat[::5]))
+    tokens = tokens_of(rng, T, V, 0.1)
+    lp = plain.rows(host(z), tokens, heat)[1]
+    old, ref = (lp + 0.4 * rng.normal(size=(2, T))).astype(np.float32)
+    adv, w = rng.normal(size=T).astype(np.float32), rng.random(T).astype(np.float32)
+    w[rng.random(T) < 0.1] = 0.0
+    up, bonus = 4.0, entropy or 0.0
+    b = Bounds(host(z), tokens, heat, w)
+    loss, lp, h, dz, g, e = plain.policy(host(z), tokens, old, adv, w, ref, heat, 0.2, 0.28, kl,
+                                         bonus, up)
+    err, dg = policy_bounds(b, old, adv, w, ref, kl, bonus, up)
+    tol = b.grad(dtype, dz, g, e, dg)
+    given = [dev(v) for v in (tokens, old, adv, w, ref, heat)]
+    options = dict(clip=0.2, clip_high=0.28, kl=kl, entropy=entropy)
+    both = lib().policy_loss_with_grad(z, *given, grad_loss=dev(np.float32([up])), **options)
+    leaf = z.clone().requires_grad_()
+    got = lib().policy_loss(leaf, *given, **options)
+    got[0].backward(torch.tensor(up, device=z.device))
+    within(host(both[1]), dz, tol, "gradient")
+    within(host(leaf.grad), dz, tol, "gradient of autograd")
+    for out in (both[:1] + both[2:], got, lib().policy_loss(z, *given, **options)):
+        within(host(out[0]), loss, err + U * abs(loss), "loss")
+        within(host(out[1]), lp, b.logprob, "logprobs")
+        if entropy is not None:
+            within(host(out[2]), h, b.entropy, "entropies")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V", [(13, 333), (13, 9001), (13, 70001), (130, 66001)])
+def test_gradients_at_any_temperature(T, V, dtype):
+    """0, below and NaN as 1; very large and very small ones; infinity."""
+    note("gradients at any temperature %d %d %s" % (T, V, dtype))
+    rng = np.random.default_rng(V + 3)
+    heat = np.resize(np.float32([0, -1, np.nan, 1e-3, 1e3, 1e30, np.inf, 1e-30, 1e-42, 3e38, 1e-38,
+                                 -np.inf, 1]), T)
+    z = logits_of(rng, T, V, dtype)
+    z[:, 5] = -float("inf")
+    z[:, 7] = 40.0                      # the largest of all rows, by more than any two are apart
+    tokens = rng.integers(8, V, T).astype(np.int32)
+    tokens[T // 2:] = 7
+    g, e = rng.normal(size=(2, T)).astype(np.float32)
+    b = Bounds(host(z), tokens, heat)
+    lp, h = lib().token_logprobs(z, dev(tokens), dev(heat), entropy=True)
+    within(host(lp), representable(b.lp, torch.float32), b.logprob, "logprobs")
+    within(host(h), b.h, b.entropy, "entropies")
+    for d_h in (None, e):
+        want = plain.combine(b.counts, b.dlp, b.dh, g, d_h)
+        got = host(lib().token_logprobs_backward(z, dev(tokens), dev(g), dev(heat), dev(d_h)))
+        within(got, representable(want, dtype), b.grad(dtype, want, g, d_h), "gradient")
