@@ -9,18 +9,18 @@
 //     dz_j = e_j (P + Q u_j) + [j = token] alpha / t,
 //     P = -(alpha + eta (entropy - log s)) / (s t),  Q = -eta ln 2 / (s t).
 // So a row is looked through for its (m, s, w), which join by rescaling, and then
-// for its gradient.  Memory is the bound: 16.4 vector instructions an element for
-// both, by counters, are 59 % of the vector units' time where rows are read and
+// for its gradient.  Memory is the bound: 16.2 vector instructions an element for
+// both, by counters, are 60 % of the vector units' time where rows are read and
 // written at a copy's rate (with entropies 10.5 for the sums, 81 % where rows are
 // only read).
 // Hence
 //   * row_kernel, a workgroup that holds a row in its registers in between: logits
-//     are read once and the gradient is written once, 4096 x 131072 bfloat16 in 395
-//     to 418 us for 2.04 GB, where a copy takes 393;
+//     are read once and the gradient is written once, 4096 x 131072 bfloat16 in 385
+//     to 413 us for 2.04 GB, where a copy takes 393;
 //   * part_kernel and gradient_kernel, which read a row twice: where a loss needs
 //     all rows before any gradient (preference), where the rows are few and a row is
 //     shared by workgroups, and, the first alone, for results of long rows (4097 x
-//     131072 with entropies 191 us, 5.6 TB/s).
+//     131072 with entropies 190 us, 5.6 TB/s).
 #include "loss_internal.h"
 
 #pragma clang fp contract(off)
@@ -138,7 +138,8 @@ __device__ __forceinline__ Scale scale_of(const LossRows &r, int64_t row) {
 // before and behind it, fewer than two packs, which threads take one each.  (Packs
 // at odd elements of 16 bits took 20 % longer: 4096 x 131073 float16 255 us for
 // 211 read, 541 for 440 read and written; and branches for a pack that is not
-// whole, at each pack that a thread holds, made 256 x 32000 27.7 us for 25.6.)
+// whole, at each pack that a thread holds, made 256 x 32000 27.7 us for 25.6 as the
+// kernel was then; now it takes 11.3.)
 template <typename T>
 struct Row {
     const T *z;       // the body
@@ -540,7 +541,10 @@ __device__ __forceinline__ Slope slope_of(const RowResult &r, const Part &p, con
 }
 
 // The gradient of one logit that is not the token's, from it less the base: 0
-// where its exponential is, also by a P that float32 does not hold.
+// where its exponential is, also by a P that float32 does not hold.  (u is by k.hi
+// alone, which is off by less than 2^-23 of u, 2^-26 at a temperature of 1: about
+// what the difference and the product are rounded by.  The second term would be an
+// instruction more for each element.)
 template <bool ENTROPY>
 __device__ __forceinline__ float gradient_of(float less, const Slope &g) {
     const float u = less * g.k;

@@ -24,8 +24,6 @@ constexpr int RT = 256;  // threads per workgroup
 constexpr int RWAVES = RT / 64;
 constexpr double LOWEST = -__builtin_inf();
 
-// ---------------------------------------- reductions over 4 .. 64 lanes
-
 // ------------------------------------------------------------ exact scores
 
 // exp(x) to 2^-40 of its value: 2^n from the exponent, a Taylor polynomial of
