@@ -603,12 +603,13 @@ nms_status nms_pick_tokens(const void *logits, nms_dtype dtype, int64_t rows, in
  * not has log probability, entropy and gradient 0 and is not read.  With t
  * the row's temperature, p = softmax(z / t) and a the token,
  *     log probability  log p_a;    entropy  H = -sum p log p.
- * A logit of -infinity has probability 0.  NaN or +infinity in a row that
- * counts makes its results NaN (nms_pick_tokens passes over a NaN; a loss does
- * not hide it); where all logits are -infinity, the log probability is
- * -infinity and entropy and gradient are 0.  A temperature of 0 or below, or
- * NaN, counts as 1 (the log probability that nms_pick_tokens gives for it); at
- * +infinity all tokens but those at -infinity weigh alike; below 4.2e-39 log2(e) / t
+ * A logit of -infinity, or further below the row's largest than float32 holds,
+ * has probability 0.  NaN or +infinity in a row that counts makes its results
+ * and its whole gradient NaN (nms_pick_tokens passes over a NaN; a loss does not
+ * hide it); where all logits are -infinity, the log probability is -infinity and
+ * entropy and gradient are 0.  A temperature of 0 or below, or NaN, counts as 1
+ * (the log probability that nms_pick_tokens gives for it); at +infinity all
+ * tokens but those of probability 0 weigh alike; below 4.2e-39 log2(e) / t
  * counts as float32's largest number in the probabilities.
  * Terms are computed in float32, sums over rows in binary64; a probability
  * below 2^-126 of the row's largest counts as 0.
